@@ -78,6 +78,8 @@ typedef enum { MLA_KV_BF16 = 0, MLA_KV_FP8_E4M3 = 1 } mla_kv_dtype;
 #define MLA_DEVERR_Q_RANGE       0x4u   /* FP8 cache, 33-64 rows: |q| above the float16 range */
 #define MLA_DEVERR_TIMEOUT       0x8u   /* a bounded pipeline wait expired */
 #define MLA_DEVERR_SLOT          0x10u  /* cache write: slot >= num_pages*page_size */
+#define MLA_DEVERR_CU_Q          0x20u  /* chunk attention: cu_q_lens do not ascend within the rows of q */
+#define MLA_DEVERR_POSITION      0x40u  /* rotating cache write: position >= max_pos */
 
 typedef struct mla_decode_params {
   int32_t batch;               /* B >= 1 */
@@ -183,6 +185,93 @@ mla_status mla_decode_noalloc(const mla_decode_params* p, const void* q, const v
  * word that the last no-allocation call left in the library's static scratch array (same
  * results and `bits` as mla_decode_check). Allocates nothing. */
 mla_status mla_decode_noalloc_check(mla_stream_t stream, uint32_t* bits);
+
+/* ---- Chunked prefill: the steps before and around the decode step ----------------------
+ * A serving engine appends the new tokens of whole prompts, of pieces of prompts and of
+ * decoding sequences to the cache in one call, attends them in another, and joins results
+ * over parts of the context (a prefix that many requests share, a long prompt attended in
+ * pieces) by their log-sum-exps. */
+
+/* Cache write of new tokens with the position rotation applied on the way, and the rotated
+ * rope part of their queries. Token t at position p = positions[t] turns each pair (a, b) of
+ * its 64 rope values by its angle: (a c - b s, b c + a s) with c = cos_sin[p][i],
+ * s = cos_sin[p][32 + i] for pair i. Pairs are neighbours (2 i, 2 i + 1) when interleaved,
+ * else (i, i + 32). Its row [latent | rotated rope] goes to slot slot_mapping[t], and the
+ * rotated q_rope[t][h] to columns 512..575 of q[t][h].
+ *   latent        rows of 512 bf16, latent_stride elements apart; rope rows of 64 bf16,
+ *                 rope_stride elements apart (both may be views of one [N, 576] projection);
+ *                 strides a multiple of 8, rows 16-byte aligned
+ *   positions     [N] int64; p < 0 marks a padding token, of which nothing is written
+ *   cos_sin       [max_pos, 64] float32, 16-byte aligned: 32 cosines, then 32 sines
+ *   slot_mapping  [N] int64; s < 0: the token's cache row is not written (its queries are).
+ *                 Slots >= 0 are distinct: of two tokens in one slot either may end up in each
+ *                 16-byte group of the row
+ *   kv_cache, kv_scale   as mla_cache_write. The rotation is computed in float32 and rounded
+ *                 once: to bf16, or as e4m3_rne_satfinite(x / kv_scale)
+ *   q_rope        64 bf16 at token t and head h: q_token_stride t + q_head_stride h elements
+ *                 on (strides a multiple of 8); q [N, num_heads, 576] bf16, whose other columns
+ *                 are left as they are. Both NULL: no queries. q_rope may be q's own last columns
+ *   device_error  optional device uint32, as mla_cache_write: MLA_DEVERR_SLOT (the cache row is
+ *                 skipped) or MLA_DEVERR_POSITION for p >= max_pos (the token is skipped)
+ * One launch on `stream`; no synchronisation. */
+mla_status mla_rope_cache_write(const void* latent, int64_t latent_stride, const void* rope,
+                                int64_t rope_stride, const int64_t* positions, const float* cos_sin,
+                                int32_t max_pos, int32_t interleaved, const int64_t* slot_mapping,
+                                int32_t num_tokens, void* kv_cache, int32_t num_pages,
+                                int32_t page_size, int32_t kv_dtype, const float* kv_scale,
+                                const void* q_rope, int64_t q_token_stride, int64_t q_head_stride,
+                                int32_t num_heads, void* q, uint32_t* device_error,
+                                mla_stream_t stream);
+
+typedef struct mla_chunk_params {
+  int32_t batch;               /* B >= 1 sequences */
+  int32_t num_tokens;          /* T >= 0: rows of q per head; T * num_heads <= 2^30 */
+  int32_t num_heads;           /* H, 1..65536 */
+  int32_t page_size;           /* P: a multiple of 8, at most 1024 (else UNSUPPORTED) */
+  int32_t num_pages;           /* Np: pages in the pool */
+  int32_t max_blocks_per_seq;  /* MB: row stride of block_table */
+  int32_t max_seq_len;         /* host-known upper bound on seq_lens[], <= 2^20 */
+  int32_t kv_dtype;            /* mla_kv_dtype */
+  int32_t causal;              /* 0 or 1 */
+} mla_chunk_params;
+
+/* Workspace bytes mla_chunk_attention needs (num_sms <= 0: the current device's count). 0 on
+ * invalid params. Depends on batch, num_tokens, num_heads and the SM count alone. */
+size_t mla_chunk_workspace_size(const mla_chunk_params* p, int32_t num_sms);
+
+/* Attention of a ragged batch of new tokens over the paged cache, which holds them already.
+ * Sequence b's n_b = cu_q_lens[b+1] - cu_q_lens[b] new tokens are rows cu_q_lens[b].. of q, its
+ * last n_b positions; n_b is 0 (an idle sequence), 1 (a decoding one) or any number. New token i
+ * sees the first L_b - n_b + 1 + i keys when causal, else all L_b (a shared prefix). A row that
+ * sees no key gets out 0 and lse -inf; rows of q that belong to no sequence are left as they
+ * are in out and lse. Keys a row does not see may hold anything, NaN and infinities included.
+ *   q            [T, H, 576] bf16;  out [T, H, 512] bf16;  lse [T, H] float32, natural log
+ *   cu_q_lens    [B + 1] int32, ascending, within [0, T] (else MLA_DEVERR_CU_Q, nothing written)
+ *   seq_lens     [B] int32, tokens in the cache including the new ones, 0..min(max_seq_len,
+ *                MB * P) (else MLA_DEVERR_SEQ_LEN, clamped); may be below n_b
+ *   kv_cache, block_table, softmax_scale, kv_scale as mla_decode (only entries that hold keys of
+ *                sequences with n_b > 0 are read)
+ *   workspace    >= mla_chunk_workspace_size(p, 0) bytes, 256-byte aligned; mla_decode_check reads
+ *                its error word. Calls that may overlap on the GPU, captured graphs among them,
+ *                need workspaces of their own.
+ * Launches a scheduler, the attention kernel and the merge of split blocks on `stream`; returns
+ * without synchronising. Results do not depend on earlier contents of workspace or outputs. */
+mla_status mla_chunk_attention(const mla_chunk_params* p, const void* q, const void* kv_cache,
+                               const int32_t* block_table, const int32_t* seq_lens,
+                               const int32_t* cu_q_lens, float softmax_scale, const float* kv_scale,
+                               void* out, float* lse, void* workspace, size_t workspace_bytes,
+                               mla_stream_t stream);
+
+/* Joins two attention results over disjoint keys (outputs and natural-log log-sum-exps of
+ * mla_decode or mla_chunk_attention): with w = exp(lse - max(lse_a, lse_b)),
+ * out = (w_a out_a + w_b out_b) / (w_a + w_b), lse = max + ln(w_a + w_b). A result with
+ * lse = -inf has weight 0 and its out row is not read; both: out 0, lse -inf.
+ *   out_a, out_b, out  [num_rows, 512] bf16, 16-byte aligned;  lse_*  [num_rows] float32
+ * out may be out_a or out_b and lse may be lse_a or lse_b, otherwise the results overlap no
+ * input. One launch on `stream`; no synchronisation. */
+mla_status mla_merge_states(const void* out_a, const float* lse_a, const void* out_b,
+                            const float* lse_b, int64_t num_rows, void* out, float* lse,
+                            mla_stream_t stream);
 
 /* Decode-kernel timing, for benchmarks and tests. After mla_profile_begin(n), each of the
  * next n mla_decode / mla_decode_noalloc calls in this process records a CUDA event on

@@ -22,7 +22,8 @@ STATUS = {0: "MLA_OK", -1: "MLA_ERR_INVALID_ARG", -2: "MLA_ERR_UNSUPPORTED",
           -6: "MLA_ERR_DEVICE_INDEX"}
 EXPORTS = ("mla_abi_version", "mla_status_string", "mla_decode_workspace_size", "mla_decode",
            "mla_decode_check", "mla_cache_write", "mla_decode_noalloc", "mla_decode_noalloc_check",
-           "mla_profile_begin", "mla_profile_end", "mla_test_set_hooks", "mla_decode_with_cache_write")
+           "mla_profile_begin", "mla_profile_end", "mla_test_set_hooks", "mla_decode_with_cache_write",
+           "mla_rope_cache_write", "mla_chunk_workspace_size", "mla_chunk_attention", "mla_merge_states")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmla.so")
@@ -37,6 +38,13 @@ class MLAError(RuntimeError):
 
 class DecodeParams(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("s_q", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("max_blocks_per_seq", ctypes.c_int32), ("max_seq_len", ctypes.c_int32),
+                ("kv_dtype", ctypes.c_int32), ("causal", ctypes.c_int32)]
+
+
+class ChunkParams(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("num_tokens", ctypes.c_int32), ("num_heads", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
                 ("max_blocks_per_seq", ctypes.c_int32), ("max_seq_len", ctypes.c_int32),
                 ("kv_dtype", ctypes.c_int32), ("causal", ctypes.c_int32)]
@@ -77,6 +85,17 @@ def lib() -> ctypes.CDLL:
         L.mla_profile_begin.argtypes = [i32]
         L.mla_profile_end.restype = i32
         L.mla_profile_end.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i32)]
+        i64 = ctypes.c_int64
+        L.mla_rope_cache_write.restype = i32
+        L.mla_rope_cache_write.argtypes = [vp, i64, vp, i64, vp, vp, i32, i32, vp, i32, vp, i32, i32, i32, vp, vp,
+                                           i64, i64, i32, vp, vp, vp]
+        L.mla_chunk_workspace_size.restype = sz
+        L.mla_chunk_workspace_size.argtypes = [ctypes.POINTER(ChunkParams), i32]
+        L.mla_chunk_attention.restype = i32
+        L.mla_chunk_attention.argtypes = [ctypes.POINTER(ChunkParams), vp, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp,
+                                          vp, sz, vp]
+        L.mla_merge_states.restype = i32
+        L.mla_merge_states.argtypes = [vp, vp, vp, vp, i64, vp, vp, vp]
         _lib = L
     return _lib
 
@@ -271,3 +290,158 @@ def cache_write(latent: torch.Tensor, rope: torch.Tensor, slot_mapping: torch.Te
                                _ptr(device_error), _stream(stream))
     if st != MLA_OK:
         raise MLAError(st, "mla_cache_write")
+
+
+def _on_current_device(*tensors) -> None:
+    """The library launches on the current device and reads these as its pointers."""
+    cuda = [t for t in tensors if t is not None]
+    if any(not t.is_cuda for t in cuda):
+        raise ValueError("every tensor must be on the GPU")
+    if any(t.device.index != torch.cuda.current_device() for t in cuda):
+        raise ValueError("every tensor must be on the current device")
+
+
+def _rows_of(t: torch.Tensor, n: int, width: int, name: str) -> int:
+    """Row stride of a bf16 [n, width] tensor whose rows are contiguous and 16-byte aligned."""
+    if t.dtype != torch.bfloat16 or t.shape != (n, width) or (n > 0 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a bf16 [N, {width}] tensor with contiguous rows")
+    stride = t.stride(0) if n > 1 else width
+    if stride < width or stride % 8 != 0:
+        raise ValueError(f"the rows of {name} must be apart by a multiple of 8 elements, {width} at least")
+    return stride
+
+
+def rope_cache_write(latent: torch.Tensor, rope: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor,
+                     slot_mapping: torch.Tensor, kv_cache: torch.Tensor, kv_scale: torch.Tensor | None = None, *,
+                     q_rope: torch.Tensor | None = None, q: torch.Tensor | None = None, interleaved: bool = True,
+                     device_error: torch.Tensor | None = None, stream=None) -> None:
+    """cache_write() with the position rotation applied on the way: token t's row
+    concat(latent[t], rotated rope[t]) goes to slot_mapping[t], and q_rope [N, H, 64] rotated
+    into q[..., 512:] (q [N, H, 576] contiguous). cos_sin [max_pos, 64] float32 holds the
+    cosines and sines of every position; pairs are neighbours (interleaved) or a half apart.
+    latent, rope and q_rope may be strided views of projections. Negative positions mark
+    padding tokens."""
+    n = latent.shape[0]
+    ls = _rows_of(latent, n, 512, "latent")
+    rs = _rows_of(rope, n, 64, "rope")
+    for name, t in (("positions", positions), ("slot_mapping", slot_mapping)):
+        if t.dtype != torch.int64 or t.shape != (n,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int64 [N] tensor")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.shape[1] != 64 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be a contiguous float32 [max_pos, 64] tensor")
+    if kv_cache.dim() != 3 or kv_cache.shape[2] != D_QK or not kv_cache.is_contiguous():
+        raise ValueError("kv_cache must be a contiguous [Np, P, 576] tensor")
+    Np, P, _ = kv_cache.shape
+    kvd = _kv_dtype_of(kv_cache)
+    if kvd == KV_FP8_E4M3 and (kv_scale is None or kv_scale.dtype != torch.float32):
+        raise ValueError("the FP8 cache needs kv_scale as a float32 device tensor")
+    if (q_rope is None) != (q is None):
+        raise ValueError("q_rope and q are given together or not at all")
+    H, qt, qh = 0, 0, 0
+    if q is not None:
+        if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[0] != n or q.shape[2] != D_QK or not q.is_contiguous():
+            raise ValueError("q must be a contiguous bf16 [N, H, 576] tensor")
+        H = q.shape[1]
+        if q_rope.dtype != torch.bfloat16 or q_rope.shape != (n, H, 64) or (q_rope.numel() > 0 and q_rope.stride(2) != 1):
+            raise ValueError("q_rope must be a bf16 [N, H, 64] tensor with contiguous last dimension")
+        qt = q_rope.stride(0) if n > 1 else 0
+        qh = q_rope.stride(1) if H > 1 else 0
+        if H < 1 or qt % 8 != 0 or qh % 8 != 0:
+            raise ValueError("q_rope's tokens and heads must be apart by a multiple of 8 elements")
+    if device_error is not None and device_error.dtype not in (torch.int32, torch.uint32):
+        raise ValueError("device_error must be a 32-bit integer tensor")
+    _on_current_device(latent, rope, positions, cos_sin, slot_mapping, kv_cache, q_rope, q, device_error,
+                       kv_scale if kvd == KV_FP8_E4M3 else None)
+    st = lib().mla_rope_cache_write(_ptr(latent), ls, _ptr(rope), rs, _ptr(positions), _ptr(cos_sin), cos_sin.shape[0],
+                                    int(bool(interleaved)), _ptr(slot_mapping), n, _ptr(kv_cache), Np, P, kvd,
+                                    _ptr(kv_scale) if kvd == KV_FP8_E4M3 else None,
+                                    _ptr(q_rope) if n > 0 else None, qt, qh, H, _ptr(q) if n > 0 else None,
+                                    _ptr(device_error), _stream(stream))
+    if st != MLA_OK:
+        raise MLAError(st, "mla_rope_cache_write")
+
+
+def make_chunk_params(batch, num_tokens, num_heads, page_size, num_pages, max_blocks_per_seq, max_seq_len,
+                      kv_dtype, causal=True) -> ChunkParams:
+    return ChunkParams(int(batch), int(num_tokens), int(num_heads), int(page_size), int(num_pages),
+                       int(max_blocks_per_seq), int(max_seq_len), int(kv_dtype), int(bool(causal)))
+
+
+def chunk_workspace_size(params: ChunkParams, num_sms: int = 0) -> int:
+    n = lib().mla_chunk_workspace_size(ctypes.byref(params), int(num_sms))
+    if n == 0:
+        raise MLAError(-1, "mla_chunk_workspace_size")
+    return int(n)
+
+
+def alloc_chunk_workspace(params: ChunkParams, device=None) -> torch.Tensor:
+    return torch.empty(chunk_workspace_size(params), dtype=torch.uint8, device=device or "cuda")
+
+
+def chunk_attention(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                    cu_q_lens: torch.Tensor, softmax_scale: float, kv_scale: torch.Tensor | None = None, *,
+                    max_seq_len: int, causal: bool = True, out: torch.Tensor | None = None,
+                    lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Attention of a ragged batch of new tokens over the paged cache. q [T, H, 576] bf16, rows
+    cu_q_lens[b] .. cu_q_lens[b+1] being the last positions of sequence b; cu_q_lens [B + 1] and
+    seq_lens [B] int32; the rest as decode(). Rows that belong to no sequence are left as they
+    are in out and lse (uninitialised when these are allocated here). Returns (out, lse)."""
+    if q.dim() != 3 or q.shape[2] != D_QK or q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 [T, H, 576] tensor")
+    T, H, _ = q.shape
+    if kv_cache.dim() != 3 or kv_cache.shape[2] != D_QK or not kv_cache.is_contiguous():
+        raise ValueError("kv_cache must be a contiguous [Np, P, 576] tensor")
+    Np, P, _ = kv_cache.shape
+    for name, t in (("block_table", block_table), ("seq_lens", seq_lens), ("cu_q_lens", cu_q_lens)):
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor")
+    B = seq_lens.numel()
+    if seq_lens.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != B or cu_q_lens.shape != (B + 1,):
+        raise ValueError("block_table must be [B, MB], seq_lens [B] and cu_q_lens [B + 1]")
+    kvd = _kv_dtype_of(kv_cache)
+    if kvd == KV_FP8_E4M3 and (kv_scale is None or kv_scale.dtype != torch.float32):
+        raise ValueError("the FP8 cache needs kv_scale as a float32 device tensor")
+    if out is None:
+        out = torch.empty((T, H, D_V), dtype=torch.bfloat16, device=q.device)
+    elif out.dtype != torch.bfloat16 or out.shape != (T, H, D_V) or not out.is_contiguous():
+        raise ValueError("out must be a contiguous bf16 [T, H, 512] tensor")
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    elif lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 [T, H] tensor")
+    _on_current_device(q, kv_cache, block_table, seq_lens, cu_q_lens, out, lse, workspace,
+                       kv_scale if kvd == KV_FP8_E4M3 else None)
+    params = make_chunk_params(B, T, H, P, Np, block_table.shape[1], max_seq_len, kvd, causal)
+    if workspace is None:
+        workspace = alloc_chunk_workspace(params, q.device)
+    st = lib().mla_chunk_attention(ctypes.byref(params), _ptr(q), _ptr(kv_cache), _ptr(block_table), _ptr(seq_lens),
+                                   _ptr(cu_q_lens), ctypes.c_float(softmax_scale),
+                                   _ptr(kv_scale) if kvd == KV_FP8_E4M3 else None, _ptr(out), _ptr(lse),
+                                   _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    if st != MLA_OK:
+        raise MLAError(st, "mla_chunk_attention")
+    return out, lse
+
+
+def merge_states(out_a: torch.Tensor, lse_a: torch.Tensor, out_b: torch.Tensor, lse_b: torch.Tensor, *,
+                 out: torch.Tensor | None = None, lse: torch.Tensor | None = None, stream=None):
+    """Join two attention results over disjoint keys: out_* [..., 512] bf16 and lse_* [...]
+    float32 as decode() and chunk_attention() return them. out and lse may be given, in place
+    of one of the inputs among others. Returns (out, lse)."""
+    shape = tuple(lse_a.shape)
+    if out is None:
+        out = torch.empty_like(out_a)
+    if lse is None:
+        lse = torch.empty_like(lse_a)
+    for name, t in (("out_a", out_a), ("out_b", out_b), ("out", out)):
+        if t.dtype != torch.bfloat16 or tuple(t.shape) != shape + (D_V,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous bf16 [..., 512] tensor of the shape of lse_a")
+    for name, t in (("lse_a", lse_a), ("lse_b", lse_b), ("lse", lse)):
+        if t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous float32 tensor of one shape")
+    _on_current_device(out_a, lse_a, out_b, lse_b, out, lse)
+    st = lib().mla_merge_states(_ptr(out_a), _ptr(lse_a), _ptr(out_b), _ptr(lse_b), lse_a.numel(), _ptr(out), _ptr(lse),
+                                _stream(stream))
+    if st != MLA_OK:
+        raise MLAError(st, "mla_merge_states")
+    return out, lse

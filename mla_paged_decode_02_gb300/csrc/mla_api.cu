@@ -6,8 +6,10 @@
 #include <mutex>
 #include <vector>
 #include <cudaTypedefs.h>
+#include "mla_chunk.h"
 #include "mla_internal.h"
 #include "mla_ptx.cuh"
+#include "mla_rope.h"
 #include "../../include/mla.h"
 
 #define MLA_EXPORT extern "C" __attribute__((visibility("default")))
@@ -434,6 +436,242 @@ MLA_EXPORT mla_status mla_cache_write(const void* latent, const void* rope,
   const int64_t total = (int64_t)num_pages * page_size;
   if (launch_cache_write(latent, rope, slot_mapping, num_tokens, kv_cache, total, fp8, kv_scale,
                          device_error, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  return MLA_OK;
+}
+
+// ---------------------------------------------------------------- ragged chunk attention
+namespace mla {
+namespace {
+
+std::atomic<uint32_t> g_chunk_prepared[kMaxDevices];   // bit per cache type
+
+mla_status check_chunk_params(const mla_chunk_params* p) {
+  if (p == nullptr) return MLA_ERR_INVALID_ARG;
+  if (p->batch < 1 || p->num_tokens < 0 || p->num_heads < 1 || p->page_size < 1 || p->num_pages < 1 ||
+      p->max_blocks_per_seq < 1 || p->max_seq_len < 1)
+    return MLA_ERR_INVALID_ARG;
+  if (p->kv_dtype != MLA_KV_BF16 && p->kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_INVALID_ARG;
+  if (p->causal != 0 && p->causal != 1) return MLA_ERR_INVALID_ARG;
+  if (p->page_size % 8 != 0 || p->page_size > 1024) return MLA_ERR_UNSUPPORTED;
+  if (p->batch > kMaxBatch || p->max_seq_len > kMaxSeqLen || p->num_heads > kMaxRows) return MLA_ERR_UNSUPPORTED;
+  if ((int64_t)p->num_tokens * p->num_heads > kMaxChunkRows) return MLA_ERR_UNSUPPORTED;
+  if ((int64_t)p->num_pages * p->page_size >= (int64_t)1 << 31) return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+
+// rows of one box: the largest power of two that divides the page, at most `most`
+int box_rows_of(int page_size, int most) { return std::min(most, page_size & -page_size); }
+
+bool encode_map(CUtensorMap* m, CUtensorMapDataType type, int rank, const void* base, const cuuint64_t* dims,
+                const cuuint64_t* strides, const cuuint32_t* box) {
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  return g_encode(m, type, rank, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// rows of 576 bf16 as [9 chunks][rows][64]
+bool encode_rows_map(CUtensorMap* m, const void* base, int64_t rows, uint32_t box_rows, uint32_t chunks) {
+  const cuuint64_t dims[3] = {64, (cuuint64_t)rows, 9};
+  const cuuint64_t strides[2] = {kDQK * 2, 128};
+  const cuuint32_t box[3] = {64, box_rows, chunks};
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box);
+}
+// rows of 576 bytes; columns past the row read as zeros
+bool encode_bytes_map(CUtensorMap* m, const void* base, int64_t rows, uint32_t box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)kDQK, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)kDQK};
+  const cuuint32_t box[2] = {128, box_rows};
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box);
+}
+
+}  // namespace
+}  // namespace mla
+
+MLA_EXPORT size_t mla_chunk_workspace_size(const mla_chunk_params* p, int32_t num_sms) {
+  if (check_chunk_params(p) != MLA_OK) return 0;
+  if (num_sms <= 0) {
+    int dev;
+    if (current_device(&dev) != cudaSuccess) return 0;
+    num_sms = sm_count(dev);
+    if (num_sms <= 0) return 0;
+  }
+  if (num_sms < 2) return 0;
+  return chunk_ws_layout(p->batch, p->num_tokens, p->num_heads, num_sms / 2).total;
+}
+
+MLA_EXPORT mla_status mla_chunk_attention(const mla_chunk_params* p, const void* q, const void* kv_cache,
+                                          const int32_t* block_table, const int32_t* seq_lens,
+                                          const int32_t* cu_q_lens, float softmax_scale, const float* kv_scale,
+                                          void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                          mla_stream_t stream) {
+  const mla_status st = check_chunk_params(p);
+  if (st != MLA_OK) return st;
+  const bool fp8 = p->kv_dtype == MLA_KV_FP8_E4M3;
+  const bool any = p->num_tokens > 0;
+  if (!kv_cache || !block_table || !seq_lens || !cu_q_lens || !workspace || (any && (!q || !out || !lse)))
+    return MLA_ERR_INVALID_ARG;
+  if (fp8 && !kv_scale) return MLA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(block_table, 4) ||
+      !aligned(seq_lens, 4) || !aligned(cu_q_lens, 4) || !aligned(workspace, 256) || !aligned(kv_scale, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (!(softmax_scale == softmax_scale) || softmax_scale > 3.0e38f || softmax_scale < -3.0e38f)
+    return MLA_ERR_INVALID_ARG;
+  int dev;
+  if (current_device(&dev) != cudaSuccess) return MLA_ERR_CUDA;
+  const int nsm = sm_count(dev);
+  if (nsm <= 0) return MLA_ERR_CUDA;
+  const int pairs = nsm / 2;
+  if (pairs < 1) return MLA_ERR_UNSUPPORTED;
+  const ChunkWs w = chunk_ws_layout(p->batch, p->num_tokens, p->num_heads, pairs);
+  if (workspace_bytes < w.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  if (!get_encoder()) return MLA_ERR_CUDA;
+  const uint32_t bit = fp8 ? 2u : 1u;
+  if (!(g_chunk_prepared[dev].load() & bit)) {
+    if (chunk_prepare(fp8) != cudaSuccess) return MLA_ERR_CUDA;
+    g_chunk_prepared[dev].fetch_or(bit);
+  }
+
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t cap = (int64_t)p->max_blocks_per_seq * p->page_size;
+  ChunkSchedArgs sa{};
+  sa.seq_lens = seq_lens;
+  sa.cu_q = cu_q_lens;
+  sa.hdr = reinterpret_cast<uint32_t*>(ws);
+  sa.gbase = reinterpret_cast<int32_t*>(ws + w.gbase_off);
+  sa.cta_first = reinterpret_cast<int32_t*>(ws + w.cta_off);
+  sa.split_list = reinterpret_cast<int4*>(ws + w.split_off);
+  sa.units = reinterpret_cast<ChunkUnit*>(ws + w.units_off);
+  sa.B = p->batch;
+  sa.H = p->num_heads;
+  sa.causal = p->causal;
+  sa.max_len = (int)std::min<int64_t>(cap, p->max_seq_len);
+  sa.workers = pairs;
+  sa.setup = 1;
+  sa.tokens = p->num_tokens;
+  sa.max_units = w.max_units;
+  ChunkArgs ca;
+  std::memset(&ca, 0, sizeof(ca));
+  const int64_t rows = (int64_t)p->num_pages * p->page_size;
+  ca.k_box = box_rows_of(p->page_size, 64);
+  ca.v_box = box_rows_of(p->page_size, fp8 ? 64 : 32);
+  if (any) {
+    if (!encode_rows_map(&ca.tm_q, q, (int64_t)p->num_tokens * p->num_heads, 64, 9)) return MLA_ERR_INVALID_ARG;
+    const bool ok =
+        fp8 ? encode_bytes_map(&ca.tm_k, kv_cache, rows, ca.k_box) && encode_bytes_map(&ca.tm_v, kv_cache, rows, ca.v_box)
+            : encode_rows_map(&ca.tm_k, kv_cache, rows, ca.k_box, 1) &&
+                  encode_rows_map(&ca.tm_v, kv_cache, rows, ca.v_box, ca.k_box < 64 ? 1 : 4);
+    if (!ok) return MLA_ERR_INVALID_ARG;
+  }
+  if (launch_chunk_schedule(sa, s) != cudaSuccess) return MLA_ERR_CUDA;
+  if (!any) return MLA_OK;
+
+  ca.block_table = block_table;
+  ca.units = sa.units;
+  ca.cta_first = sa.cta_first;
+  ca.err = sa.hdr;
+  ca.out = static_cast<__nv_bfloat16*>(out);
+  ca.lse = lse;
+  ca.part_o = reinterpret_cast<float*>(ws + w.po_off);
+  ca.part_lse = reinterpret_cast<float*>(ws + w.plse_off);
+  ca.kv_scale = kv_scale;
+  ca.H = p->num_heads;
+  ca.P = p->page_size;
+  ca.MB = p->max_blocks_per_seq;
+  ca.num_pages = p->num_pages;
+  ca.causal = p->causal;
+  ca.total_rows = (int32_t)rows;
+  ca.softmax_scale = softmax_scale;
+  ca.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  ca.test_stall = g_test_stall.load(std::memory_order_relaxed);
+  if (launch_chunk(ca, fp8, pairs, s) != cudaSuccess) return MLA_ERR_CUDA;
+
+  ChunkCombineArgs cc{};
+  cc.hdr = sa.hdr;
+  cc.err = sa.hdr;
+  cc.block_table = block_table;
+  cc.seq_lens = seq_lens;
+  cc.cu_q = cu_q_lens;
+  cc.B = p->batch;
+  cc.MB = p->max_blocks_per_seq;
+  cc.P = p->page_size;
+  cc.num_pages = p->num_pages;
+  cc.max_len = sa.max_len;
+  cc.tokens = p->num_tokens;
+  cc.split_list = sa.split_list;
+  cc.part_o = ca.part_o;
+  cc.part_lse = ca.part_lse;
+  cc.out = ca.out;
+  cc.lse = ca.lse;
+  if (launch_chunk_combine(cc, 8 * nsm, s) != cudaSuccess) return MLA_ERR_CUDA;
+  return MLA_OK;
+}
+
+// ------------------------------------------------------------ rotating append, state merge
+MLA_EXPORT mla_status mla_rope_cache_write(const void* latent, int64_t latent_stride, const void* rope,
+                                           int64_t rope_stride, const int64_t* positions, const float* cos_sin,
+                                           int32_t max_pos, int32_t interleaved, const int64_t* slot_mapping,
+                                           int32_t num_tokens, void* kv_cache, int32_t num_pages, int32_t page_size,
+                                           int32_t kv_dtype, const float* kv_scale, const void* q_rope,
+                                           int64_t q_token_stride, int64_t q_head_stride, int32_t num_heads, void* q,
+                                           uint32_t* device_error, mla_stream_t stream) {
+  if (num_tokens < 0 || num_pages < 1 || page_size < 1 || max_pos < 1) return MLA_ERR_INVALID_ARG;
+  if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_INVALID_ARG;
+  if (interleaved != 0 && interleaved != 1) return MLA_ERR_INVALID_ARG;
+  const bool fp8 = kv_dtype == MLA_KV_FP8_E4M3;
+  if ((q_rope == nullptr) != (q == nullptr)) return MLA_ERR_INVALID_ARG;
+  if (q != nullptr && num_heads < 1) return MLA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return MLA_OK;
+  if (!latent || !rope || !positions || !cos_sin || !slot_mapping || !kv_cache || (fp8 && !kv_scale))
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned(latent, 16) || !aligned(rope, 16) || !aligned(kv_cache, 16) || !aligned(cos_sin, 16) ||
+      !aligned(positions, 8) || !aligned(slot_mapping, 8) || !aligned(q, 16) || !aligned(q_rope, 16) ||
+      !aligned(kv_scale, 4) || !aligned(device_error, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (latent_stride < kDV || rope_stride < kDRope || latent_stride % 8 != 0 || rope_stride % 8 != 0)
+    return MLA_ERR_INVALID_ARG;
+  if (q != nullptr && (q_token_stride % 8 != 0 || q_head_stride % 8 != 0 || q_token_stride < 0 || q_head_stride < 0))
+    return MLA_ERR_INVALID_ARG;
+  if (q != nullptr && num_heads > kMaxRows) return MLA_ERR_UNSUPPORTED;
+  // one warp per task, eight to a block: within the grid's limit
+  if ((int64_t)num_tokens * (1 + (q != nullptr ? (num_heads + 31) / 32 : 0)) > (int64_t)1 << 33) return MLA_ERR_UNSUPPORTED;
+  RopeWriteArgs a{};
+  a.latent = static_cast<const __nv_bfloat16*>(latent);
+  a.rope = static_cast<const __nv_bfloat16*>(rope);
+  a.positions = positions;
+  a.slots = slot_mapping;
+  a.cos_sin = cos_sin;
+  a.q_rope = static_cast<const __nv_bfloat16*>(q_rope);
+  a.q = static_cast<__nv_bfloat16*>(q);
+  a.cache = static_cast<uint8_t*>(kv_cache);
+  a.kv_scale = kv_scale;
+  a.err = device_error;
+  a.latent_stride = latent_stride;
+  a.rope_stride = rope_stride;
+  a.q_token_stride = q_token_stride;
+  a.q_head_stride = q_head_stride;
+  a.total_slots = (int64_t)num_pages * page_size;
+  a.n = num_tokens;
+  a.H = num_heads;
+  a.max_pos = max_pos;
+  a.interleaved = interleaved;
+  if (launch_rope_write(a, fp8, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_CUDA;
+  return MLA_OK;
+}
+
+MLA_EXPORT mla_status mla_merge_states(const void* out_a, const float* lse_a, const void* out_b, const float* lse_b,
+                                       int64_t num_rows, void* out, float* lse, mla_stream_t stream) {
+  if (num_rows < 0) return MLA_ERR_INVALID_ARG;
+  if (num_rows == 0) return MLA_OK;
+  if (!out_a || !lse_a || !out_b || !lse_b || !out || !lse) return MLA_ERR_INVALID_ARG;
+  if (!aligned(out_a, 16) || !aligned(out_b, 16) || !aligned(out, 16) || !aligned(lse_a, 4) || !aligned(lse_b, 4) ||
+      !aligned(lse, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (num_rows > (int64_t)1 << 33) return MLA_ERR_UNSUPPORTED;
+  if (launch_merge_states(out_a, lse_a, out_b, lse_b, num_rows, out, lse, reinterpret_cast<cudaStream_t>(stream)) !=
+      cudaSuccess)
     return MLA_ERR_CUDA;
   return MLA_OK;
 }

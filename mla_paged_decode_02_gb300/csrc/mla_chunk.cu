@@ -1,0 +1,781 @@
+// mla_chunk.cu — attention of a ragged batch of new tokens over the paged latent cache, on CTA
+// pairs (sm_103a: a cluster of two CTAs on two SMs, tcgen05 MMAs with cta_group::2).
+//
+// For a block of 128 query rows of one sequence (row = token * H + head; the token sees the
+// first n_r keys) the kernel computes  s = scale q.K,  p = exp(s - m),  O = sum p V,  l = sum p
+// in one pass over the keys, with a running reference m (moved only when a score exceeds it by
+// more than 2^8; O is rescaled then), and leaves out = O / l, lse = m + ln l.
+//
+// Rows on M. The float32 accumulator of 128 rows x 512 columns fills one SM's tensor memory, so
+// a pair shares it: CTA k holds rows 64 k .. 64 k + 63 (M = 128 over the pair), and every MMA
+// has N = 256, half of its B operand from each CTA. Both are full rate on this GPU: 37 ns per
+// K = 16 step, like M = 256 with N = 128 (N = 128 here would cost 26 ns, more than half).
+//   QK^T  N = 256 keys of a tile: CTA k holds keys 128 k .. as B;
+//   PV    N = 256 value columns, twice (j = 0, 1): CTA k holds columns 256 k + 128 j .. as B.
+// An SM's accumulator rows then hold, in tensor-memory lane l, row l % 64: N columns 0..127 in
+// lanes 0..63 and 128..255 in lanes 64..127. So a thread owns one row and half of its keys, the
+// softmax stays inside the CTA (two threads compare maxima), and P needs no exchange.
+// Tensor memory per CTA: S 2 x 128 columns, O 2 x 128.
+//
+// Shared memory per CTA: 64 query rows (72 KB), P (64 rows x 256 keys, 32 KB), and a ring of
+// seven 16 KB slots, filled in the order the MMAs consume them: the keys of tile n (slots of 128
+// keys x 128 bytes of the row), then the values of tile n - 1 (this CTA's 256 columns of 32 or,
+// E4M3, 64 keys). The 512-byte value pieces come from L2: the peer has just read those keys.
+//
+// The FP8 cache. As in the decode kernels, the MMAs read the E4M3 bytes as they land
+// (kind::f8f6f4) against q and P written as two E4M3 terms each (hi + lo): q scaled per row by a
+// power of two, P times 2^4, exact or about 8 significant bits.
+//
+// Masks. Scores of keys a row does not see are selected away by index, whatever they hold. In
+// the PV product such keys meet P = 0, and 0 x NaN is NaN: value slots with a key that some row
+// of the block does not see pass through two warps that write zeros over rows no row sees and
+// over non-finite values of rows that only some see (a row that does see such a key has a
+// non-finite score there, which makes its result NaN without the value; a score of -inf gives
+// the key weight 0). Boxes past the last key start at the end of the pool, so TMA fills zeros.
+//
+// Roles (384 threads): warp 0 producer, warp 1 of the even CTA MMA issuer, warps 2-3 value fixes
+// and (E4M3) the split of q, warps 4-7 softmax, warps 8-11 epilogue. Every wait is bounded; a
+// stall sets the device error word, and both CTAs drain and leave through a cluster barrier.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include "mla_chunk.h"
+#include "mla_ptx.cuh"
+#include "../../include/mla.h"
+
+namespace mla {
+namespace {
+
+constexpr int kCRing = 7;
+constexpr int kCSlot = 16384;
+constexpr int kCQChunk = 8192;                   // 64 rows x 64 columns bf16
+constexpr int kCQBytes = 9 * kCQChunk;
+constexpr int kCPBytes = 64 * kChunkTile * 2;    // bf16, or E4M3 hi and lo
+constexpr int kCThreads = 384;
+constexpr int kCTmemCols = 512;
+constexpr int kCOCol = 256;                      // O at columns 256 + 128 j
+constexpr int kCDynBytes = 1024 + kCQBytes + kCPBytes + kCRing * kCSlot;
+constexpr int kCSmemLimit = 232448;
+constexpr int kCStaticBudget = 6144;
+static_assert(kCDynBytes + kCStaticBudget <= kCSmemLimit, "shared memory budget");
+constexpr float kCLog2e = 1.4426950408889634f;
+constexpr float kCLn2 = 0.6931471805599453f;
+
+template <bool FP8>
+struct ChunkCfg {
+  static constexpr int kKeySlots = FP8 ? 5 : 9;          // 128 bytes of the key row each
+  static constexpr int kSlotKeys = FP8 ? 64 : 32;        // keys of a value slot
+  static constexpr int kValueChunks = FP8 ? 2 : 4;       // 128-byte pieces of its rows
+  static constexpr float kRescaleLog2 = FP8 ? 4.f : 8.f;
+  static constexpr float kPOffLog2 = FP8 ? 4.f : 0.f;
+  static_assert(kSlotKeys * kValueChunks * 128 == kCSlot, "value slot");
+};
+
+struct CUnit {
+  int b, row0, srow0, tb, te, slot, len, vis, nrows;
+  int lo, hi;    // keys every row sees; keys some row sees
+};
+
+__device__ __forceinline__ CUnit load_cunit(const ChunkArgs& a, int u) {
+  const int4* p = reinterpret_cast<const int4*>(a.units + u);
+  const int4 x = p[0], y = p[1];
+  CUnit r;
+  r.b = x.x;
+  r.row0 = x.y;
+  r.srow0 = x.z;
+  r.tb = x.w & 0xFFFF;
+  r.te = (int)((unsigned)x.w >> 16);
+  r.slot = y.x;
+  r.len = y.y;
+  r.vis = y.z;
+  r.nrows = y.w;
+  if (a.causal) {
+    r.lo = max(0, r.vis + r.srow0 / a.H);
+    r.hi = max(0, r.vis + (r.srow0 + r.nrows - 1) / a.H);
+  } else {
+    r.lo = r.hi = r.len;
+  }
+  return r;
+}
+
+// value slots of tile `tile` of a block that sees hi keys
+template <int kSlotKeys>
+__device__ __forceinline__ int value_slots(int hi, int tile) {
+  const int left = hi - tile * kChunkTile;
+  return left >= kChunkTile ? kChunkTile / kSlotKeys : (left + kSlotKeys - 1) / kSlotKeys;
+}
+
+// First cache row of the 8 keys 8 lane .. of a tile (page_rows below turns it into boxes): the
+// pool's end (a box there is filled with zeros) past the keys the block sees; a block-table
+// entry outside the pool reads page 0 (the combine kernel reports it).
+__device__ __forceinline__ int tile_row(const ChunkArgs& a, const CUnit& U, int tile, int lane) {
+  const int tok = tile * kChunkTile + 8 * lane;
+  if (tok >= U.hi) return a.total_rows;
+  const int page = tok / a.P, in = tok - page * a.P;
+  const int pg = __ldg(a.block_table + (int64_t)U.b * a.MB + page);
+  return (pg < 0 || pg >= a.num_pages) ? in : pg * a.P + in;
+}
+
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* m, uint32_t bar_cluster, int32_t c0,
+                                                 int32_t c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];"
+      :: "r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(c0), "r"(c1) : "memory");
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// zero over the non-finite values of 16 bytes
+template <bool FP8>
+__device__ __forceinline__ uint32_t finite_word(uint32_t w) {
+  if (FP8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (((w >> (8 * i)) & 0x7Fu) == 0x7Fu) w &= ~(0xFFu << (8 * i));
+  } else {
+    if ((w & 0x7F80u) == 0x7F80u) w &= 0xFFFF0000u;
+    if ((w & 0x7F800000u) == 0x7F800000u) w &= 0x0000FFFFu;
+  }
+  return w;
+}
+
+// 32 lanes x 32 consecutive 32-bit columns
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  tmem_ld16(taddr, v);
+  tmem_ld16(taddr + 16, v + 16);
+}
+
+}  // namespace
+
+template <bool FP8, bool kSub>
+__global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
+  using Cfg = ChunkCfg<FP8>;
+  constexpr int KS = Cfg::kKeySlots, VK = Cfg::kSlotKeys, VC = Cfg::kValueChunks;
+  extern __shared__ uint8_t dsmem_raw[];
+  __shared__ __align__(8) uint64_t bar_full[kCRing], bar_empty[kCRing], bar_aux[kCRing];
+  __shared__ __align__(8) uint64_t bar_qfull, bar_qempty, bar_qraw, bar_qsc, bar_qfree;
+  __shared__ __align__(8) uint64_t bar_sfull[2], bar_p, bar_pv, bar_oempty, bar_stat, bar_statfree, bar_drain, bar_never;
+  __shared__ __align__(16) uint32_t sig_s[4];
+  __shared__ uint32_t tmem_base_s, abort_s;
+  __shared__ float qf_s[64];                 // E4M3: 2^-e of this CTA's rows
+  __shared__ float mx_s[128], sum_s[128], ref_s[128];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const uint32_t peer = rank ^ 1u;
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1;
+
+  const uint32_t raw = smem_u32(dsmem_raw);
+  const uint32_t sQ = (raw + 1023u) & ~1023u;
+  uint8_t* gQ = dsmem_raw + (sQ - raw);
+  const uint32_t sP = sQ + kCQBytes, sR = sP + kCPBytes;
+  uint8_t* gP = gQ + kCQBytes;
+  uint8_t* gR = gP + kCPBytes;
+
+  const uint32_t b_full = smem_u32(bar_full), b_empty = smem_u32(bar_empty), b_aux = smem_u32(bar_aux);
+  const uint32_t b_qfull = smem_u32(&bar_qfull), b_qempty = smem_u32(&bar_qempty), b_qraw = smem_u32(&bar_qraw);
+  const uint32_t b_qsc = smem_u32(&bar_qsc), b_qfree = smem_u32(&bar_qfree);
+  const uint32_t b_sfull = smem_u32(bar_sfull), b_p = smem_u32(&bar_p), b_pv = smem_u32(&bar_pv);
+  const uint32_t b_oempty = smem_u32(&bar_oempty), b_stat = smem_u32(&bar_stat), b_statfree = smem_u32(&bar_statfree);
+  const uint32_t b_drain = smem_u32(&bar_drain), b_never = smem_u32(&bar_never);
+  volatile uint32_t* abort_flag = &abort_s;
+  uint32_t* err = a.err;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kCRing; ++i) {
+      mbar_init(b_full + 8 * i, 1);       // the even CTA's producer, with both CTAs' bytes
+      mbar_init(b_empty + 8 * i, 1);      // the issuer's commit (both CTAs)
+      mbar_init(b_aux + 8 * i, 1);        // a slot that is fixed before it counts as full
+    }
+    mbar_init(b_qfull, 1);                // bf16: as b_full; E4M3: the converters of both CTAs
+    mbar_init(b_qempty, 1);
+    mbar_init(b_qraw, 1);
+    mbar_init(b_qsc, 1);
+    mbar_init(b_qfree, 1);
+    mbar_init(b_sfull, 1);
+    mbar_init(b_sfull + 8, 1);
+    mbar_init(b_p, 2);                    // both CTAs' softmax
+    mbar_init(b_pv, 1);
+    mbar_init(b_oempty, 2);               // both CTAs' epilogue
+    mbar_init(b_stat, 128);
+    mbar_init(b_statfree, 128);
+    mbar_init(b_drain, 1);
+    mbar_init(b_never, 1);
+    abort_s = 0u;
+    fence_mbarrier_init();
+    tma_prefetch_desc(&a.tm_q);
+    tma_prefetch_desc(&a.tm_k);
+    tma_prefetch_desc(&a.tm_v);
+  }
+  if (warp == 0) tmem_alloc_pair(smem_u32(&tmem_base_s), kCTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                         // both CTAs' barriers exist before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_s;
+  griddep_wait();
+
+  const int u0 = a.cta_first[pair], u1 = a.cta_first[pair + 1];
+  auto lead = [&](uint32_t addr) { return map_to_rank(addr, 0); };
+  // a failed wait also raises the peer's abort flag, so that its waits end too
+  auto fail_peer = [&]() { st_cluster_u32(map_to_rank(smem_u32(&abort_s), peer), 1u); };
+  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+    const bool ok = mbar_wait(bar, parity, abort_flag, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns);
+    if (!ok) fail_peer();
+    return ok;
+  };
+
+  if (warp == 0) {
+    // ================================================================== producer
+    // lane i issues box i of a slot; every slot takes the same bytes from both CTAs
+    const int kbox = kSub ? a.k_box : 64, vbox = kSub ? a.v_box : VK;
+    const int nk = 128 / kbox;                          // boxes of a key slot
+    const int nvr = VK / vbox;                          // boxes down a value slot
+    const bool wide = !FP8 && !kSub;                    // one box of all four value chunks
+    const int nv = wide ? 1 : nvr * VC;
+    uint32_t r = 0, uq = 0;
+    bool ok = true;
+    auto slot_free = [&](uint32_t slot) -> bool {
+      int w = 1;
+      if (lane == 0) w = wait(b_empty + 8 * slot, ((r / kCRing) & 1) ^ 1) ? 1 : 0;
+      return __shfl_sync(0xffffffffu, w, 0) != 0;
+    };
+    auto load_keys = [&](int rows) -> bool {
+      const int row = __shfl_sync(0xffffffffu, rows, 16 * (int)rank + (lane < nk ? lane * (kbox >> 3) : 0));
+      for (int c = 0; c < KS; ++c, ++r) {
+        const uint32_t slot = r % kCRing;
+        if (!slot_free(slot)) return false;
+        const uint32_t lb = lead(b_full + 8 * slot);
+        if (leader && lane == 0) mbar_arrive_expect_tx(b_full + 8 * slot, 2 * kCSlot);
+        if (lane < nk) {
+          const uint32_t dst = sR + slot * kCSlot + (uint32_t)(lane * kbox) * 128u;
+          if (FP8) tma_load_2d_pair(dst, &a.tm_k, lb, 128 * c, row);
+          else tma_load_3d_pair(dst, &a.tm_k, lb, 0, row, c);
+        }
+      }
+      return true;
+    };
+    auto load_values = [&](const CUnit& U, int tile, int rows) -> bool {
+      const int n = value_slots<VK>(U.hi, tile);
+      for (int s = 0; s < n; ++s, ++r) {
+        const uint32_t slot = r % kCRing;
+        if (!slot_free(slot)) return false;
+        const int i = wide ? 0 : lane % nvr, c = wide ? 0 : lane / nvr;   // box i of chunk c
+        const int row = __shfl_sync(0xffffffffu, rows, (s * VK + (lane < nv ? i * vbox : 0)) >> 3);
+        const bool fix = tile * kChunkTile + (s + 1) * VK > U.lo;
+        if (lane == 0) {
+          if (leader) mbar_arrive_expect_tx(b_full + 8 * slot, 2 * kCSlot);
+          if (fix) mbar_arrive_expect_tx(b_aux + 8 * slot, kCSlot);
+        }
+        __syncwarp();
+        if (lane < nv) {
+          const uint32_t dst = sR + slot * kCSlot + (uint32_t)(c * VK + i * vbox) * 128u;
+          const int col = VC * (int)rank + c;                            // 128-byte piece of the row
+          if (fix) {
+            if (FP8) tma_load_2d(dst, &a.tm_v, b_aux + 8 * slot, 128 * col, row);
+            else tma_load_3d(dst, &a.tm_v, b_aux + 8 * slot, 0, row, col);
+          } else {
+            const uint32_t lb = lead(b_full + 8 * slot);
+            if (FP8) tma_load_2d_pair(dst, &a.tm_v, lb, 128 * col, row);
+            else tma_load_3d_pair(dst, &a.tm_v, lb, 0, row, col);
+          }
+        }
+      }
+      return true;
+    };
+    for (int u = u0; u < u1 && ok; ++u) {
+      const CUnit U = load_cunit(a, u);
+      if (U.te == U.tb) continue;
+      int rows = tile_row(a, U, U.tb, lane), prev_rows = 0;
+      int w = 1;
+      if (lane == 0) {
+        w = wait(b_qempty, (uq & 1) ^ 1) ? 1 : 0;
+        if (w) {
+          const int32_t q0 = U.row0 + 64 * (int)rank;
+          if (FP8) {
+            mbar_arrive_expect_tx(b_qraw, kCQBytes);
+            tma_load_3d(sQ, &a.tm_q, b_qraw, 0, q0, 0);
+          } else {
+            if (leader) mbar_arrive_expect_tx(b_qfull, 2 * kCQBytes);
+            tma_load_3d_pair(sQ, &a.tm_q, lead(b_qfull), 0, q0, 0);
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, w, 0) != 0;
+      ++uq;
+      for (int tile = U.tb; tile < U.te && ok; ++tile) {
+        // the next tile's page numbers are on their way while this tile's keys are issued
+        const int next_rows = tile + 1 < U.te ? tile_row(a, U, tile + 1, lane) : 0;
+        ok = load_keys(rows);
+        if (ok && tile > U.tb) ok = load_values(U, tile - 1, prev_rows);
+        prev_rows = rows;
+        rows = next_rows;
+      }
+      if (ok) ok = load_values(U, U.te - 1, prev_rows);
+    }
+    // after an abort the odd CTA cannot observe its own loads (they count on the even CTA's
+    // barriers): both producers wait 50 us, far longer than a load takes, before leaving
+    if (*abort_flag) {
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 50000ull) {
+      }
+    }
+  } else if (warp == 1) {
+    // ================================================================== MMA issuer (even CTA)
+    if (leader && lane == 0) {
+      constexpr uint32_t idesc_qk = make_idesc(128, 256, FP8 ? 0u : 1u, 0, 0);
+      constexpr uint32_t idesc_pv = make_idesc(128, 256, FP8 ? 0u : 1u, 0, 1);
+      // Q chunk c (64 columns): [64 rows][128 B] at 8 KB c; E4M3: hi and lo are the first and
+      // second 512 bytes of each 1 KB group of 8 rows, 64-byte rows
+      const uint64_t dQ0 = make_sdesc(sQ, 16, 1024, FP8 ? kSwizzle64 : kSwizzle128);
+      const uint64_t dK0 = make_sdesc(sR, 16, 1024, kSwizzle128);          // [128 keys][128 B]
+      const uint64_t dP0 = make_sdesc(sP, 16, 1024, kSwizzle128);          // [key chunk][64 rows][128 B]
+      const uint64_t dV0 = make_sdesc(sR, VK * 128, 1024, kSwizzle128);    // [VC pieces][VK keys][128 B], MN-major
+      uint32_t r = 0, n = 0, pvn = 0, uc = 0;
+      bool ok = true;
+      auto issue_pv = [&](const CUnit& U, int tile) -> bool {
+        if (!wait(b_p, pvn & 1)) return false;
+        if (tile == U.tb && !wait(b_oempty, (uc & 1) ^ 1)) return false;
+        const int ns = value_slots<VK>(U.hi, tile);
+        for (int s = 0; s < ns; ++s, ++r) {
+          const uint32_t slot = r % kCRing;
+          if (!wait(b_full + 8 * slot, (r / kCRing) & 1)) return false;
+          tc_fence_after();
+          const uint64_t vd = dV0 + (uint64_t)(slot * (kCSlot >> 4));
+          const bool first = tile == U.tb && s == 0;
+          if constexpr (FP8) {
+            // keys 64 s ..: half s & 1 of the 128-key chunk s / 2; lo 16 KB after hi
+            const uint64_t pd = dP0 + (uint64_t)((s >> 1) * (8192 >> 4) + (s & 1) * 4);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int kk = 0; kk < 2; ++kk) {
+                const uint64_t vk = vd + (uint64_t)((j * 8192 + kk * 4096) >> 4);
+                umma_pair_f8(tmem + kCOCol + 128 * j, pd + 2 * kk, vk, idesc_pv, !(first && kk == 0));
+                umma_pair_f8(tmem + kCOCol + 128 * j, pd + 2 * kk + (16384 >> 4), vk, idesc_pv, 1u);
+              }
+          } else {
+            const uint64_t pd = dP0 + (uint64_t)((s >> 1) * (8192 >> 4) + (s & 1) * 4);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int kk = 0; kk < 2; ++kk)
+                umma_pair_f16(tmem + kCOCol + 128 * j, pd + 2 * kk, vd + (uint64_t)((j * 8192 + kk * 2048) >> 4),
+                              idesc_pv, !(first && kk == 0));
+          }
+          umma_pair_commit(b_empty + 8 * slot);
+        }
+        umma_pair_commit(b_pv);
+        ++pvn;
+        return true;
+      };
+      for (int u = u0; u < u1 && ok; ++u) {
+        const CUnit U = load_cunit(a, u);
+        if (U.te == U.tb) continue;
+        ok = wait(b_qfull, uc & 1);
+        for (int tile = U.tb; tile < U.te && ok; ++tile, ++n) {
+          const uint32_t d = tmem + (n & 1) * 128;
+          for (int c = 0; c < KS && ok; ++c, ++r) {
+            const uint32_t slot = r % kCRing;
+            ok = wait(b_full + 8 * slot, (r / kCRing) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t kd = dK0 + (uint64_t)(slot * (kCSlot >> 4));
+            if constexpr (FP8) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                if (c == KS - 1 && kk >= 2) break;       // the row's last 64 bytes
+                const uint64_t qd = dQ0 + (uint64_t)((2 * c + (kk >> 1)) * (kCQChunk >> 4) + (kk & 1) * 2);
+                umma_pair_f8(d, qd, kd + 2 * kk, idesc_qk, (c | kk) != 0);
+                umma_pair_f8(d, qd + (512 >> 4), kd + 2 * kk, idesc_qk, 1u);
+              }
+            } else {
+              const uint64_t qd = dQ0 + (uint64_t)(c * (kCQChunk >> 4));
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) umma_pair_f16(d, qd + 2 * kk, kd + 2 * kk, idesc_qk, (c | kk) != 0);
+            }
+            umma_pair_commit(b_empty + 8 * slot);
+          }
+          if (!ok) break;
+          umma_pair_commit(b_sfull + 8 * (n & 1));
+          if (tile == U.te - 1) umma_pair_commit(b_qempty);
+          if (tile > U.tb) ok = issue_pv(U, tile - 1);
+        }
+        if (ok) ok = issue_pv(U, U.te - 1);
+        ++uc;
+      }
+      // every MMA issued has completed before tensor memory is released
+      umma_pair_commit(b_drain);
+      volatile uint32_t no_abort = 0;
+      mbar_wait(b_drain, 0, &no_abort, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns);
+    }
+  } else if (warp < 4) {
+    // ================================================================== q terms, value fixes
+    constexpr uint32_t cbar = 3;
+    const int t = threadIdx.x - 64;
+    uint32_t r = 0, uq = 0, aux_phase = 0;     // aux_phase: a bit per slot
+    bool ok = true;
+    for (int u = u0; u < u1 && ok; ++u) {
+      const CUnit U = load_cunit(a, u);
+      const int T = U.te - U.tb;
+      if (T == 0) continue;
+      if constexpr (FP8) {
+        // The 64 rows of this CTA, bf16 as TMA landed them, become q' = q 2^e (the row's largest
+        // |q| in [128, 256)) as E4M3 hi and lo in place: every 1 KB group of 8 rows x 64 columns
+        // becomes hi in its first 512 bytes and lo in its second (64-byte swizzled rows). A warp
+        // owns whole groups; lane 4 q + p holds 16-byte units p and p + 4 of row q.
+        bool mine = wait(b_qraw, uq & 1);
+        if (mine && uq > 0) mine = wait(b_qfree, (uq - 1) & 1);   // the previous factors were read
+        if (named_bar_or(cbar, 64, !mine)) { ok = false; break; }
+        const int qrow = lane >> 2, part = lane & 3;
+        for (int g = warp - 2; g < 8; g += 2) {
+          auto block_of = [&](int c) -> uint8_t* { return gQ + c * kCQChunk + g * 1024; };
+          __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
+#pragma unroll
+          for (int c = 0; c < 9; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint4 v = *reinterpret_cast<const uint4*>(block_of(c) + qrow * 128 + (((part + 4 * h) ^ qrow) << 4));
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) m2 = __hmax2(m2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[k])));
+            }
+          float mx = fmaxf(__low2float(m2), __high2float(m2));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          int e = 0;
+          if (mx > 0.f) e = min(max(7 - ((int)((__float_as_uint(mx) >> 23) & 0xFFu) - 127), -126), 126);
+          const float f = __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll 3
+          for (int c = 0; c < 9; ++c) {
+            uint8_t* blk = block_of(c);
+            uint4 v[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              v[h] = *reinterpret_cast<const uint4*>(blk + qrow * 128 + (((part + 4 * h) ^ qrow) << 4));
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int un = part + 4 * h;           // columns 8 un .. of the chunk
+              const uint32_t w[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
+              uint32_t o[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[k] = split_e4m3x2(bf_lo(w[k]) * f, bf_hi(w[k]) * f);
+              const uint32_t off = qrow * 64 + (((un >> 1) ^ ((qrow >> 1) & 3)) << 4) + (un & 1) * 8;
+              *reinterpret_cast<uint2*>(blk + off) = make_uint2(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410));
+              *reinterpret_cast<uint2*>(blk + 512 + off) =
+                  make_uint2(__byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632));
+            }
+          }
+          if (part == 0) qf_s[8 * g + qrow] = __uint_as_float((uint32_t)(127 - e) << 23);
+        }
+        fence_proxy_async_smem();
+        named_bar_sync(cbar, 64);
+        if (t == 0) {
+          mbar_arrive(b_qsc);
+          // the issuer needs both CTAs' terms: the odd CTA signals by st.async
+          if (leader) mbar_arrive_expect_tx(b_qfull, 16);
+          else st_async_v4(lead(smem_u32(sig_s)), make_uint4(0u, 0u, 0u, 0u), lead(b_qfull));
+        }
+        ++uq;
+      }
+      // value slots with a key that some row of the block does not see (the last one or two
+      // tiles of a block); ring order: keys of the first tile, then keys of tile n + 1 and values
+      // of tile n, the last tile's values at the end
+      uint32_t rv = r + KS;                    // ring index of the unit's first value slot, tile tb
+      for (int k = 0; k < T; ++k) {
+        const int tile = U.tb + k;
+        rv += k + 1 < T ? KS : 0;
+        const int ns = value_slots<VK>(U.hi, tile);
+        for (int s = 0; s < ns && ok; ++s) {
+          const int key0 = tile * kChunkTile + s * VK;
+          if (key0 + VK <= U.lo) continue;
+          const uint32_t slot = (rv + s) % kCRing;
+          const bool mine = wait(b_aux + 8 * slot, (aux_phase >> slot) & 1);
+          aux_phase ^= 1u << slot;
+          if (named_bar_or(cbar, 64, !mine)) { ok = false; break; }
+          uint8_t* g = gR + slot * kCSlot;
+          for (int idx = t; idx < kCSlot / 16; idx += 64) {
+            const int row = (idx >> 3) % VK;
+            const int key = key0 + row;
+            if (key < U.lo) continue;
+            uint4* p = reinterpret_cast<uint4*>(g + idx * 16);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (key < U.hi) {
+              v = *p;
+              v.x = finite_word<FP8>(v.x);
+              v.y = finite_word<FP8>(v.y);
+              v.z = finite_word<FP8>(v.z);
+              v.w = finite_word<FP8>(v.w);
+            }
+            *p = v;
+          }
+          fence_proxy_async_smem();
+          named_bar_sync(cbar, 64);
+          if (t == 0) {
+            fence_acq_rel_cluster();
+            mbar_complete_tx_cluster(lead(b_full + 8 * slot), kCSlot);   // this CTA's share is in place
+          }
+        }
+        rv += ns;
+        if (!ok) break;
+      }
+      r = rv;
+    }
+  } else if (warp < 8) {
+    // ================================================================== softmax
+    constexpr uint32_t sbar = 1;
+    const int t = threadIdx.x - 128;           // tensor-memory lane
+    const int row = t & 63, half = t >> 6;     // row of this CTA, half of the tile's keys
+    const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+    const float c0 = a.softmax_scale * (FP8 ? __ldg(a.kv_scale) : 1.0f) * kCLog2e;
+    uint32_t n = 0, uc = 0, us = 0;
+    bool fail = false, stop = false;
+    for (int u = u0; u < u1 && !stop; ++u) {
+      const CUnit U = load_cunit(a, u);
+      const int T = U.te - U.tb;
+      const int br = 64 * (int)rank + row;     // row of the block
+      int vis = U.hi;
+      if (a.causal && br < U.nrows) vis = max(0, U.vis + (U.srow0 + br) / a.H);
+      float c = c0;
+      if (FP8 && T > 0) {
+        fail |= !wait(b_qsc, uc & 1);
+        c *= qf_s[row];
+        if (named_bar_or(sbar, 128, fail)) break;
+        if (t == 0) mbar_arrive(b_qfree);
+      }
+      float ref = -INFINITY, sum = 0.f;
+      for (int k = 0; k < T; ++k, ++n) {
+        const int tile = U.tb + k;
+        if (a.test_stall && n == 0) fail |= !wait(b_never, 0);   // tests: this wait runs out
+        fail |= !wait(b_sfull + 8 * (n & 1), (n >> 1) & 1);
+        tc_fence_after();
+        const uint32_t ts = tmem + lane_addr + (n & 1) * 128;
+        const int mine = vis - tile * kChunkTile - 128 * half;   // keys of this thread its row sees
+        // pass 1: the largest score
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float s[32];
+          tmem_ld32(ts + 32 * i, s);
+          tmem_wait_ld();
+          if (mine >= 32 * i + 32) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) mx = fmaxf(mx, s[x] * c);
+          } else {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) mx = fmaxf(mx, 32 * i + x < mine ? s[x] * c : -INFINITY);
+          }
+        }
+        float alpha = 1.f;
+        bool rescale = false;
+        if (named_bar_or(sbar, 128, fail || mx > ref + Cfg::kRescaleLog2)) {
+          if (named_bar_or(sbar, 128, fail)) { stop = true; break; }
+          mx_s[t] = mx;
+          named_bar_sync(sbar, 128);
+          const float nm = fmaxf(ref, fmaxf(mx, mx_s[t ^ 64]));
+          alpha = nm == -INFINITY ? 1.f : ex2_approx(ref - nm);
+          ref = nm;
+          sum *= alpha;
+          rescale = k > 0;
+        }
+        // pass 2: P, packed
+        const float off = (ref == -INFINITY ? 0.f : ref) - Cfg::kPOffLog2;
+        uint32_t pw[64];        // bf16: key pairs; E4M3: hi bytes (words 0-31), lo bytes (32-63)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float s[32];
+          tmem_ld32(ts + 32 * i, s);
+          tmem_wait_ld();
+          if (mine >= 32 * i + 32) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) s[x] = ex2_approx(fmaf(s[x], c, -off));
+          } else {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) s[x] = 32 * i + x < mine ? ex2_approx(fmaf(s[x], c, -off)) : 0.f;
+          }
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int x = 0; x < 32; ++x) part[x & 3] += s[x];      // the normaliser sums the unrounded values
+          sum += (part[0] + part[1]) + (part[2] + part[3]);
+          if constexpr (FP8) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const uint32_t o0 = split_e4m3x2(s[4 * x], s[4 * x + 1]), o1 = split_e4m3x2(s[4 * x + 2], s[4 * x + 3]);
+              pw[8 * i + x] = __byte_perm(o0, o1, 0x5410);
+              pw[32 + 8 * i + x] = __byte_perm(o0, o1, 0x7632);
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              __nv_bfloat162 h = __floats2bfloat162_rn(s[2 * x], s[2 * x + 1]);
+              pw[16 * i + x] = *reinterpret_cast<uint32_t*>(&h);
+            }
+          }
+        }
+        // P and O are free once the previous PV has completed
+        if (n > 0) fail |= !wait(b_pv, (n - 1) & 1);
+        if (rescale) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int cc = 0; cc < 16; ++cc) {
+            float o[16];
+            const uint32_t ta = tmem + lane_addr + kCOCol + 16 * cc;
+            tmem_ld16(ta, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] *= alpha;
+            tmem_st16(ta, o);
+          }
+          tmem_wait_st();
+        }
+        // bf16: key chunks 2 half and 2 half + 1 (64 keys each); E4M3: chunk `half`, lo 16 KB on
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint8_t* p = gP + (FP8 ? half * 8192 + h * 16384 : (2 * half + h) * 8192) + (row >> 3) * 1024 + (row & 7) * 128;
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            *reinterpret_cast<uint4*>(p + ((x ^ (row & 7)) << 4)) =
+                make_uint4(pw[32 * h + 4 * x], pw[32 * h + 4 * x + 1], pw[32 * h + 4 * x + 2], pw[32 * h + 4 * x + 3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        if (named_bar_or(sbar, 128, fail)) { stop = true; break; }
+        if (t == 0) {
+          if (leader) mbar_arrive(b_p);
+          else mbar_arrive_cluster(lead(b_p));
+        }
+      }
+      if (stop) break;
+      // the row's reference and this half's sum, for the epilogue
+      if (us > 0) fail |= !wait(b_statfree, (us - 1) & 1);
+      sum_s[t] = sum;
+      ref_s[t] = ref;
+      mbar_arrive(b_stat);
+      ++us;
+      if (T > 0) ++uc;
+    }
+  } else {
+    // ================================================================== epilogue
+    constexpr uint32_t ebar = 2;
+    const int t = threadIdx.x - 256;
+    const int row = t & 63, half = t >> 6;     // this thread: value columns 256 half ..
+    const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+    const float kvs = FP8 ? __ldg(a.kv_scale) : 1.0f;
+    uint32_t n = 0, us = 0;
+    bool fail = false;
+    for (int u = u0; u < u1; ++u) {
+      const CUnit U = load_cunit(a, u);
+      const int T = U.te - U.tb;
+      n += T;
+      fail |= !wait(b_stat, us & 1);
+      const float ref = ref_s[t], sum = sum_s[t] + sum_s[t ^ 64];
+      mbar_arrive(b_statfree);
+      ++us;
+      if (T > 0) fail |= !wait(b_pv, (n - 1) & 1);
+      if (named_bar_or(ebar, 128, fail)) break;
+      tc_fence_after();
+      const int br = 64 * (int)rank + row;
+      const bool keep = br < U.nrows;
+      const float inv = sum == 0.f ? 0.f : kvs / sum;          // a row that sees no key: zeros
+      const int64_t orow = (int64_t)U.row0 + br;
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        float o[32];
+        if (T > 0) {
+          tmem_ld32(tmem + lane_addr + kCOCol + 32 * i, o);
+          tmem_wait_ld();
+        }
+#pragma unroll
+        for (int x = 0; x < 32; ++x) o[x] = sum == 0.f ? 0.f : o[x] * inv;
+        const int col = 256 * half + 32 * i;
+        if (keep && U.slot < 0) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + orow * kDV + col);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t w[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              __nv_bfloat162 h = __floats2bfloat162_rn(o[8 * x + 2 * y], o[8 * x + 2 * y + 1]);
+              w[y] = *reinterpret_cast<uint32_t*>(&h);
+            }
+            dst[x] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else if (keep) {
+          float4* dst = reinterpret_cast<float4*>(a.part_o + ((int64_t)U.slot * kChunkRows + br) * kDV + col);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+        }
+        __syncwarp();
+      }
+      if (T > 0) {
+        // O has been read: the next unit's first PV may overwrite it
+        tc_fence_before();
+        named_bar_sync(ebar, 128);
+        if (t == 0) {
+          if (leader) mbar_arrive(b_oempty);
+          else mbar_arrive_cluster(lead(b_oempty));
+        }
+      }
+      if (half == 0 && keep) {
+        // P was computed times 2^kPOffLog2, and so was the row sum
+        const float l = sum == 0.f ? -INFINITY : (ref + log2f(sum) - Cfg::kPOffLog2) * kCLn2;
+        if (U.slot < 0) a.lse[orow] = l;
+        else a.part_lse[(int64_t)U.slot * kChunkRows + br] = l;
+      }
+    }
+  }
+
+  // ==================================================================== teardown
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                         // neither CTA leaves while its peer may still use it
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc_pair(tmem, kCTmemCols);
+}
+
+namespace {
+
+template <bool FP8, bool kSub>
+cudaError_t prepare_variant() {
+  cudaError_t e =
+      cudaFuncSetAttribute(chunk_kernel<FP8, kSub>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCDynBytes);
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes attr;
+  e = cudaFuncGetAttributes(&attr, chunk_kernel<FP8, kSub>);
+  if (e != cudaSuccess) return e;
+  return (int)attr.sharedSizeBytes > kCStaticBudget ? cudaErrorInvalidConfiguration : cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t chunk_prepare(bool fp8) {
+  cudaError_t e = fp8 ? prepare_variant<true, false>() : prepare_variant<false, false>();
+  if (e != cudaSuccess) return e;
+  return fp8 ? prepare_variant<true, true>() : prepare_variant<false, true>();
+}
+
+cudaError_t launch_chunk(const ChunkArgs& a, bool fp8, int pairs, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(kCThreads);
+  cfg.dynamicSmemBytes = kCDynBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // overlap the scheduler
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  // pages that are no multiple of 64 rows take the kernel that loads a slot as several boxes
+  const bool sub = a.k_box < 64;
+  if (fp8) return sub ? cudaLaunchKernelEx(&cfg, chunk_kernel<true, true>, a) : cudaLaunchKernelEx(&cfg, chunk_kernel<true, false>, a);
+  return sub ? cudaLaunchKernelEx(&cfg, chunk_kernel<false, true>, a) : cudaLaunchKernelEx(&cfg, chunk_kernel<false, false>, a);
+}
+
+}  // namespace mla

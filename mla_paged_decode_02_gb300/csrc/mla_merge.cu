@@ -1,0 +1,72 @@
+// mla_merge.cu — joins two attention results over disjoint sets of keys.
+//
+// With w_k = exp(lse_k - max(lse_a, lse_b)):
+//   out = (w_a out_a + w_b out_b) / (w_a + w_b),   lse = max + ln(w_a + w_b).
+// A result over no keys has lse = -inf: its weight is 0 and its row is not read. HBM bound:
+// 3 x 1024 bytes and 12 bytes of log-sum-exps per row; a warp takes one row, 16-byte loads.
+#include "mla_internal.h"
+#include "mla_rope.h"
+#include "../../include/mla.h"
+
+namespace mla {
+namespace {
+
+__device__ __forceinline__ void scaled(const uint4& v, float w, float* f) {
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = w * __uint_as_float(u[i] << 16);
+    f[2 * i + 1] = w * __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ uint4 rounded(const float* f) {
+  uint32_t u[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    u[i] = *reinterpret_cast<uint32_t*>(&h);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+}  // namespace
+
+// out may be out_a or out_b, and lse lse_a or lse_b: a warp reads its row before it writes it.
+__global__ void __launch_bounds__(256) merge_kernel(const uint4* out_a, const float* lse_a, const uint4* out_b,
+                                                    const float* lse_b, int64_t rows, uint4* out, float* lse) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const float la = lse_a[row], lb = lse_b[row];
+  const bool ra = la != -INFINITY, rb = lb != -INFINITY;
+  const int64_t base = row * (kDV / 8) + lane;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const uint4 a0 = ra ? out_a[base] : zero, a1 = ra ? out_a[base + 32] : zero;
+  const uint4 b0 = rb ? out_b[base] : zero, b1 = rb ? out_b[base + 32] : zero;
+  const float m = fmaxf(la, lb);
+  const float wa = ra ? expf(la - m) : 0.f, wb = rb ? expf(lb - m) : 0.f;
+  const float z = wa + wb;
+  const float inv = z == 0.f ? 0.f : 1.f / z;
+  __syncwarp();
+  float x[8], y[8];
+  scaled(a0, wa * inv, x);
+  scaled(b0, wb * inv, y);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] += y[i];
+  out[base] = rounded(x);
+  scaled(a1, wa * inv, x);
+  scaled(b1, wb * inv, y);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] += y[i];
+  out[base + 32] = rounded(x);
+  if (lane == 0) lse[row] = z == 0.f ? -INFINITY : m + logf(z);
+}
+
+cudaError_t launch_merge_states(const void* out_a, const float* lse_a, const void* out_b, const float* lse_b,
+                                int64_t rows, void* out, float* lse, cudaStream_t s) {
+  merge_kernel<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>((const uint4*)out_a, lse_a, (const uint4*)out_b, lse_b, rows,
+                                                          (uint4*)out, lse);
+  return cudaGetLastError();
+}
+
+}  // namespace mla
