@@ -17,10 +17,15 @@
 // softmax stays inside the CTA (two threads compare maxima), and P needs no exchange.
 // Tensor memory per CTA: S 2 x 128 columns, O 2 x 128.
 //
-// Shared memory per CTA: 64 query rows (72 KB), P (64 rows x 256 keys, 32 KB), and a ring of
-// seven 16 KB slots, filled in the order the MMAs consume them: the keys of tile n (slots of 128
-// keys x 128 bytes of the row), then the values of tile n - 1 (this CTA's 256 columns of 32 or,
-// E4M3, 64 keys). The 512-byte value pieces come from L2: the peer has just read those keys.
+// Shared memory per CTA: 64 query rows (72 KB), P (64 rows x 256 keys, 32 KB), a ring of four
+// 16 KB key slots (128 keys x 128 bytes of the row) and one of three 16 KB value slots (this
+// CTA's 256 columns of 32 or, E4M3, 64 keys). The 512-byte value pieces come from L2: the peer has
+// just read those keys.
+//
+// Two issuing warps, each with a ring and a producer, so that QK^T of tile n + 1 (of the next unit
+// too) overlaps the softmax and PV of tile n. They stay converged, every lane waiting and one
+// elected lane issuing: with a wait before every four MMAs an issuing thread in a branch of its
+// own takes 56 ns per MMA, an elected lane of a converged warp 36 (the rate of the tensor core).
 //
 // The FP8 cache. As in the decode kernels, the MMAs read the E4M3 bytes as they land
 // (kind::f8f6f4) against q and P written as two E4M3 terms each (hi + lo): q scaled per row by a
@@ -33,9 +38,10 @@
 // non-finite score there, which makes its result NaN without the value; a score of -inf gives
 // the key weight 0). Boxes past the last key start at the end of the pool, so TMA fills zeros.
 //
-// Roles (384 threads): warp 0 producer, warp 1 of the even CTA MMA issuer, warps 2-3 value fixes
-// and (E4M3) the split of q, warps 4-7 softmax, warps 8-11 epilogue. Every wait is bounded; a
-// stall sets the device error word, and both CTAs drain and leave through a cluster barrier.
+// Roles (448 threads): warp 0 loads q and keys, warp 2 values; warps 1 and 3 of the even CTA issue
+// QK^T and PV; warps 4-7 softmax; warps 8-11 epilogue; warps 12-13 value fixes and (E4M3) the
+// split of q. Every wait is bounded; a stall sets the device error word, and both CTAs drain and
+// leave through a cluster barrier.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include "mla_chunk.h"
@@ -45,15 +51,16 @@
 namespace mla {
 namespace {
 
-constexpr int kCRing = 7;
+constexpr int kKRing = 4;                        // key slots
+constexpr int kVRing = 3;                        // value slots
 constexpr int kCSlot = 16384;
 constexpr int kCQChunk = 8192;                   // 64 rows x 64 columns bf16
 constexpr int kCQBytes = 9 * kCQChunk;
 constexpr int kCPBytes = 64 * kChunkTile * 2;    // bf16, or E4M3 hi and lo
-constexpr int kCThreads = 384;
+constexpr int kCThreads = 448;
 constexpr int kCTmemCols = 512;
 constexpr int kCOCol = 256;                      // O at columns 256 + 128 j
-constexpr int kCDynBytes = 1024 + kCQBytes + kCPBytes + kCRing * kCSlot;
+constexpr int kCDynBytes = 1024 + kCQBytes + kCPBytes + (kKRing + kVRing) * kCSlot;
 constexpr int kCSmemLimit = 232448;
 constexpr int kCStaticBudget = 6144;
 static_assert(kCDynBytes + kCStaticBudget <= kCSmemLimit, "shared memory budget");
@@ -140,6 +147,14 @@ __device__ __forceinline__ uint32_t finite_word(uint32_t w) {
   return w;
 }
 
+// One lane of a converged warp. The issuing warps stay converged around it, their barrier waits
+// and descriptor arithmetic warp-uniform.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // 32 lanes x 32 consecutive 32-bit columns
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   tmem_ld16(taddr, v);
@@ -153,15 +168,15 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
   using Cfg = ChunkCfg<FP8>;
   constexpr int KS = Cfg::kKeySlots, VK = Cfg::kSlotKeys, VC = Cfg::kValueChunks;
   extern __shared__ uint8_t dsmem_raw[];
-  __shared__ __align__(8) uint64_t bar_full[kCRing], bar_empty[kCRing], bar_aux[kCRing];
+  __shared__ __align__(8) uint64_t bar_kfull[kKRing], bar_kempty[kKRing], bar_vfull[kVRing], bar_vempty[kVRing], bar_aux[kVRing];
   __shared__ __align__(8) uint64_t bar_qfull, bar_qempty, bar_qraw, bar_qsc, bar_qfree;
-  __shared__ __align__(8) uint64_t bar_sfull[2], bar_p, bar_pv, bar_oempty, bar_stat, bar_statfree, bar_drain, bar_never;
+  __shared__ __align__(8) uint64_t bar_sfull[2], bar_sempty[2], bar_p, bar_pv, bar_oempty, bar_stat, bar_statfree, bar_drain, bar_never;
   __shared__ __align__(16) uint32_t sig_s[4];
   __shared__ uint32_t tmem_base_s, abort_s;
   __shared__ float qf_s[64];                 // E4M3: 2^-e of this CTA's rows
   __shared__ float mx_s[128], sum_s[128], ref_s[128];
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const uint32_t peer = rank ^ 1u;
   const bool leader = rank == 0;
@@ -170,11 +185,13 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
   const uint32_t raw = smem_u32(dsmem_raw);
   const uint32_t sQ = (raw + 1023u) & ~1023u;
   uint8_t* gQ = dsmem_raw + (sQ - raw);
-  const uint32_t sP = sQ + kCQBytes, sR = sP + kCPBytes;
+  const uint32_t sP = sQ + kCQBytes, sK = sP + kCPBytes, sV = sK + kKRing * kCSlot;
   uint8_t* gP = gQ + kCQBytes;
-  uint8_t* gR = gP + kCPBytes;
+  uint8_t* gV = gP + kCPBytes + kKRing * kCSlot;
 
-  const uint32_t b_full = smem_u32(bar_full), b_empty = smem_u32(bar_empty), b_aux = smem_u32(bar_aux);
+  const uint32_t b_kfull = smem_u32(bar_kfull), b_kempty = smem_u32(bar_kempty);
+  const uint32_t b_vfull = smem_u32(bar_vfull), b_vempty = smem_u32(bar_vempty), b_aux = smem_u32(bar_aux);
+  const uint32_t b_sempty = smem_u32(bar_sempty);
   const uint32_t b_qfull = smem_u32(&bar_qfull), b_qempty = smem_u32(&bar_qempty), b_qraw = smem_u32(&bar_qraw);
   const uint32_t b_qsc = smem_u32(&bar_qsc), b_qfree = smem_u32(&bar_qfree);
   const uint32_t b_sfull = smem_u32(bar_sfull), b_p = smem_u32(&bar_p), b_pv = smem_u32(&bar_pv);
@@ -184,24 +201,30 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
   uint32_t* err = a.err;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kCRing; ++i) {
-      mbar_init(b_full + 8 * i, 1);       // the even CTA's producer, with both CTAs' bytes
-      mbar_init(b_empty + 8 * i, 1);      // the issuer's commit (both CTAs)
+    for (int i = 0; i < kKRing; ++i) {
+      mbar_init(b_kfull + 8 * i, 1);      // the even CTA's producer, with both CTAs' bytes
+      mbar_init(b_kempty + 8 * i, 1);     // the issuer's commit (both CTAs)
+    }
+    for (int i = 0; i < kVRing; ++i) {
+      mbar_init(b_vfull + 8 * i, 1);
+      mbar_init(b_vempty + 8 * i, 1);
       mbar_init(b_aux + 8 * i, 1);        // a slot that is fixed before it counts as full
     }
-    mbar_init(b_qfull, 1);                // bf16: as b_full; E4M3: the converters of both CTAs
+    mbar_init(b_qfull, 1);                // bf16: as b_kfull; E4M3: the converters of both CTAs
     mbar_init(b_qempty, 1);
     mbar_init(b_qraw, 1);
     mbar_init(b_qsc, 1);
     mbar_init(b_qfree, 1);
-    mbar_init(b_sfull, 1);
-    mbar_init(b_sfull + 8, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(b_sfull + 8 * i, 1);
+      mbar_init(b_sempty + 8 * i, 2);     // both CTAs' softmax
+    }
     mbar_init(b_p, 2);                    // both CTAs' softmax
     mbar_init(b_pv, 1);
     mbar_init(b_oempty, 2);               // both CTAs' epilogue
     mbar_init(b_stat, 128);
     mbar_init(b_statfree, 128);
-    mbar_init(b_drain, 1);
+    mbar_init(b_drain, 2);                // both issuers
     mbar_init(b_never, 1);
     abort_s = 0u;
     fence_mbarrier_init();
@@ -227,195 +250,251 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
     return ok;
   };
 
+  // the same by every lane of a warp that stays converged
+  auto wait_warp = [&](uint32_t bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
+
   if (warp == 0) {
-    // ================================================================== producer
-    // lane i issues box i of a slot; every slot takes the same bytes from both CTAs
-    const int kbox = kSub ? a.k_box : 64, vbox = kSub ? a.v_box : VK;
+    // ================================================================== q and keys
+    // one thread issues two boxes per slot; pages smaller than 64 rows: lane i issues box i.
+    // Every slot takes the same bytes from both CTAs.
+    const int kbox = kSub ? a.k_box : 64;
     const int nk = 128 / kbox;                          // boxes of a key slot
-    const int nvr = VK / vbox;                          // boxes down a value slot
-    const bool wide = !FP8 && !kSub;                    // one box of all four value chunks
-    const int nv = wide ? 1 : nvr * VC;
-    uint32_t r = 0, uq = 0;
+    const bool el = elect_one();
+    uint32_t slot = 0, ph = 1, uq = 0;
     bool ok = true;
-    auto slot_free = [&](uint32_t slot) -> bool {
-      int w = 1;
-      if (lane == 0) w = wait(b_empty + 8 * slot, ((r / kCRing) & 1) ^ 1) ? 1 : 0;
-      return __shfl_sync(0xffffffffu, w, 0) != 0;
+    auto load = [&](uint32_t dst, uint32_t bar, int row, int c) {
+      if (FP8) tma_load_2d_pair(dst, &a.tm_k, bar, 128 * c, row);
+      else tma_load_3d_pair(dst, &a.tm_k, bar, 0, row, c);
     };
-    auto load_keys = [&](int rows) -> bool {
-      const int row = __shfl_sync(0xffffffffu, rows, 16 * (int)rank + (lane < nk ? lane * (kbox >> 3) : 0));
-      for (int c = 0; c < KS; ++c, ++r) {
-        const uint32_t slot = r % kCRing;
-        if (!slot_free(slot)) return false;
-        const uint32_t lb = lead(b_full + 8 * slot);
-        if (leader && lane == 0) mbar_arrive_expect_tx(b_full + 8 * slot, 2 * kCSlot);
-        if (lane < nk) {
-          const uint32_t dst = sR + slot * kCSlot + (uint32_t)(lane * kbox) * 128u;
-          if (FP8) tma_load_2d_pair(dst, &a.tm_k, lb, 128 * c, row);
-          else tma_load_3d_pair(dst, &a.tm_k, lb, 0, row, c);
-        }
-      }
-      return true;
-    };
-    auto load_values = [&](const CUnit& U, int tile, int rows) -> bool {
-      const int n = value_slots<VK>(U.hi, tile);
-      for (int s = 0; s < n; ++s, ++r) {
-        const uint32_t slot = r % kCRing;
-        if (!slot_free(slot)) return false;
-        const int i = wide ? 0 : lane % nvr, c = wide ? 0 : lane / nvr;   // box i of chunk c
-        const int row = __shfl_sync(0xffffffffu, rows, (s * VK + (lane < nv ? i * vbox : 0)) >> 3);
-        const bool fix = tile * kChunkTile + (s + 1) * VK > U.lo;
-        if (lane == 0) {
-          if (leader) mbar_arrive_expect_tx(b_full + 8 * slot, 2 * kCSlot);
-          if (fix) mbar_arrive_expect_tx(b_aux + 8 * slot, kCSlot);
-        }
-        __syncwarp();
-        if (lane < nv) {
-          const uint32_t dst = sR + slot * kCSlot + (uint32_t)(c * VK + i * vbox) * 128u;
-          const int col = VC * (int)rank + c;                            // 128-byte piece of the row
-          if (fix) {
-            if (FP8) tma_load_2d(dst, &a.tm_v, b_aux + 8 * slot, 128 * col, row);
-            else tma_load_3d(dst, &a.tm_v, b_aux + 8 * slot, 0, row, col);
-          } else {
-            const uint32_t lb = lead(b_full + 8 * slot);
-            if (FP8) tma_load_2d_pair(dst, &a.tm_v, lb, 128 * col, row);
-            else tma_load_3d_pair(dst, &a.tm_v, lb, 0, row, col);
-          }
-        }
-      }
-      return true;
-    };
+    const uint32_t lb = lead(b_kfull);
     for (int u = u0; u < u1 && ok; ++u) {
       const CUnit U = load_cunit(a, u);
       if (U.te == U.tb) continue;
-      int rows = tile_row(a, U, U.tb, lane), prev_rows = 0;
-      int w = 1;
-      if (lane == 0) {
-        w = wait(b_qempty, (uq & 1) ^ 1) ? 1 : 0;
-        if (w) {
-          const int32_t q0 = U.row0 + 64 * (int)rank;
-          if (FP8) {
-            mbar_arrive_expect_tx(b_qraw, kCQBytes);
-            tma_load_3d(sQ, &a.tm_q, b_qraw, 0, q0, 0);
-          } else {
-            if (leader) mbar_arrive_expect_tx(b_qfull, 2 * kCQBytes);
-            tma_load_3d_pair(sQ, &a.tm_q, lead(b_qfull), 0, q0, 0);
-          }
+      int rows = tile_row(a, U, U.tb, lane);
+      ok = wait_warp(b_qempty, (uq & 1) ^ 1);
+      if (!ok) break;
+      if (el) {
+        const int32_t q0 = U.row0 + 64 * (int)rank;
+        if (FP8) {
+          mbar_arrive_expect_tx(b_qraw, kCQBytes);
+          tma_load_3d(sQ, &a.tm_q, b_qraw, 0, q0, 0);
+        } else {
+          if (leader) mbar_arrive_expect_tx(b_qfull, 2 * kCQBytes);
+          tma_load_3d_pair(sQ, &a.tm_q, lead(b_qfull), 0, q0, 0);
         }
       }
-      ok = __shfl_sync(0xffffffffu, w, 0) != 0;
       ++uq;
-      for (int tile = U.tb; tile < U.te && ok; ++tile) {
+      for (int tile = U.tb; tile < U.te; ++tile) {
         // the next tile's page numbers are on their way while this tile's keys are issued
         const int next_rows = tile + 1 < U.te ? tile_row(a, U, tile + 1, lane) : 0;
-        ok = load_keys(rows);
-        if (ok && tile > U.tb) ok = load_values(U, tile - 1, prev_rows);
-        prev_rows = rows;
+        const int r0 = __shfl_sync(0xffffffffu, rows, 16 * (int)rank), r1 = __shfl_sync(0xffffffffu, rows, 16 * (int)rank + 8);
+        const int row = __shfl_sync(0xffffffffu, rows, 16 * (int)rank + (lane < nk ? lane * (kbox >> 3) : 0));
+        for (int c = 0; c < KS; ++c) {
+          ok = wait_warp(b_kempty + 8 * slot, ph);
+          if (!ok) break;
+          const uint32_t dst = sK + slot * kCSlot, bar = lb + 8 * slot;
+          if (el) {
+            if (leader) mbar_arrive_expect_tx(b_kfull + 8 * slot, 2 * kCSlot);
+            if (!kSub) {
+              load(dst, bar, r0, c);
+              load(dst + kCSlot / 2, bar, r1, c);
+            }
+          }
+          if (kSub && lane < nk) load(dst + (uint32_t)(lane * kbox) * 128u, bar, row, c);
+          if (++slot == kKRing) {
+            slot = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
         rows = next_rows;
       }
-      if (ok) ok = load_values(U, U.te - 1, prev_rows);
     }
     // after an abort the odd CTA cannot observe its own loads (they count on the even CTA's
-    // barriers): both producers wait 50 us, far longer than a load takes, before leaving
+    // barriers): the producers wait 50 us, far longer than a load takes, before leaving
+    if (*abort_flag) {
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 50000ull) {
+      }
+    }
+  } else if (warp == 2) {
+    // ================================================================== values
+    const int vbox = kSub ? a.v_box : VK;
+    const int nvr = VK / vbox;                          // boxes down a value slot
+    const int nv = nvr * VC;
+    const bool el = elect_one();
+    uint32_t slot = 0, ph = 1;
+    bool ok = true;
+    const uint32_t lb = lead(b_vfull);
+    // a slot with a key that some row does not see is loaded on a barrier of this CTA; the
+    // fixing warps then count its bytes
+    auto load = [&](uint32_t dst, bool fix, int row, int col) {   // col: 128-byte piece of the row
+      if (fix) {
+        if (FP8) tma_load_2d(dst, &a.tm_v, b_aux + 8 * slot, 128 * col, row);
+        else tma_load_3d(dst, &a.tm_v, b_aux + 8 * slot, 0, row, col);
+      } else {
+        if (FP8) tma_load_2d_pair(dst, &a.tm_v, lb + 8 * slot, 128 * col, row);
+        else tma_load_3d_pair(dst, &a.tm_v, lb + 8 * slot, 0, row, col);
+      }
+    };
+    const int c0 = VC * (int)rank;
+    for (int u = u0; u < u1 && ok; ++u) {
+      const CUnit U = load_cunit(a, u);
+      if (U.te == U.tb) continue;
+      int rows = tile_row(a, U, U.tb, lane);
+      for (int tile = U.tb; tile < U.te; ++tile) {
+        const int next_rows = tile + 1 < U.te ? tile_row(a, U, tile + 1, lane) : 0;
+        const int n = value_slots<VK>(U.hi, tile);
+        int key = tile * kChunkTile;
+        const int i = lane % nvr, c = lane / nvr;       // kSub: this lane's box i of piece c
+        for (int s = 0; s < n; ++s) {
+          const int r0 = __shfl_sync(0xffffffffu, rows, s * VK >> 3);
+          const int row = kSub ? __shfl_sync(0xffffffffu, rows, (s * VK + (lane < nv ? i * vbox : 0)) >> 3) : 0;
+          key += VK;
+          const bool fix = key > U.lo;
+          ok = wait_warp(b_vempty + 8 * slot, ph);
+          if (!ok) break;
+          const uint32_t dst = sV + slot * kCSlot;
+          if (el) {
+            if (leader) mbar_arrive_expect_tx(b_vfull + 8 * slot, 2 * kCSlot);
+            if (fix) mbar_arrive_expect_tx(b_aux + 8 * slot, kCSlot);
+            if (!kSub) {
+              load(dst, fix, r0, c0);                            // bf16: four pieces in one box
+              if (FP8) load(dst + kCSlot / 2, fix, r0, c0 + 1);
+            }
+          }
+          if (kSub) {
+            __syncwarp();
+            if (lane < nv) load(dst + (uint32_t)(c * VK + i * vbox) * 128u, fix, row, c0 + c);
+          }
+          if (++slot == kVRing) {
+            slot = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+        rows = next_rows;
+      }
+    }
     if (*abort_flag) {
       const uint64_t t0 = global_timer_ns();
       while (global_timer_ns() - t0 < 50000ull) {
       }
     }
   } else if (warp == 1) {
-    // ================================================================== MMA issuer (even CTA)
-    if (leader && lane == 0) {
-      constexpr uint32_t idesc_qk = make_idesc(128, 256, FP8 ? 0u : 1u, 0, 0);
-      constexpr uint32_t idesc_pv = make_idesc(128, 256, FP8 ? 0u : 1u, 0, 1);
+    // ================================================================== QK^T (even CTA)
+    if (leader) {
+      const bool el = elect_one();
+      constexpr uint32_t idesc = make_idesc(128, 256, FP8 ? 0u : 1u, 0, 0);
       // Q chunk c (64 columns): [64 rows][128 B] at 8 KB c; E4M3: hi and lo are the first and
       // second 512 bytes of each 1 KB group of 8 rows, 64-byte rows
       const uint64_t dQ0 = make_sdesc(sQ, 16, 1024, FP8 ? kSwizzle64 : kSwizzle128);
-      const uint64_t dK0 = make_sdesc(sR, 16, 1024, kSwizzle128);          // [128 keys][128 B]
-      const uint64_t dP0 = make_sdesc(sP, 16, 1024, kSwizzle128);          // [key chunk][64 rows][128 B]
-      const uint64_t dV0 = make_sdesc(sR, VK * 128, 1024, kSwizzle128);    // [VC pieces][VK keys][128 B], MN-major
-      uint32_t r = 0, n = 0, pvn = 0, uc = 0;
+      const uint64_t dK0 = make_sdesc(sK, 16, 1024, kSwizzle128);          // [128 keys][128 B]
+      uint32_t slot = 0, ph = 0, n = 0, uc = 0;
       bool ok = true;
-      auto issue_pv = [&](const CUnit& U, int tile) -> bool {
-        if (!wait(b_p, pvn & 1)) return false;
-        if (tile == U.tb && !wait(b_oempty, (uc & 1) ^ 1)) return false;
-        const int ns = value_slots<VK>(U.hi, tile);
-        for (int s = 0; s < ns; ++s, ++r) {
-          const uint32_t slot = r % kCRing;
-          if (!wait(b_full + 8 * slot, (r / kCRing) & 1)) return false;
-          tc_fence_after();
-          const uint64_t vd = dV0 + (uint64_t)(slot * (kCSlot >> 4));
-          const bool first = tile == U.tb && s == 0;
-          if constexpr (FP8) {
-            // keys 64 s ..: half s & 1 of the 128-key chunk s / 2; lo 16 KB after hi
-            const uint64_t pd = dP0 + (uint64_t)((s >> 1) * (8192 >> 4) + (s & 1) * 4);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int kk = 0; kk < 2; ++kk) {
-                const uint64_t vk = vd + (uint64_t)((j * 8192 + kk * 4096) >> 4);
-                umma_pair_f8(tmem + kCOCol + 128 * j, pd + 2 * kk, vk, idesc_pv, !(first && kk == 0));
-                umma_pair_f8(tmem + kCOCol + 128 * j, pd + 2 * kk + (16384 >> 4), vk, idesc_pv, 1u);
-              }
-          } else {
-            const uint64_t pd = dP0 + (uint64_t)((s >> 1) * (8192 >> 4) + (s & 1) * 4);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int kk = 0; kk < 2; ++kk)
-                umma_pair_f16(tmem + kCOCol + 128 * j, pd + 2 * kk, vd + (uint64_t)((j * 8192 + kk * 2048) >> 4),
-                              idesc_pv, !(first && kk == 0));
-          }
-          umma_pair_commit(b_empty + 8 * slot);
-        }
-        umma_pair_commit(b_pv);
-        ++pvn;
-        return true;
-      };
       for (int u = u0; u < u1 && ok; ++u) {
         const CUnit U = load_cunit(a, u);
         if (U.te == U.tb) continue;
-        ok = wait(b_qfull, uc & 1);
+        ok = wait_warp(b_qfull, uc & 1);
         for (int tile = U.tb; tile < U.te && ok; ++tile, ++n) {
           const uint32_t d = tmem + (n & 1) * 128;
-          for (int c = 0; c < KS && ok; ++c, ++r) {
-            const uint32_t slot = r % kCRing;
-            ok = wait(b_full + 8 * slot, (r / kCRing) & 1);
+          ok = wait_warp(b_sempty + 8 * (n & 1), ((n >> 1) & 1) ^ 1);
+          for (int c = 0; c < KS && ok; ++c) {
+            ok = wait_warp(b_kfull + 8 * slot, ph);
             if (!ok) break;
             tc_fence_after();
             const uint64_t kd = dK0 + (uint64_t)(slot * (kCSlot >> 4));
-            if constexpr (FP8) {
+            if (!el) {
+            } else if constexpr (FP8) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk) {
                 if (c == KS - 1 && kk >= 2) break;       // the row's last 64 bytes
                 const uint64_t qd = dQ0 + (uint64_t)((2 * c + (kk >> 1)) * (kCQChunk >> 4) + (kk & 1) * 2);
-                umma_pair_f8(d, qd, kd + 2 * kk, idesc_qk, (c | kk) != 0);
-                umma_pair_f8(d, qd + (512 >> 4), kd + 2 * kk, idesc_qk, 1u);
+                umma_pair_f8(d, qd, kd + 2 * kk, idesc, (c | kk) != 0);
+                umma_pair_f8(d, qd + (512 >> 4), kd + 2 * kk, idesc, 1u);
               }
             } else {
               const uint64_t qd = dQ0 + (uint64_t)(c * (kCQChunk >> 4));
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) umma_pair_f16(d, qd + 2 * kk, kd + 2 * kk, idesc_qk, (c | kk) != 0);
+              for (int kk = 0; kk < 4; ++kk) umma_pair_f16(d, qd + 2 * kk, kd + 2 * kk, idesc, (c | kk) != 0);
             }
-            umma_pair_commit(b_empty + 8 * slot);
+            if (el) umma_pair_commit(b_kempty + 8 * slot);
+            if (++slot == kKRing) {
+              slot = 0;
+              ph ^= 1;
+            }
           }
           if (!ok) break;
-          umma_pair_commit(b_sfull + 8 * (n & 1));
-          if (tile == U.te - 1) umma_pair_commit(b_qempty);
-          if (tile > U.tb) ok = issue_pv(U, tile - 1);
+          if (el) {
+            umma_pair_commit(b_sfull + 8 * (n & 1));
+            if (tile == U.te - 1) umma_pair_commit(b_qempty);
+          }
         }
-        if (ok) ok = issue_pv(U, U.te - 1);
         ++uc;
       }
       // every MMA issued has completed before tensor memory is released
-      umma_pair_commit(b_drain);
+      if (el) umma_pair_commit(b_drain);
       volatile uint32_t no_abort = 0;
       mbar_wait(b_drain, 0, &no_abort, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns);
     }
-  } else if (warp < 4) {
+  } else if (warp == 3) {
+    // ================================================================== PV (even CTA)
+    if (leader) {
+      const bool el = elect_one();
+      constexpr uint32_t idesc = make_idesc(128, 256, FP8 ? 0u : 1u, 0, 1);
+      const uint64_t dP0 = make_sdesc(sP, 16, 1024, kSwizzle128);          // [key chunk][64 rows][128 B]
+      const uint64_t dV0 = make_sdesc(sV, VK * 128, 1024, kSwizzle128);    // [VC pieces][VK keys][128 B], MN-major
+      uint32_t slot = 0, ph = 0, n = 0, uc = 0;
+      bool ok = true;
+      for (int u = u0; u < u1 && ok; ++u) {
+        const CUnit U = load_cunit(a, u);
+        if (U.te == U.tb) continue;
+        for (int tile = U.tb; tile < U.te && ok; ++tile, ++n) {
+          ok = wait_warp(b_p, n & 1);
+          if (ok && tile == U.tb) ok = wait_warp(b_oempty, (uc & 1) ^ 1);
+          const int ns = value_slots<VK>(U.hi, tile);
+          for (int s = 0; s < ns && ok; ++s) {
+            ok = wait_warp(b_vfull + 8 * slot, ph);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t vd = dV0 + (uint64_t)(slot * (kCSlot >> 4));
+            // keys VK s ..: half s & 1 of a 128-byte chunk of P's columns; E4M3: lo 16 KB after hi
+            const uint64_t pd = dP0 + (uint64_t)((s >> 1) * (8192 >> 4) + (s & 1) * 4);
+            const bool first = tile == U.tb && s == 0;
+            if (el) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                  const uint64_t vk = vd + (uint64_t)((j * 8192 + kk * (FP8 ? 4096 : 2048)) >> 4);
+                  const uint32_t acc = !(first && kk == 0);
+                  if constexpr (FP8) {
+                    umma_pair_f8(tmem + kCOCol + 128 * j, pd + 2 * kk, vk, idesc, acc);
+                    umma_pair_f8(tmem + kCOCol + 128 * j, pd + 2 * kk + (16384 >> 4), vk, idesc, 1u);
+                  } else {
+                    umma_pair_f16(tmem + kCOCol + 128 * j, pd + 2 * kk, vk, idesc, acc);
+                  }
+                }
+              umma_pair_commit(b_vempty + 8 * slot);
+            }
+            if (++slot == kVRing) {
+              slot = 0;
+              ph ^= 1;
+            }
+          }
+          if (ok && el) umma_pair_commit(b_pv);
+        }
+        ++uc;
+      }
+      if (el) umma_pair_commit(b_drain);
+      volatile uint32_t no_abort = 0;
+      mbar_wait(b_drain, 0, &no_abort, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns);
+    }
+  } else if (warp >= 12) {
     // ================================================================== q terms, value fixes
     constexpr uint32_t cbar = 3;
-    const int t = threadIdx.x - 64;
-    uint32_t r = 0, uq = 0, aux_phase = 0;     // aux_phase: a bit per slot
+    const int t = threadIdx.x - 384;
+    uint32_t rv = 0, uq = 0, aux_phase = 0;    // value slots so far; a phase bit per slot
     bool ok = true;
     for (int u = u0; u < u1 && ok; ++u) {
       const CUnit U = load_cunit(a, u);
@@ -430,7 +509,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         if (mine && uq > 0) mine = wait(b_qfree, (uq - 1) & 1);   // the previous factors were read
         if (named_bar_or(cbar, 64, !mine)) { ok = false; break; }
         const int qrow = lane >> 2, part = lane & 3;
-        for (int g = warp - 2; g < 8; g += 2) {
+        for (int g = warp - 12; g < 8; g += 2) {
           auto block_of = [&](int c) -> uint8_t* { return gQ + c * kCQChunk + g * 1024; };
           __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
 #pragma unroll
@@ -482,21 +561,18 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         ++uq;
       }
       // value slots with a key that some row of the block does not see (the last one or two
-      // tiles of a block); ring order: keys of the first tile, then keys of tile n + 1 and values
-      // of tile n, the last tile's values at the end
-      uint32_t rv = r + KS;                    // ring index of the unit's first value slot, tile tb
+      // tiles of a block)
       for (int k = 0; k < T; ++k) {
         const int tile = U.tb + k;
-        rv += k + 1 < T ? KS : 0;
         const int ns = value_slots<VK>(U.hi, tile);
         for (int s = 0; s < ns && ok; ++s) {
           const int key0 = tile * kChunkTile + s * VK;
           if (key0 + VK <= U.lo) continue;
-          const uint32_t slot = (rv + s) % kCRing;
+          const uint32_t slot = (rv + s) % kVRing;
           const bool mine = wait(b_aux + 8 * slot, (aux_phase >> slot) & 1);
           aux_phase ^= 1u << slot;
           if (named_bar_or(cbar, 64, !mine)) { ok = false; break; }
-          uint8_t* g = gR + slot * kCSlot;
+          uint8_t* g = gV + slot * kCSlot;
           for (int idx = t; idx < kCSlot / 16; idx += 64) {
             const int row = (idx >> 3) % VK;
             const int key = key0 + row;
@@ -516,13 +592,12 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
           named_bar_sync(cbar, 64);
           if (t == 0) {
             fence_acq_rel_cluster();
-            mbar_complete_tx_cluster(lead(b_full + 8 * slot), kCSlot);   // this CTA's share is in place
+            mbar_complete_tx_cluster(lead(b_vfull + 8 * slot), kCSlot);   // this CTA's share is in place
           }
         }
         rv += ns;
         if (!ok) break;
       }
-      r = rv;
     }
   } else if (warp < 8) {
     // ================================================================== softmax
@@ -615,6 +690,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
             }
           }
         }
+        // S has been read (every thread's part, at the barrier below): its buffer is released with P
         // P and O are free once the previous PV has completed
         if (n > 0) fail |= !wait(b_pv, (n - 1) & 1);
         if (rescale) {
@@ -644,8 +720,13 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         tc_fence_before();
         if (named_bar_or(sbar, 128, fail)) { stop = true; break; }
         if (t == 0) {
-          if (leader) mbar_arrive(b_p);
-          else mbar_arrive_cluster(lead(b_p));
+          if (leader) {
+            mbar_arrive(b_p);
+            mbar_arrive(b_sempty + 8 * (n & 1));
+          } else {
+            mbar_arrive_cluster(lead(b_p));
+            mbar_arrive_cluster(lead(b_sempty + 8 * (n & 1)));
+          }
         }
       }
       if (stop) break;
@@ -657,7 +738,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
       ++us;
       if (T > 0) ++uc;
     }
-  } else {
+  } else if (warp < 12) {
     // ================================================================== epilogue
     constexpr uint32_t ebar = 2;
     const int t = threadIdx.x - 256;
