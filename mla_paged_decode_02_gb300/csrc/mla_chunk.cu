@@ -38,9 +38,9 @@
 // non-finite score there, which makes its result NaN without the value; a score of -inf gives
 // the key weight 0). Boxes past the last key start at the end of the pool, so TMA fills zeros.
 //
-// Roles (448 threads): warp 0 loads q and keys, warp 2 values; warps 1 and 3 of the even CTA issue
+// Roles (512 threads): warp 0 loads q and keys, warp 2 values; warps 1 and 3 of the even CTA issue
 // QK^T and PV; warps 4-7 softmax; warps 8-11 epilogue; warps 12-13 value fixes and (E4M3) the
-// split of q. Every wait is bounded; a stall sets the device error word, and both CTAs drain and
+// split of q (14-15 idle). Every wait is bounded; a stall sets the device error word, and both CTAs drain and
 // leave through a cluster barrier.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -57,7 +57,7 @@ constexpr int kCSlot = 16384;
 constexpr int kCQChunk = 8192;                   // 64 rows x 64 columns bf16
 constexpr int kCQBytes = 9 * kCQChunk;
 constexpr int kCPBytes = 64 * kChunkTile * 2;    // bf16, or E4M3 hi and lo
-constexpr int kCThreads = 448;
+constexpr int kCThreads = 512;
 constexpr int kCTmemCols = 512;
 constexpr int kCOCol = 256;                      // O at columns 256 + 128 j
 constexpr int kCDynBytes = 1024 + kCQBytes + kCPBytes + (kKRing + kVRing) * kCSlot;
@@ -130,6 +130,11 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       :: "r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(c0), "r"(c1) : "memory");
 }
 
+// An arrival at the cluster's even CTA that publishes no writes (what it releases was only read).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar_cluster) : "memory");
+}
+
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
@@ -170,7 +175,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
   extern __shared__ uint8_t dsmem_raw[];
   __shared__ __align__(8) uint64_t bar_kfull[kKRing], bar_kempty[kKRing], bar_vfull[kVRing], bar_vempty[kVRing], bar_aux[kVRing];
   __shared__ __align__(8) uint64_t bar_qfull, bar_qempty, bar_qraw, bar_qsc, bar_qfree;
-  __shared__ __align__(8) uint64_t bar_sfull[2], bar_sempty[2], bar_p, bar_pv, bar_oempty, bar_stat, bar_statfree, bar_drain, bar_never;
+  __shared__ __align__(8) uint64_t bar_sfull[2], bar_sempty[2], bar_p[2], bar_pv[2], bar_oempty, bar_stat, bar_statfree, bar_drain, bar_never;
   __shared__ __align__(16) uint32_t sig_s[4];
   __shared__ uint32_t tmem_base_s, abort_s;
   __shared__ float qf_s[64];                 // E4M3: 2^-e of this CTA's rows
@@ -194,7 +199,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
   const uint32_t b_sempty = smem_u32(bar_sempty);
   const uint32_t b_qfull = smem_u32(&bar_qfull), b_qempty = smem_u32(&bar_qempty), b_qraw = smem_u32(&bar_qraw);
   const uint32_t b_qsc = smem_u32(&bar_qsc), b_qfree = smem_u32(&bar_qfree);
-  const uint32_t b_sfull = smem_u32(bar_sfull), b_p = smem_u32(&bar_p), b_pv = smem_u32(&bar_pv);
+  const uint32_t b_sfull = smem_u32(bar_sfull), b_p = smem_u32(bar_p), b_pv = smem_u32(bar_pv);
   const uint32_t b_oempty = smem_u32(&bar_oempty), b_stat = smem_u32(&bar_stat), b_statfree = smem_u32(&bar_statfree);
   const uint32_t b_drain = smem_u32(&bar_drain), b_never = smem_u32(&bar_never);
   volatile uint32_t* abort_flag = &abort_s;
@@ -217,10 +222,10 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
     mbar_init(b_qfree, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_sfull + 8 * i, 1);
-      mbar_init(b_sempty + 8 * i, 2);     // both CTAs' softmax
+      mbar_init(b_sempty + 8 * i, 8);     // both CTAs' softmax warps
+      mbar_init(b_p + 8 * i, 2);          // half i of P's keys: both CTAs' softmax
+      mbar_init(b_pv + 8 * i, 1);
     }
-    mbar_init(b_p, 2);                    // both CTAs' softmax
-    mbar_init(b_pv, 1);
     mbar_init(b_oempty, 2);               // both CTAs' epilogue
     mbar_init(b_stat, 128);
     mbar_init(b_statfree, 128);
@@ -253,353 +258,258 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
   // the same by every lane of a warp that stays converged
   auto wait_warp = [&](uint32_t bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
 
-  if (warp == 0) {
-    // ================================================================== q and keys
-    // one thread issues two boxes per slot; pages smaller than 64 rows: lane i issues box i.
-    // Every slot takes the same bytes from both CTAs.
-    const int kbox = kSub ? a.k_box : 64;
-    const int nk = 128 / kbox;                          // boxes of a key slot
-    const bool el = elect_one();
-    uint32_t slot = 0, ph = 1, uq = 0;
-    bool ok = true;
-    auto load = [&](uint32_t dst, uint32_t bar, int row, int c) {
-      if (FP8) tma_load_2d_pair(dst, &a.tm_k, bar, 128 * c, row);
-      else tma_load_3d_pair(dst, &a.tm_k, bar, 0, row, c);
-    };
-    const uint32_t lb = lead(b_kfull);
-    for (int u = u0; u < u1 && ok; ++u) {
-      const CUnit U = load_cunit(a, u);
-      if (U.te == U.tb) continue;
-      int rows = tile_row(a, U, U.tb, lane);
-      ok = wait_warp(b_qempty, (uq & 1) ^ 1);
-      if (!ok) break;
-      if (el) {
-        const int32_t q0 = U.row0 + 64 * (int)rank;
-        if (FP8) {
-          mbar_arrive_expect_tx(b_qraw, kCQBytes);
-          tma_load_3d(sQ, &a.tm_q, b_qraw, 0, q0, 0);
-        } else {
-          if (leader) mbar_arrive_expect_tx(b_qfull, 2 * kCQBytes);
-          tma_load_3d_pair(sQ, &a.tm_q, lead(b_qfull), 0, q0, 0);
-        }
-      }
-      ++uq;
-      for (int tile = U.tb; tile < U.te; ++tile) {
-        // the next tile's page numbers are on their way while this tile's keys are issued
-        const int next_rows = tile + 1 < U.te ? tile_row(a, U, tile + 1, lane) : 0;
-        const int r0 = __shfl_sync(0xffffffffu, rows, 16 * (int)rank), r1 = __shfl_sync(0xffffffffu, rows, 16 * (int)rank + 8);
-        const int row = __shfl_sync(0xffffffffu, rows, 16 * (int)rank + (lane < nk ? lane * (kbox >> 3) : 0));
-        for (int c = 0; c < KS; ++c) {
-          ok = wait_warp(b_kempty + 8 * slot, ph);
-          if (!ok) break;
-          const uint32_t dst = sK + slot * kCSlot, bar = lb + 8 * slot;
-          if (el) {
-            if (leader) mbar_arrive_expect_tx(b_kfull + 8 * slot, 2 * kCSlot);
-            if (!kSub) {
-              load(dst, bar, r0, c);
-              load(dst + kCSlot / 2, bar, r1, c);
-            }
-          }
-          if (kSub && lane < nk) load(dst + (uint32_t)(lane * kbox) * 128u, bar, row, c);
-          if (++slot == kKRing) {
-            slot = 0;
-            ph ^= 1;
-          }
-        }
-        if (!ok) break;
-        rows = next_rows;
-      }
-    }
-    // after an abort the odd CTA cannot observe its own loads (they count on the even CTA's
-    // barriers): the producers wait 50 us, far longer than a load takes, before leaving
-    if (*abort_flag) {
-      const uint64_t t0 = global_timer_ns();
-      while (global_timer_ns() - t0 < 50000ull) {
-      }
-    }
-  } else if (warp == 2) {
-    // ================================================================== values
-    const int vbox = kSub ? a.v_box : VK;
-    const int nvr = VK / vbox;                          // boxes down a value slot
-    const int nv = nvr * VC;
-    const bool el = elect_one();
-    uint32_t slot = 0, ph = 1;
-    bool ok = true;
-    const uint32_t lb = lead(b_vfull);
-    // a slot with a key that some row does not see is loaded on a barrier of this CTA; the
-    // fixing warps then count its bytes
-    auto load = [&](uint32_t dst, bool fix, int row, int col) {   // col: 128-byte piece of the row
-      if (fix) {
-        if (FP8) tma_load_2d(dst, &a.tm_v, b_aux + 8 * slot, 128 * col, row);
-        else tma_load_3d(dst, &a.tm_v, b_aux + 8 * slot, 0, row, col);
-      } else {
-        if (FP8) tma_load_2d_pair(dst, &a.tm_v, lb + 8 * slot, 128 * col, row);
-        else tma_load_3d_pair(dst, &a.tm_v, lb + 8 * slot, 0, row, col);
-      }
-    };
-    const int c0 = VC * (int)rank;
-    for (int u = u0; u < u1 && ok; ++u) {
-      const CUnit U = load_cunit(a, u);
-      if (U.te == U.tb) continue;
-      int rows = tile_row(a, U, U.tb, lane);
-      for (int tile = U.tb; tile < U.te; ++tile) {
-        const int next_rows = tile + 1 < U.te ? tile_row(a, U, tile + 1, lane) : 0;
-        const int n = value_slots<VK>(U.hi, tile);
-        int key = tile * kChunkTile;
-        const int i = lane % nvr, c = lane / nvr;       // kSub: this lane's box i of piece c
-        for (int s = 0; s < n; ++s) {
-          const int r0 = __shfl_sync(0xffffffffu, rows, s * VK >> 3);
-          const int row = kSub ? __shfl_sync(0xffffffffu, rows, (s * VK + (lane < nv ? i * vbox : 0)) >> 3) : 0;
-          key += VK;
-          const bool fix = key > U.lo;
-          ok = wait_warp(b_vempty + 8 * slot, ph);
-          if (!ok) break;
-          const uint32_t dst = sV + slot * kCSlot;
-          if (el) {
-            if (leader) mbar_arrive_expect_tx(b_vfull + 8 * slot, 2 * kCSlot);
-            if (fix) mbar_arrive_expect_tx(b_aux + 8 * slot, kCSlot);
-            if (!kSub) {
-              load(dst, fix, r0, c0);                            // bf16: four pieces in one box
-              if (FP8) load(dst + kCSlot / 2, fix, r0, c0 + 1);
-            }
-          }
-          if (kSub) {
-            __syncwarp();
-            if (lane < nv) load(dst + (uint32_t)(c * VK + i * vbox) * 128u, fix, row, c0 + c);
-          }
-          if (++slot == kVRing) {
-            slot = 0;
-            ph ^= 1;
-          }
-        }
-        if (!ok) break;
-        rows = next_rows;
-      }
-    }
-    if (*abort_flag) {
-      const uint64_t t0 = global_timer_ns();
-      while (global_timer_ns() - t0 < 50000ull) {
-      }
-    }
-  } else if (warp == 1) {
-    // ================================================================== QK^T (even CTA)
-    if (leader) {
+  // The launch gives every thread 128 registers. The epilogue's threads hold 256 columns of a row
+  // as bf16, the softmax's 128 probabilities: 72 + 152 + 208 + 80 = 4 x 128.
+  if (warp < 4) {
+    regs_lower<72>();
+    if (warp == 0) {
+      // ================================================================== q and keys
+      // one thread issues two boxes per slot; pages smaller than 64 rows: lane i issues box i.
+      // Every slot takes the same bytes from both CTAs.
+      const int kbox = kSub ? a.k_box : 64;
+      const int nk = 128 / kbox;                          // boxes of a key slot
       const bool el = elect_one();
-      constexpr uint32_t idesc = make_idesc(128, 256, FP8 ? 0u : 1u, 0, 0);
-      // Q chunk c (64 columns): [64 rows][128 B] at 8 KB c; E4M3: hi and lo are the first and
-      // second 512 bytes of each 1 KB group of 8 rows, 64-byte rows
-      const uint64_t dQ0 = make_sdesc(sQ, 16, 1024, FP8 ? kSwizzle64 : kSwizzle128);
-      const uint64_t dK0 = make_sdesc(sK, 16, 1024, kSwizzle128);          // [128 keys][128 B]
-      uint32_t slot = 0, ph = 0, n = 0, uc = 0;
+      uint32_t slot = 0, ph = 1, uq = 0;
       bool ok = true;
+      auto load = [&](uint32_t dst, uint32_t bar, int row, int c) {
+        if (FP8) tma_load_2d_pair(dst, &a.tm_k, bar, 128 * c, row);
+        else tma_load_3d_pair(dst, &a.tm_k, bar, 0, row, c);
+      };
+      const uint32_t lb = lead(b_kfull);
       for (int u = u0; u < u1 && ok; ++u) {
         const CUnit U = load_cunit(a, u);
         if (U.te == U.tb) continue;
-        ok = wait_warp(b_qfull, uc & 1);
-        for (int tile = U.tb; tile < U.te && ok; ++tile, ++n) {
-          const uint32_t d = tmem + (n & 1) * 128;
-          ok = wait_warp(b_sempty + 8 * (n & 1), ((n >> 1) & 1) ^ 1);
-          for (int c = 0; c < KS && ok; ++c) {
-            ok = wait_warp(b_kfull + 8 * slot, ph);
+        int rows = tile_row(a, U, U.tb, lane);
+        ok = wait_warp(b_qempty, (uq & 1) ^ 1);
+        if (!ok) break;
+        if (el) {
+          const int32_t q0 = U.row0 + 64 * (int)rank;
+          if (FP8) {
+            mbar_arrive_expect_tx(b_qraw, kCQBytes);
+            tma_load_3d(sQ, &a.tm_q, b_qraw, 0, q0, 0);
+          } else {
+            if (leader) mbar_arrive_expect_tx(b_qfull, 2 * kCQBytes);
+            tma_load_3d_pair(sQ, &a.tm_q, lead(b_qfull), 0, q0, 0);
+          }
+        }
+        ++uq;
+        for (int tile = U.tb; tile < U.te; ++tile) {
+          // the next tile's page numbers are on their way while this tile's keys are issued
+          const int next_rows = tile + 1 < U.te ? tile_row(a, U, tile + 1, lane) : 0;
+          const int r0 = __shfl_sync(0xffffffffu, rows, 16 * (int)rank), r1 = __shfl_sync(0xffffffffu, rows, 16 * (int)rank + 8);
+          const int row = __shfl_sync(0xffffffffu, rows, 16 * (int)rank + (lane < nk ? lane * (kbox >> 3) : 0));
+          for (int c = 0; c < KS; ++c) {
+            ok = wait_warp(b_kempty + 8 * slot, ph);
             if (!ok) break;
-            tc_fence_after();
-            const uint64_t kd = dK0 + (uint64_t)(slot * (kCSlot >> 4));
-            if (!el) {
-            } else if constexpr (FP8) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) {
-                if (c == KS - 1 && kk >= 2) break;       // the row's last 64 bytes
-                const uint64_t qd = dQ0 + (uint64_t)((2 * c + (kk >> 1)) * (kCQChunk >> 4) + (kk & 1) * 2);
-                umma_pair_f8(d, qd, kd + 2 * kk, idesc, (c | kk) != 0);
-                umma_pair_f8(d, qd + (512 >> 4), kd + 2 * kk, idesc, 1u);
+            const uint32_t dst = sK + slot * kCSlot, bar = lb + 8 * slot;
+            if (el) {
+              if (leader) mbar_arrive_expect_tx(b_kfull + 8 * slot, 2 * kCSlot);
+              if (!kSub) {
+                load(dst, bar, r0, c);
+                load(dst + kCSlot / 2, bar, r1, c);
               }
-            } else {
-              const uint64_t qd = dQ0 + (uint64_t)(c * (kCQChunk >> 4));
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk) umma_pair_f16(d, qd + 2 * kk, kd + 2 * kk, idesc, (c | kk) != 0);
             }
-            if (el) umma_pair_commit(b_kempty + 8 * slot);
+            if (kSub && lane < nk) load(dst + (uint32_t)(lane * kbox) * 128u, bar, row, c);
             if (++slot == kKRing) {
               slot = 0;
               ph ^= 1;
             }
           }
           if (!ok) break;
-          if (el) {
-            umma_pair_commit(b_sfull + 8 * (n & 1));
-            if (tile == U.te - 1) umma_pair_commit(b_qempty);
-          }
+          rows = next_rows;
         }
-        ++uc;
       }
-      // every MMA issued has completed before tensor memory is released
-      if (el) umma_pair_commit(b_drain);
-      volatile uint32_t no_abort = 0;
-      mbar_wait(b_drain, 0, &no_abort, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns);
-    }
-  } else if (warp == 3) {
-    // ================================================================== PV (even CTA)
-    if (leader) {
+      // after an abort the odd CTA cannot observe its own loads (they count on the even CTA's
+      // barriers): the producers wait 50 us, far longer than a load takes, before leaving
+      if (*abort_flag) {
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 50000ull) {
+        }
+      }
+    } else if (warp == 2) {
+      // ================================================================== values
+      const int vbox = kSub ? a.v_box : VK;
+      const int nvr = VK / vbox;                          // boxes down a value slot
+      const int nv = nvr * VC;
       const bool el = elect_one();
-      constexpr uint32_t idesc = make_idesc(128, 256, FP8 ? 0u : 1u, 0, 1);
-      const uint64_t dP0 = make_sdesc(sP, 16, 1024, kSwizzle128);          // [key chunk][64 rows][128 B]
-      const uint64_t dV0 = make_sdesc(sV, VK * 128, 1024, kSwizzle128);    // [VC pieces][VK keys][128 B], MN-major
-      uint32_t slot = 0, ph = 0, n = 0, uc = 0;
+      uint32_t slot = 0, ph = 1;
       bool ok = true;
+      const uint32_t lb = lead(b_vfull);
+      // a slot with a key that some row does not see is loaded on a barrier of this CTA; the
+      // fixing warps then count its bytes
+      auto load = [&](uint32_t dst, bool fix, int row, int col) {   // col: 128-byte piece of the row
+        if (fix) {
+          if (FP8) tma_load_2d(dst, &a.tm_v, b_aux + 8 * slot, 128 * col, row);
+          else tma_load_3d(dst, &a.tm_v, b_aux + 8 * slot, 0, row, col);
+        } else {
+          if (FP8) tma_load_2d_pair(dst, &a.tm_v, lb + 8 * slot, 128 * col, row);
+          else tma_load_3d_pair(dst, &a.tm_v, lb + 8 * slot, 0, row, col);
+        }
+      };
+      const int c0 = VC * (int)rank;
       for (int u = u0; u < u1 && ok; ++u) {
         const CUnit U = load_cunit(a, u);
         if (U.te == U.tb) continue;
-        for (int tile = U.tb; tile < U.te && ok; ++tile, ++n) {
-          ok = wait_warp(b_p, n & 1);
-          if (ok && tile == U.tb) ok = wait_warp(b_oempty, (uc & 1) ^ 1);
-          const int ns = value_slots<VK>(U.hi, tile);
-          for (int s = 0; s < ns && ok; ++s) {
-            ok = wait_warp(b_vfull + 8 * slot, ph);
+        int rows = tile_row(a, U, U.tb, lane);
+        for (int tile = U.tb; tile < U.te; ++tile) {
+          const int next_rows = tile + 1 < U.te ? tile_row(a, U, tile + 1, lane) : 0;
+          const int n = value_slots<VK>(U.hi, tile);
+          int key = tile * kChunkTile;
+          const int i = lane % nvr, c = lane / nvr;       // kSub: this lane's box i of piece c
+          for (int s = 0; s < n; ++s) {
+            const int r0 = __shfl_sync(0xffffffffu, rows, s * VK >> 3);
+            const int row = kSub ? __shfl_sync(0xffffffffu, rows, (s * VK + (lane < nv ? i * vbox : 0)) >> 3) : 0;
+            key += VK;
+            const bool fix = key > U.lo;
+            ok = wait_warp(b_vempty + 8 * slot, ph);
             if (!ok) break;
-            tc_fence_after();
-            const uint64_t vd = dV0 + (uint64_t)(slot * (kCSlot >> 4));
-            // keys VK s ..: half s & 1 of a 128-byte chunk of P's columns; E4M3: lo 16 KB after hi
-            const uint64_t pd = dP0 + (uint64_t)((s >> 1) * (8192 >> 4) + (s & 1) * 4);
-            const bool first = tile == U.tb && s == 0;
+            const uint32_t dst = sV + slot * kCSlot;
             if (el) {
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                  const uint64_t vk = vd + (uint64_t)((j * 8192 + kk * (FP8 ? 4096 : 2048)) >> 4);
-                  const uint32_t acc = !(first && kk == 0);
-                  if constexpr (FP8) {
-                    umma_pair_f8(tmem + kCOCol + 128 * j, pd + 2 * kk, vk, idesc, acc);
-                    umma_pair_f8(tmem + kCOCol + 128 * j, pd + 2 * kk + (16384 >> 4), vk, idesc, 1u);
-                  } else {
-                    umma_pair_f16(tmem + kCOCol + 128 * j, pd + 2 * kk, vk, idesc, acc);
-                  }
-                }
-              umma_pair_commit(b_vempty + 8 * slot);
+              if (leader) mbar_arrive_expect_tx(b_vfull + 8 * slot, 2 * kCSlot);
+              if (fix) mbar_arrive_expect_tx(b_aux + 8 * slot, kCSlot);
+              if (!kSub) {
+                load(dst, fix, r0, c0);                            // bf16: four pieces in one box
+                if (FP8) load(dst + kCSlot / 2, fix, r0, c0 + 1);
+              }
+            }
+            if (kSub) {
+              __syncwarp();
+              if (lane < nv) load(dst + (uint32_t)(c * VK + i * vbox) * 128u, fix, row, c0 + c);
             }
             if (++slot == kVRing) {
               slot = 0;
               ph ^= 1;
             }
           }
-          if (ok && el) umma_pair_commit(b_pv);
+          if (!ok) break;
+          rows = next_rows;
         }
-        ++uc;
       }
-      if (el) umma_pair_commit(b_drain);
-      volatile uint32_t no_abort = 0;
-      mbar_wait(b_drain, 0, &no_abort, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns);
-    }
-  } else if (warp >= 12) {
-    // ================================================================== q terms, value fixes
-    constexpr uint32_t cbar = 3;
-    const int t = threadIdx.x - 384;
-    uint32_t rv = 0, uq = 0, aux_phase = 0;    // value slots so far; a phase bit per slot
-    bool ok = true;
-    for (int u = u0; u < u1 && ok; ++u) {
-      const CUnit U = load_cunit(a, u);
-      const int T = U.te - U.tb;
-      if (T == 0) continue;
-      if constexpr (FP8) {
-        // The 64 rows of this CTA, bf16 as TMA landed them, become q' = q 2^e (the row's largest
-        // |q| in [128, 256)) as E4M3 hi and lo in place: every 1 KB group of 8 rows x 64 columns
-        // becomes hi in its first 512 bytes and lo in its second (64-byte swizzled rows). A warp
-        // owns whole groups; lane 4 q + p holds 16-byte units p and p + 4 of row q.
-        bool mine = wait(b_qraw, uq & 1);
-        if (mine && uq > 0) mine = wait(b_qfree, (uq - 1) & 1);   // the previous factors were read
-        if (named_bar_or(cbar, 64, !mine)) { ok = false; break; }
-        const int qrow = lane >> 2, part = lane & 3;
-        for (int g = warp - 12; g < 8; g += 2) {
-          auto block_of = [&](int c) -> uint8_t* { return gQ + c * kCQChunk + g * 1024; };
-          __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
-#pragma unroll
-          for (int c = 0; c < 9; ++c)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint4 v = *reinterpret_cast<const uint4*>(block_of(c) + qrow * 128 + (((part + 4 * h) ^ qrow) << 4));
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) m2 = __hmax2(m2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[k])));
-            }
-          float mx = fmaxf(__low2float(m2), __high2float(m2));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          int e = 0;
-          if (mx > 0.f) e = min(max(7 - ((int)((__float_as_uint(mx) >> 23) & 0xFFu) - 127), -126), 126);
-          const float f = __uint_as_float((uint32_t)(e + 127) << 23);
-#pragma unroll 3
-          for (int c = 0; c < 9; ++c) {
-            uint8_t* blk = block_of(c);
-            uint4 v[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              v[h] = *reinterpret_cast<const uint4*>(blk + qrow * 128 + (((part + 4 * h) ^ qrow) << 4));
-            __syncwarp();
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int un = part + 4 * h;           // columns 8 un .. of the chunk
-              const uint32_t w[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
-              uint32_t o[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) o[k] = split_e4m3x2(bf_lo(w[k]) * f, bf_hi(w[k]) * f);
-              const uint32_t off = qrow * 64 + (((un >> 1) ^ ((qrow >> 1) & 3)) << 4) + (un & 1) * 8;
-              *reinterpret_cast<uint2*>(blk + off) = make_uint2(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410));
-              *reinterpret_cast<uint2*>(blk + 512 + off) =
-                  make_uint2(__byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632));
-            }
-          }
-          if (part == 0) qf_s[8 * g + qrow] = __uint_as_float((uint32_t)(127 - e) << 23);
+      if (*abort_flag) {
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 50000ull) {
         }
-        fence_proxy_async_smem();
-        named_bar_sync(cbar, 64);
-        if (t == 0) {
-          mbar_arrive(b_qsc);
-          // the issuer needs both CTAs' terms: the odd CTA signals by st.async
-          if (leader) mbar_arrive_expect_tx(b_qfull, 16);
-          else st_async_v4(lead(smem_u32(sig_s)), make_uint4(0u, 0u, 0u, 0u), lead(b_qfull));
-        }
-        ++uq;
       }
-      // value slots with a key that some row of the block does not see (the last one or two
-      // tiles of a block)
-      for (int k = 0; k < T; ++k) {
-        const int tile = U.tb + k;
-        const int ns = value_slots<VK>(U.hi, tile);
-        for (int s = 0; s < ns && ok; ++s) {
-          const int key0 = tile * kChunkTile + s * VK;
-          if (key0 + VK <= U.lo) continue;
-          const uint32_t slot = (rv + s) % kVRing;
-          const bool mine = wait(b_aux + 8 * slot, (aux_phase >> slot) & 1);
-          aux_phase ^= 1u << slot;
-          if (named_bar_or(cbar, 64, !mine)) { ok = false; break; }
-          uint8_t* g = gV + slot * kCSlot;
-          for (int idx = t; idx < kCSlot / 16; idx += 64) {
-            const int row = (idx >> 3) % VK;
-            const int key = key0 + row;
-            if (key < U.lo) continue;
-            uint4* p = reinterpret_cast<uint4*>(g + idx * 16);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (key < U.hi) {
-              v = *p;
-              v.x = finite_word<FP8>(v.x);
-              v.y = finite_word<FP8>(v.y);
-              v.z = finite_word<FP8>(v.z);
-              v.w = finite_word<FP8>(v.w);
+    } else if (warp == 1) {
+      // ================================================================== QK^T (even CTA)
+      if (leader) {
+        const bool el = elect_one();
+        constexpr uint32_t idesc = make_idesc(128, 256, FP8 ? 0u : 1u, 0, 0);
+        // Q chunk c (64 columns): [64 rows][128 B] at 8 KB c; E4M3: hi and lo are the first and
+        // second 512 bytes of each 1 KB group of 8 rows, 64-byte rows
+        const uint64_t dQ0 = make_sdesc(sQ, 16, 1024, FP8 ? kSwizzle64 : kSwizzle128);
+        const uint64_t dK0 = make_sdesc(sK, 16, 1024, kSwizzle128);          // [128 keys][128 B]
+        uint32_t slot = 0, ph = 0, n = 0, uc = 0;
+        bool ok = true;
+        for (int u = u0; u < u1 && ok; ++u) {
+          const CUnit U = load_cunit(a, u);
+          if (U.te == U.tb) continue;
+          ok = wait_warp(b_qfull, uc & 1);
+          for (int tile = U.tb; tile < U.te && ok; ++tile, ++n) {
+            const uint32_t d = tmem + (n & 1) * 128;
+            ok = wait_warp(b_sempty + 8 * (n & 1), ((n >> 1) & 1) ^ 1);
+            for (int c = 0; c < KS && ok; ++c) {
+              ok = wait_warp(b_kfull + 8 * slot, ph);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t kd = dK0 + (uint64_t)(slot * (kCSlot >> 4));
+              if (!el) {
+              } else if constexpr (FP8) {
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                  if (c == KS - 1 && kk >= 2) break;       // the row's last 64 bytes
+                  const uint64_t qd = dQ0 + (uint64_t)((2 * c + (kk >> 1)) * (kCQChunk >> 4) + (kk & 1) * 2);
+                  umma_pair_f8(d, qd, kd + 2 * kk, idesc, (c | kk) != 0);
+                  umma_pair_f8(d, qd + (512 >> 4), kd + 2 * kk, idesc, 1u);
+                }
+              } else {
+                const uint64_t qd = dQ0 + (uint64_t)(c * (kCQChunk >> 4));
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) umma_pair_f16(d, qd + 2 * kk, kd + 2 * kk, idesc, (c | kk) != 0);
+              }
+              if (el) umma_pair_commit(b_kempty + 8 * slot);
+              if (++slot == kKRing) {
+                slot = 0;
+                ph ^= 1;
+              }
             }
-            *p = v;
+            if (!ok) break;
+            if (el) {
+              umma_pair_commit(b_sfull + 8 * (n & 1));
+              if (tile == U.te - 1) umma_pair_commit(b_qempty);
+            }
           }
-          fence_proxy_async_smem();
-          named_bar_sync(cbar, 64);
-          if (t == 0) {
-            fence_acq_rel_cluster();
-            mbar_complete_tx_cluster(lead(b_vfull + 8 * slot), kCSlot);   // this CTA's share is in place
-          }
+          ++uc;
         }
-        rv += ns;
-        if (!ok) break;
+        // every MMA issued has completed before tensor memory is released
+        if (el) umma_pair_commit(b_drain);
+        volatile uint32_t no_abort = 0;
+        mbar_wait(b_drain, 0, &no_abort, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns);
+      }
+    } else if (warp == 3) {
+      // ================================================================== PV (even CTA)
+      if (leader) {
+        const bool el = elect_one();
+        constexpr uint32_t idesc = make_idesc(128, 256, FP8 ? 0u : 1u, 0, 1);
+        const uint64_t dP0 = make_sdesc(sP, 16, 1024, kSwizzle128);          // [key chunk][64 rows][128 B]
+        const uint64_t dV0 = make_sdesc(sV, VK * 128, 1024, kSwizzle128);    // [VC pieces][VK keys][128 B], MN-major
+        constexpr int kHalfSlots = kChunkTile / VK / 2;
+        uint32_t slot = 0, ph = 0, n = 0, uc = 0;
+        bool ok = true;
+        for (int u = u0; u < u1 && ok; ++u) {
+          const CUnit U = load_cunit(a, u);
+          if (U.te == U.tb) continue;
+          for (int tile = U.tb; tile < U.te && ok; ++tile, ++n) {
+            const int ns = value_slots<VK>(U.hi, tile);
+            if (tile == U.tb) ok = wait_warp(b_oempty, (uc & 1) ^ 1);
+            // by halves of the tile's keys, whose P is written and released apart: the way from one
+            // PV over its completion, the next P and the signal back is hidden by the other half
+            for (int s = 0; s < kHalfSlots * 2 && ok; ++s) {
+              if (s % kHalfSlots == 0) {
+                ok = wait_warp(b_p + 8 * (s / kHalfSlots), n & 1);
+                if (!ok) break;
+              }
+              if (s < ns) {
+                ok = wait_warp(b_vfull + 8 * slot, ph);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t vd = dV0 + (uint64_t)(slot * (kCSlot >> 4));
+                // keys VK s ..: half s & 1 of a 128-byte chunk of P's columns; E4M3: lo 16 KB after hi
+                const uint64_t pd = dP0 + (uint64_t)((s >> 1) * (8192 >> 4) + (s & 1) * 4);
+                const bool first = tile == U.tb && s == 0;
+                if (el) {
+#pragma unroll
+                  for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) {
+                      const uint64_t vk = vd + (uint64_t)((j * 8192 + kk * (FP8 ? 4096 : 2048)) >> 4);
+                      const uint32_t acc = !(first && kk == 0);
+                      if constexpr (FP8) {
+                        umma_pair_f8(tmem + kCOCol + 128 * j, pd + 2 * kk, vk, idesc, acc);
+                        umma_pair_f8(tmem + kCOCol + 128 * j, pd + 2 * kk + (16384 >> 4), vk, idesc, 1u);
+                      } else {
+                        umma_pair_f16(tmem + kCOCol + 128 * j, pd + 2 * kk, vk, idesc, acc);
+                      }
+                    }
+                  umma_pair_commit(b_vempty + 8 * slot);
+                }
+                if (++slot == kVRing) {
+                  slot = 0;
+                  ph ^= 1;
+                }
+              }
+              if (s % kHalfSlots == kHalfSlots - 1 && el) umma_pair_commit(b_pv + 8 * (s / kHalfSlots));
+            }
+          }
+          ++uc;
+        }
+        if (el) umma_pair_commit(b_drain);
+        volatile uint32_t no_abort = 0;
+        mbar_wait(b_drain, 0, &no_abort, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns);
       }
     }
   } else if (warp < 8) {
+    regs_raise<152>();
     // ================================================================== softmax
     constexpr uint32_t sbar = 1;
     const int t = threadIdx.x - 128;           // tensor-memory lane
@@ -690,9 +600,15 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
             }
           }
         }
-        // S has been read (every thread's part, at the barrier below): its buffer is released with P
-        // P and O are free once the previous PV has completed
-        if (n > 0) fail |= !wait(b_pv, (n - 1) & 1);
+        // S has been read: its buffer is free (nothing this thread wrote is published with it)
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(lead(b_sempty + 8 * (n & 1)));
+        // this half of P is free once the previous tile's PV over it has completed, O once all of it
+        if (n > 0) {
+          fail |= !wait(b_pv + 8 * half, (n - 1) & 1);
+          if (rescale) fail |= !wait(b_pv + 8 * (half ^ 1), (n - 1) & 1);
+        }
         if (rescale) {
           tc_fence_after();
 #pragma unroll 1
@@ -706,6 +622,8 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
             tmem_st16(ta, o);
           }
           tmem_wait_st();
+          tc_fence_before();
+          named_bar_sync(sbar, 128);             // all of O, before either half of P is announced
         }
         // bf16: key chunks 2 half and 2 half + 1 (64 keys each); E4M3: chunk `half`, lo 16 KB on
 #pragma unroll
@@ -718,15 +636,11 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        if (named_bar_or(sbar, 128, fail)) { stop = true; break; }
-        if (t == 0) {
-          if (leader) {
-            mbar_arrive(b_p);
-            mbar_arrive(b_sempty + 8 * (n & 1));
-          } else {
-            mbar_arrive_cluster(lead(b_p));
-            mbar_arrive_cluster(lead(b_sempty + 8 * (n & 1)));
-          }
+        // a failed wait is carried to the next barrier of all 128 threads
+        fail |= named_bar_or(4 + half, 64, fail);
+        if (!fail && (t & 63) == 0) {
+          if (leader) mbar_arrive(b_p + 8 * half);
+          else mbar_arrive_cluster(lead(b_p + 8 * half));
         }
       }
       if (stop) break;
@@ -739,6 +653,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
       if (T > 0) ++uc;
     }
   } else if (warp < 12) {
+    regs_raise<208>();
     // ================================================================== epilogue
     constexpr uint32_t ebar = 2;
     const int t = threadIdx.x - 256;
@@ -755,56 +670,183 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
       const float ref = ref_s[t], sum = sum_s[t] + sum_s[t ^ 64];
       mbar_arrive(b_statfree);
       ++us;
-      if (T > 0) fail |= !wait(b_pv, (n - 1) & 1);
+      if (T > 0) fail |= !wait(b_pv + 8, (n - 1) & 1);
       if (named_bar_or(ebar, 128, fail)) break;
       tc_fence_after();
       const int br = 64 * (int)rank + row;
       const bool keep = br < U.nrows;
       const float inv = sum == 0.f ? 0.f : kvs / sum;          // a row that sees no key: zeros
       const int64_t orow = (int64_t)U.row0 + br;
-#pragma unroll 1
-      for (int i = 0; i < 8; ++i) {
-        float o[32];
+      auto load_o = [&](int i, float* o) {       // 32 columns, normalised
         if (T > 0) {
           tmem_ld32(tmem + lane_addr + kCOCol + 32 * i, o);
           tmem_wait_ld();
         }
 #pragma unroll
         for (int x = 0; x < 32; ++x) o[x] = sum == 0.f ? 0.f : o[x] * inv;
-        const int col = 256 * half + 32 * i;
-        if (keep && U.slot < 0) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + orow * kDV + col);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t w[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              __nv_bfloat162 h = __floats2bfloat162_rn(o[8 * x + 2 * y], o[8 * x + 2 * y + 1]);
-              w[y] = *reinterpret_cast<uint32_t*>(&h);
-            }
-            dst[x] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        } else if (keep) {
-          float4* dst = reinterpret_cast<float4*>(a.part_o + ((int64_t)U.slot * kChunkRows + br) * kDV + col);
-#pragma unroll
-          for (int x = 0; x < 8; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-        }
-        __syncwarp();
-      }
-      if (T > 0) {
-        // O has been read: the next unit's first PV may overwrite it
+      };
+      // O has been read: the next unit's first PV may overwrite it
+      auto release_o = [&]() {
+        if (T == 0) return;
         tc_fence_before();
         named_bar_sync(ebar, 128);
         if (t == 0) {
           if (leader) mbar_arrive(b_oempty);
-          else mbar_arrive_cluster(lead(b_oempty));
+          else mbar_arrive_cluster_relaxed(lead(b_oempty));
         }
+      };
+      if (U.slot < 0) {
+        // all of the thread's columns into registers as bf16 first, so that the next unit's PV
+        // waits for the reads and not for the stores
+        uint32_t w[128];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float o[32];
+          load_o(i, o);
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * x], o[2 * x + 1]);
+            w[16 * i + x] = *reinterpret_cast<uint32_t*>(&h);
+          }
+        }
+        release_o();
+        if (keep) {
+          __nv_bfloat16* dst = a.out + orow * kDV + 256 * half;
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            reinterpret_cast<uint4*>(dst)[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {
+          float o[32];
+          load_o(i, o);
+          if (keep) {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + ((int64_t)U.slot * kChunkRows + br) * kDV + 256 * half + 32 * i);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          }
+          __syncwarp();
+        }
+        release_o();
       }
       if (half == 0 && keep) {
         // P was computed times 2^kPOffLog2, and so was the row sum
         const float l = sum == 0.f ? -INFINITY : (ref + log2f(sum) - Cfg::kPOffLog2) * kCLn2;
         if (U.slot < 0) a.lse[orow] = l;
         else a.part_lse[(int64_t)U.slot * kChunkRows + br] = l;
+      }
+    }
+  } else {
+    regs_lower<80>();
+    if (warp < 14) {
+      // ================================================================== q terms, value fixes
+      constexpr uint32_t cbar = 3;
+      const int t = threadIdx.x - 384;
+      uint32_t rv = 0, uq = 0, aux_phase = 0;    // value slots so far; a phase bit per slot
+      bool ok = true;
+      for (int u = u0; u < u1 && ok; ++u) {
+        const CUnit U = load_cunit(a, u);
+        const int T = U.te - U.tb;
+        if (T == 0) continue;
+        if constexpr (FP8) {
+          // The 64 rows of this CTA, bf16 as TMA landed them, become q' = q 2^e (the row's largest
+          // |q| in [128, 256)) as E4M3 hi and lo in place: every 1 KB group of 8 rows x 64 columns
+          // becomes hi in its first 512 bytes and lo in its second (64-byte swizzled rows). A warp
+          // owns whole groups; lane 4 q + p holds 16-byte units p and p + 4 of row q.
+          bool mine = wait(b_qraw, uq & 1);
+          if (mine && uq > 0) mine = wait(b_qfree, (uq - 1) & 1);   // the previous factors were read
+          if (named_bar_or(cbar, 64, !mine)) { ok = false; break; }
+          const int qrow = lane >> 2, part = lane & 3;
+          for (int g = warp - 12; g < 8; g += 2) {
+            auto block_of = [&](int c) -> uint8_t* { return gQ + c * kCQChunk + g * 1024; };
+            __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
+#pragma unroll
+            for (int c = 0; c < 9; ++c)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint4 v = *reinterpret_cast<const uint4*>(block_of(c) + qrow * 128 + (((part + 4 * h) ^ qrow) << 4));
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) m2 = __hmax2(m2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[k])));
+              }
+            float mx = fmaxf(__low2float(m2), __high2float(m2));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            int e = 0;
+            if (mx > 0.f) e = min(max(7 - ((int)((__float_as_uint(mx) >> 23) & 0xFFu) - 127), -126), 126);
+            const float f = __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll 3
+            for (int c = 0; c < 9; ++c) {
+              uint8_t* blk = block_of(c);
+              uint4 v[2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                v[h] = *reinterpret_cast<const uint4*>(blk + qrow * 128 + (((part + 4 * h) ^ qrow) << 4));
+              __syncwarp();
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int un = part + 4 * h;           // columns 8 un .. of the chunk
+                const uint32_t w[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[k] = split_e4m3x2(bf_lo(w[k]) * f, bf_hi(w[k]) * f);
+                const uint32_t off = qrow * 64 + (((un >> 1) ^ ((qrow >> 1) & 3)) << 4) + (un & 1) * 8;
+                *reinterpret_cast<uint2*>(blk + off) = make_uint2(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410));
+                *reinterpret_cast<uint2*>(blk + 512 + off) =
+                    make_uint2(__byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632));
+              }
+            }
+            if (part == 0) qf_s[8 * g + qrow] = __uint_as_float((uint32_t)(127 - e) << 23);
+          }
+          fence_proxy_async_smem();
+          named_bar_sync(cbar, 64);
+          if (t == 0) {
+            mbar_arrive(b_qsc);
+            // the issuer needs both CTAs' terms: the odd CTA signals by st.async
+            if (leader) mbar_arrive_expect_tx(b_qfull, 16);
+            else st_async_v4(lead(smem_u32(sig_s)), make_uint4(0u, 0u, 0u, 0u), lead(b_qfull));
+          }
+          ++uq;
+        }
+        // value slots with a key that some row of the block does not see (the last one or two
+        // tiles of a block)
+        for (int k = 0; k < T; ++k) {
+          const int tile = U.tb + k;
+          const int ns = value_slots<VK>(U.hi, tile);
+          for (int s = 0; s < ns && ok; ++s) {
+            const int key0 = tile * kChunkTile + s * VK;
+            if (key0 + VK <= U.lo) continue;
+            const uint32_t slot = (rv + s) % kVRing;
+            const bool mine = wait(b_aux + 8 * slot, (aux_phase >> slot) & 1);
+            aux_phase ^= 1u << slot;
+            if (named_bar_or(cbar, 64, !mine)) { ok = false; break; }
+            uint8_t* g = gV + slot * kCSlot;
+            for (int idx = t; idx < kCSlot / 16; idx += 64) {
+              const int row = (idx >> 3) % VK;
+              const int key = key0 + row;
+              if (key < U.lo) continue;
+              uint4* p = reinterpret_cast<uint4*>(g + idx * 16);
+              uint4 v = make_uint4(0, 0, 0, 0);
+              if (key < U.hi) {
+                v = *p;
+                v.x = finite_word<FP8>(v.x);
+                v.y = finite_word<FP8>(v.y);
+                v.z = finite_word<FP8>(v.z);
+                v.w = finite_word<FP8>(v.w);
+              }
+              *p = v;
+            }
+            fence_proxy_async_smem();
+            named_bar_sync(cbar, 64);
+            if (t == 0) {
+              fence_acq_rel_cluster();
+              mbar_complete_tx_cluster(lead(b_vfull + 8 * slot), kCSlot);   // this CTA's share is in place
+            }
+          }
+          rv += ns;
+          if (!ok) break;
+        }
       }
     }
   }
