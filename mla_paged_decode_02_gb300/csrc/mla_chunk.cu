@@ -13,8 +13,8 @@
 //   QK^T  N = 256 keys of a tile: CTA k holds keys 128 k .. as B;
 //   PV    N = 256 value columns, twice (j = 0, 1): CTA k holds columns 256 k + 128 j .. as B.
 // An SM's accumulator rows then hold, in tensor-memory lane l, row l % 64: N columns 0..127 in
-// lanes 0..63 and 128..255 in lanes 64..127. So a thread owns one row and half of its keys, the
-// softmax stays inside the CTA (two threads compare maxima), and P needs no exchange.
+// lanes 0..63 and 128..255 in lanes 64..127. So a thread owns a quarter of the keys of one row, the
+// softmax stays inside the CTA (four threads compare maxima), and P needs no exchange.
 // Tensor memory per CTA: S 2 x 128 columns, O 2 x 128.
 //
 // Shared memory per CTA: 64 query rows (72 KB), P (64 rows x 256 keys, 32 KB), a ring of four
@@ -39,8 +39,8 @@
 // the key weight 0). Boxes past the last key start at the end of the pool, so TMA fills zeros.
 //
 // Roles (512 threads): warp 0 loads q and keys, warp 2 values; warps 1 and 3 of the even CTA issue
-// QK^T and PV; warps 4-7 softmax; warps 8-11 epilogue; warps 12-13 value fixes and (E4M3) the
-// split of q (14-15 idle). Every wait is bounded; a stall sets the device error word, and both CTAs drain and
+// QK^T and PV; warps 4-11 softmax, four threads to a row; warps 12-15 value fixes, (E4M3) the split
+// of q, and the epilogue. Every wait is bounded; a stall sets the device error word, and both CTAs drain and
 // leave through a cluster barrier.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -160,6 +160,35 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
+__device__ __forceinline__ float max64(const float* s) {
+  float m[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+  for (int i = 4; i < 64; i += 8)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = i + 4 + j < 64 ? fmaxf(m[j], fmaxf(s[i + j], s[i + 4 + j])) : fmaxf(m[j], s[i + j]);
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+// (x, y) * c + d and pairwise sums, two values per instruction
+__device__ __forceinline__ void fma2(float& x, float& y, float c, float d) {
+  asm("{\n\t.reg .b64 v, w, z;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+      "fma.rn.f32x2 v, v, w, z;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y) : "f"(c), "f"(d));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+  asm("{\n\t.reg .b64 v, w;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 w, {%2, %3};\n\t"
+      "add.rn.f32x2 v, v, w;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y) : "f"(a), "f"(b));
+}
+__device__ __forceinline__ float sum32(const float* s) {
+  float a[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+  for (int i = 4; i < 32; i += 4) {
+    add2(a[0], a[1], s[i], s[i + 1]);
+    add2(a[2], a[3], s[i + 2], s[i + 3]);
+  }
+  return (a[0] + a[1]) + (a[2] + a[3]);
+}
+
 // 32 lanes x 32 consecutive 32-bit columns
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   tmem_ld16(taddr, v);
@@ -179,7 +208,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
   __shared__ __align__(16) uint32_t sig_s[4];
   __shared__ uint32_t tmem_base_s, abort_s;
   __shared__ float qf_s[64];                 // E4M3: 2^-e of this CTA's rows
-  __shared__ float mx_s[128], sum_s[128], ref_s[128];
+  __shared__ float mx_s[256], sum_s[256], ref_s[128];
 
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -222,12 +251,12 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
     mbar_init(b_qfree, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_sfull + 8 * i, 1);
-      mbar_init(b_sempty + 8 * i, 8);     // both CTAs' softmax warps
+      mbar_init(b_sempty + 8 * i, 16);     // both CTAs' softmax warps
       mbar_init(b_p + 8 * i, 2);          // half i of P's keys: both CTAs' softmax
       mbar_init(b_pv + 8 * i, 1);
     }
     mbar_init(b_oempty, 2);               // both CTAs' epilogue
-    mbar_init(b_stat, 128);
+    mbar_init(b_stat, 256);
     mbar_init(b_statfree, 128);
     mbar_init(b_drain, 2);                // both issuers
     mbar_init(b_never, 1);
@@ -259,7 +288,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
   auto wait_warp = [&](uint32_t bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
 
   // The launch gives every thread 128 registers. The epilogue's threads hold 256 columns of a row
-  // as bf16, the softmax's 128 probabilities: 72 + 152 + 208 + 80 = 4 x 128.
+  // as bf16: 72 + 2 x 112 + 216 = 4 x 128.
   if (warp < 4) {
     regs_lower<72>();
     if (warp == 0) {
@@ -508,12 +537,12 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         mbar_wait(b_drain, 0, &no_abort, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns);
       }
     }
-  } else if (warp < 8) {
-    regs_raise<152>();
+  } else if (warp < 12) {
     // ================================================================== softmax
+    regs_lower<112>();
     constexpr uint32_t sbar = 1;
-    const int t = threadIdx.x - 128;           // tensor-memory lane
-    const int row = t & 63, half = t >> 6;     // row of this CTA, half of the tile's keys
+    const int t = threadIdx.x - 128;
+    const int row = t & 63, half = (t >> 6) & 1, quarter = t >> 7;   // row of this CTA; keys 128 half + 64 quarter ..
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const float c0 = a.softmax_scale * (FP8 ? __ldg(a.kv_scale) : 1.0f) * kCLog2e;
     uint32_t n = 0, uc = 0, us = 0;
@@ -528,7 +557,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
       if (FP8 && T > 0) {
         fail |= !wait(b_qsc, uc & 1);
         c *= qf_s[row];
-        if (named_bar_or(sbar, 128, fail)) break;
+        if (named_bar_or(sbar, 256, fail)) break;
         if (t == 0) mbar_arrive(b_qfree);
       }
       float ref = -INFINITY, sum = 0.f;
@@ -537,30 +566,34 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         if (a.test_stall && n == 0) fail |= !wait(b_never, 0);   // tests: this wait runs out
         fail |= !wait(b_sfull + 8 * (n & 1), (n >> 1) & 1);
         tc_fence_after();
-        const uint32_t ts = tmem + lane_addr + (n & 1) * 128;
-        const int mine = vis - tile * kChunkTile - 128 * half;   // keys of this thread its row sees
+        const uint32_t ts = tmem + lane_addr + (n & 1) * 128 + 64 * quarter;
+        const int mine = vis - tile * kChunkTile - 128 * half - 64 * quarter;   // keys of this thread its row sees
         // pass 1: the largest score
         float mx = -INFINITY;
+        {
+          float s[64];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float s[32];
-          tmem_ld32(ts + 32 * i, s);
+          for (int i = 0; i < 4; ++i) tmem_ld16(ts + 16 * i, s + 16 * i);
           tmem_wait_ld();
-          if (mine >= 32 * i + 32) {
+          if (mine < 64) {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) mx = fmaxf(mx, s[x] * c);
+            for (int x = 0; x < 64; ++x) s[x] = x < mine ? s[x] * c : -INFINITY;
+            mx = max64(s);
+          } else if (c >= 0.f) {
+            mx = max64(s) * c;
           } else {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) mx = fmaxf(mx, 32 * i + x < mine ? s[x] * c : -INFINITY);
+            for (int x = 0; x < 64; ++x) s[x] *= c;
+            mx = max64(s);
           }
         }
         float alpha = 1.f;
         bool rescale = false;
-        if (named_bar_or(sbar, 128, fail || mx > ref + Cfg::kRescaleLog2)) {
-          if (named_bar_or(sbar, 128, fail)) { stop = true; break; }
+        if (named_bar_or(sbar, 256, fail || mx > ref + Cfg::kRescaleLog2)) {
+          if (named_bar_or(sbar, 256, fail)) { stop = true; break; }
           mx_s[t] = mx;
-          named_bar_sync(sbar, 128);
-          const float nm = fmaxf(ref, fmaxf(mx, mx_s[t ^ 64]));
+          named_bar_sync(sbar, 256);
+          const float nm = fmaxf(fmaxf(ref, fmaxf(mx, mx_s[t ^ 64])), fmaxf(mx_s[t ^ 128], mx_s[t ^ 192]));
           alpha = nm == -INFINITY ? 1.f : ex2_approx(ref - nm);
           ref = nm;
           sum *= alpha;
@@ -568,29 +601,28 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         }
         // pass 2: P, packed
         const float off = (ref == -INFINITY ? 0.f : ref) - Cfg::kPOffLog2;
-        uint32_t pw[64];        // bf16: key pairs; E4M3: hi bytes (words 0-31), lo bytes (32-63)
+        uint32_t pw[32];        // bf16: key pairs; E4M3: hi bytes (words 0-15), lo bytes (16-31)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
           float s[32];
           tmem_ld32(ts + 32 * i, s);
           tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) fma2(s[x], s[x + 1], c, -off);
           if (mine >= 32 * i + 32) {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) s[x] = ex2_approx(fmaf(s[x], c, -off));
+            for (int x = 0; x < 32; ++x) s[x] = ex2_approx(s[x]);
           } else {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) s[x] = 32 * i + x < mine ? ex2_approx(fmaf(s[x], c, -off)) : 0.f;
+            for (int x = 0; x < 32; ++x) s[x] = 32 * i + x < mine ? ex2_approx(s[x]) : 0.f;
           }
-          float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int x = 0; x < 32; ++x) part[x & 3] += s[x];      // the normaliser sums the unrounded values
-          sum += (part[0] + part[1]) + (part[2] + part[3]);
+          sum += sum32(s);                               // the normaliser sums the unrounded values
           if constexpr (FP8) {
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
               const uint32_t o0 = split_e4m3x2(s[4 * x], s[4 * x + 1]), o1 = split_e4m3x2(s[4 * x + 2], s[4 * x + 3]);
               pw[8 * i + x] = __byte_perm(o0, o1, 0x5410);
-              pw[32 + 8 * i + x] = __byte_perm(o0, o1, 0x7632);
+              pw[16 + 8 * i + x] = __byte_perm(o0, o1, 0x7632);
             }
           } else {
 #pragma unroll
@@ -612,9 +644,9 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         if (rescale) {
           tc_fence_after();
 #pragma unroll 1
-          for (int cc = 0; cc < 16; ++cc) {
+          for (int cc = 0; cc < 8; ++cc) {
             float o[16];
-            const uint32_t ta = tmem + lane_addr + kCOCol + 16 * cc;
+            const uint32_t ta = tmem + lane_addr + kCOCol + 128 * quarter + 16 * cc;
             tmem_ld16(ta, o);
             tmem_wait_ld();
 #pragma unroll
@@ -623,51 +655,178 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
           }
           tmem_wait_st();
           tc_fence_before();
-          named_bar_sync(sbar, 128);             // all of O, before either half of P is announced
+          named_bar_sync(sbar, 256);             // all of O, before either half of P is announced
         }
-        // bf16: key chunks 2 half and 2 half + 1 (64 keys each); E4M3: chunk `half`, lo 16 KB on
+        if constexpr (FP8) {
+          // hi and lo (16 KB on): 64 bytes of the row of 128-key chunk `half`
+          uint8_t* p = gP + half * 8192 + (row >> 3) * 1024 + (row & 7) * 128;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint8_t* p = gP + (FP8 ? half * 8192 + h * 16384 : (2 * half + h) * 8192) + (row >> 3) * 1024 + (row & 7) * 128;
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              *reinterpret_cast<uint4*>(p + h * 16384 + (((4 * quarter + x) ^ (row & 7)) << 4)) =
+                  make_uint4(pw[16 * h + 4 * x], pw[16 * h + 4 * x + 1], pw[16 * h + 4 * x + 2], pw[16 * h + 4 * x + 3]);
+        } else {
+          // the row of 64-key chunk 2 half + quarter
+          uint8_t* p = gP + (2 * half + quarter) * 8192 + (row >> 3) * 1024 + (row & 7) * 128;
 #pragma unroll
           for (int x = 0; x < 8; ++x)
             *reinterpret_cast<uint4*>(p + ((x ^ (row & 7)) << 4)) =
-                make_uint4(pw[32 * h + 4 * x], pw[32 * h + 4 * x + 1], pw[32 * h + 4 * x + 2], pw[32 * h + 4 * x + 3]);
+                make_uint4(pw[4 * x], pw[4 * x + 1], pw[4 * x + 2], pw[4 * x + 3]);
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        // a failed wait is carried to the next barrier of all 128 threads
-        fail |= named_bar_or(4 + half, 64, fail);
-        if (!fail && (t & 63) == 0) {
+        // a failed wait is carried to the next barrier of all 256 threads
+        fail |= named_bar_or(4 + half, 128, fail);
+        if (!fail && (t & 191) == 0) {
           if (leader) mbar_arrive(b_p + 8 * half);
           else mbar_arrive_cluster(lead(b_p + 8 * half));
         }
       }
       if (stop) break;
-      // the row's reference and this half's sum, for the epilogue
+      // the row's reference and this thread's sum, for the epilogue
       if (us > 0) fail |= !wait(b_statfree, (us - 1) & 1);
       sum_s[t] = sum;
-      ref_s[t] = ref;
+      if (t < 128) ref_s[t] = ref;
       mbar_arrive(b_stat);
       ++us;
       if (T > 0) ++uc;
     }
-  } else if (warp < 12) {
-    regs_raise<208>();
-    // ================================================================== epilogue
+  } else {
+    // ================================================================== q terms, value fixes, epilogue
+    regs_raise<216>();
     constexpr uint32_t ebar = 2;
-    const int t = threadIdx.x - 256;
-    const int row = t & 63, half = t >> 6;     // this thread: value columns 256 half ..
+    const int t = threadIdx.x - 384;
+    const int row = t & 63, half = t >> 6;     // epilogue: this thread's row and value columns 256 half ..
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const float kvs = FP8 ? __ldg(a.kv_scale) : 1.0f;
+    uint32_t rv = 0, uq = 0, aux_phase = 0;    // value slots so far; units; a phase bit per slot
     uint32_t n = 0, us = 0;
     bool fail = false;
-    for (int u = u0; u < u1; ++u) {
+    // E4M3: the 64 rows of this CTA, bf16 as TMA landed them, become q' = q 2^e (the row's largest
+    // |q| in [128, 256)) as E4M3 hi and lo in place: every 1 KB group of 8 rows x 64 columns becomes
+    // hi in its first 512 bytes and lo in its second (64-byte swizzled rows). A warp owns whole
+    // groups; lane 4 q + p holds 16-byte units p and p + 4 of row q. False after a failed wait.
+    auto split_q = [&]() -> bool {
+      bool mine = wait(b_qraw, uq & 1);
+      if (mine && uq > 0) mine = wait(b_qfree, (uq - 1) & 1);   // the previous factors were read
+      if (named_bar_or(ebar, 128, !mine)) return false;
+      const int qrow = lane >> 2, part = lane & 3;
+#pragma unroll 1
+      for (int g = warp - 12; g < 8; g += 4) {
+        auto block_of = [&](int c) -> uint8_t* { return gQ + c * kCQChunk + g * 1024; };
+        __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
+#pragma unroll
+        for (int c = 0; c < 9; ++c)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 v = *reinterpret_cast<const uint4*>(block_of(c) + qrow * 128 + (((part + 4 * h) ^ qrow) << 4));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m2 = __hmax2(m2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[k])));
+          }
+        float mx = fmaxf(__low2float(m2), __high2float(m2));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        int e = 0;
+        if (mx > 0.f) e = min(max(7 - ((int)((__float_as_uint(mx) >> 23) & 0xFFu) - 127), -126), 126);
+        const float f = __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll 3
+        for (int c = 0; c < 9; ++c) {
+          uint8_t* blk = block_of(c);
+          uint4 v[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            v[h] = *reinterpret_cast<const uint4*>(blk + qrow * 128 + (((part + 4 * h) ^ qrow) << 4));
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int un = part + 4 * h;           // columns 8 un .. of the chunk
+            const uint32_t w[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = split_e4m3x2(bf_lo(w[k]) * f, bf_hi(w[k]) * f);
+            const uint32_t off = qrow * 64 + (((un >> 1) ^ ((qrow >> 1) & 3)) << 4) + (un & 1) * 8;
+            *reinterpret_cast<uint2*>(blk + off) = make_uint2(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410));
+            *reinterpret_cast<uint2*>(blk + 512 + off) =
+                make_uint2(__byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632));
+          }
+        }
+        if (part == 0) qf_s[8 * g + qrow] = __uint_as_float((uint32_t)(127 - e) << 23);
+      }
+      fence_proxy_async_smem();
+      named_bar_sync(ebar, 128);
+      if (t == 0) {
+        mbar_arrive(b_qsc);
+        // the issuer needs both CTAs' terms: the odd CTA signals by st.async
+        if (leader) mbar_arrive_expect_tx(b_qfull, 16);
+        else st_async_v4(lead(smem_u32(sig_s)), make_uint4(0u, 0u, 0u, 0u), lead(b_qfull));
+      }
+      ++uq;
+      return true;
+    };
+    // value slots with a key that some row of the block does not see (the last one or two tiles of
+    // a block). False after a failed wait.
+    auto fix_values = [&](const CUnit& U) -> bool {
+      for (int tile = U.tb; tile < U.te; ++tile) {
+        const int ns = value_slots<VK>(U.hi, tile);
+        const int s0 = max(0, (U.lo - tile * kChunkTile) / VK);      // the first such slot
+        for (int s = s0; s < ns; ++s) {
+          const int key0 = tile * kChunkTile + s * VK;
+          const uint32_t slot = (rv + s) % kVRing;
+          const bool mine = wait(b_aux + 8 * slot, (aux_phase >> slot) & 1);
+          aux_phase ^= 1u << slot;
+          if (named_bar_or(ebar, 128, !mine)) return false;
+          uint8_t* g = gV + slot * kCSlot;
+#pragma unroll
+          for (int idx = t; idx < kCSlot / 16; idx += 128) {
+            const int key = key0 + (idx >> 3) % VK;
+            if (key < U.lo) continue;
+            uint4* p = reinterpret_cast<uint4*>(g + idx * 16);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (key < U.hi) {
+              v = *p;
+              v.x = finite_word<FP8>(v.x);
+              v.y = finite_word<FP8>(v.y);
+              v.z = finite_word<FP8>(v.z);
+              v.w = finite_word<FP8>(v.w);
+            }
+            *p = v;
+          }
+          fence_proxy_async_smem();
+          named_bar_sync(ebar, 128);
+          if (t == 0) {
+            fence_acq_rel_cluster();
+            mbar_complete_tx_cluster(lead(b_vfull + 8 * slot), kCSlot);   // this CTA's share is in place
+          }
+        }
+        rv += ns;
+      }
+      return true;
+    };
+    // q of the first unit; then per unit its value fixes, q of the next one (whose load waits for
+    // this unit's QK^T only), and its results
+    int nu = u0;                               // E4M3: the next unit whose q is to be split
+    auto split_next = [&]() -> bool {
+      if (!FP8) return true;
+      for (; nu < u1; ++nu) {
+        const CUnit N = load_cunit(a, nu);
+        if (N.te != N.tb) {
+          ++nu;
+          return split_q();
+        }
+      }
+      return true;
+    };
+    bool ok = split_next();
+    for (int u = u0; u < u1 && ok; ++u) {
       const CUnit U = load_cunit(a, u);
       const int T = U.te - U.tb;
+      if (T > 0) ok = fix_values(U) && split_next();
+      if (!ok) break;
       n += T;
       fail |= !wait(b_stat, us & 1);
-      const float ref = ref_s[t], sum = sum_s[t] + sum_s[t ^ 64];
+      const float ref = ref_s[t], sum = (sum_s[t] + sum_s[t ^ 64]) + (sum_s[t + 128] + sum_s[(t ^ 64) + 128]);
       mbar_arrive(b_statfree);
       ++us;
       if (T > 0) fail |= !wait(b_pv + 8, (n - 1) & 1);
@@ -735,118 +894,6 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         const float l = sum == 0.f ? -INFINITY : (ref + log2f(sum) - Cfg::kPOffLog2) * kCLn2;
         if (U.slot < 0) a.lse[orow] = l;
         else a.part_lse[(int64_t)U.slot * kChunkRows + br] = l;
-      }
-    }
-  } else {
-    regs_lower<80>();
-    if (warp < 14) {
-      // ================================================================== q terms, value fixes
-      constexpr uint32_t cbar = 3;
-      const int t = threadIdx.x - 384;
-      uint32_t rv = 0, uq = 0, aux_phase = 0;    // value slots so far; a phase bit per slot
-      bool ok = true;
-      for (int u = u0; u < u1 && ok; ++u) {
-        const CUnit U = load_cunit(a, u);
-        const int T = U.te - U.tb;
-        if (T == 0) continue;
-        if constexpr (FP8) {
-          // The 64 rows of this CTA, bf16 as TMA landed them, become q' = q 2^e (the row's largest
-          // |q| in [128, 256)) as E4M3 hi and lo in place: every 1 KB group of 8 rows x 64 columns
-          // becomes hi in its first 512 bytes and lo in its second (64-byte swizzled rows). A warp
-          // owns whole groups; lane 4 q + p holds 16-byte units p and p + 4 of row q.
-          bool mine = wait(b_qraw, uq & 1);
-          if (mine && uq > 0) mine = wait(b_qfree, (uq - 1) & 1);   // the previous factors were read
-          if (named_bar_or(cbar, 64, !mine)) { ok = false; break; }
-          const int qrow = lane >> 2, part = lane & 3;
-          for (int g = warp - 12; g < 8; g += 2) {
-            auto block_of = [&](int c) -> uint8_t* { return gQ + c * kCQChunk + g * 1024; };
-            __nv_bfloat162 m2 = __float2bfloat162_rn(0.f);
-#pragma unroll
-            for (int c = 0; c < 9; ++c)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint4 v = *reinterpret_cast<const uint4*>(block_of(c) + qrow * 128 + (((part + 4 * h) ^ qrow) << 4));
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) m2 = __hmax2(m2, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[k])));
-              }
-            float mx = fmaxf(__low2float(m2), __high2float(m2));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            int e = 0;
-            if (mx > 0.f) e = min(max(7 - ((int)((__float_as_uint(mx) >> 23) & 0xFFu) - 127), -126), 126);
-            const float f = __uint_as_float((uint32_t)(e + 127) << 23);
-#pragma unroll 3
-            for (int c = 0; c < 9; ++c) {
-              uint8_t* blk = block_of(c);
-              uint4 v[2];
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-                v[h] = *reinterpret_cast<const uint4*>(blk + qrow * 128 + (((part + 4 * h) ^ qrow) << 4));
-              __syncwarp();
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int un = part + 4 * h;           // columns 8 un .. of the chunk
-                const uint32_t w[4] = {v[h].x, v[h].y, v[h].z, v[h].w};
-                uint32_t o[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) o[k] = split_e4m3x2(bf_lo(w[k]) * f, bf_hi(w[k]) * f);
-                const uint32_t off = qrow * 64 + (((un >> 1) ^ ((qrow >> 1) & 3)) << 4) + (un & 1) * 8;
-                *reinterpret_cast<uint2*>(blk + off) = make_uint2(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410));
-                *reinterpret_cast<uint2*>(blk + 512 + off) =
-                    make_uint2(__byte_perm(o[0], o[1], 0x7632), __byte_perm(o[2], o[3], 0x7632));
-              }
-            }
-            if (part == 0) qf_s[8 * g + qrow] = __uint_as_float((uint32_t)(127 - e) << 23);
-          }
-          fence_proxy_async_smem();
-          named_bar_sync(cbar, 64);
-          if (t == 0) {
-            mbar_arrive(b_qsc);
-            // the issuer needs both CTAs' terms: the odd CTA signals by st.async
-            if (leader) mbar_arrive_expect_tx(b_qfull, 16);
-            else st_async_v4(lead(smem_u32(sig_s)), make_uint4(0u, 0u, 0u, 0u), lead(b_qfull));
-          }
-          ++uq;
-        }
-        // value slots with a key that some row of the block does not see (the last one or two
-        // tiles of a block)
-        for (int k = 0; k < T; ++k) {
-          const int tile = U.tb + k;
-          const int ns = value_slots<VK>(U.hi, tile);
-          for (int s = 0; s < ns && ok; ++s) {
-            const int key0 = tile * kChunkTile + s * VK;
-            if (key0 + VK <= U.lo) continue;
-            const uint32_t slot = (rv + s) % kVRing;
-            const bool mine = wait(b_aux + 8 * slot, (aux_phase >> slot) & 1);
-            aux_phase ^= 1u << slot;
-            if (named_bar_or(cbar, 64, !mine)) { ok = false; break; }
-            uint8_t* g = gV + slot * kCSlot;
-            for (int idx = t; idx < kCSlot / 16; idx += 64) {
-              const int row = (idx >> 3) % VK;
-              const int key = key0 + row;
-              if (key < U.lo) continue;
-              uint4* p = reinterpret_cast<uint4*>(g + idx * 16);
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (key < U.hi) {
-                v = *p;
-                v.x = finite_word<FP8>(v.x);
-                v.y = finite_word<FP8>(v.y);
-                v.z = finite_word<FP8>(v.z);
-                v.w = finite_word<FP8>(v.w);
-              }
-              *p = v;
-            }
-            fence_proxy_async_smem();
-            named_bar_sync(cbar, 64);
-            if (t == 0) {
-              fence_acq_rel_cluster();
-              mbar_complete_tx_cluster(lead(b_vfull + 8 * slot), kCSlot);   // this CTA's share is in place
-            }
-          }
-          rv += ns;
-          if (!ok) break;
-        }
       }
     }
   }
