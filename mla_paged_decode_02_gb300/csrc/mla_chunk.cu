@@ -33,14 +33,14 @@
 //
 // Masks. Scores of keys a row does not see are selected away by index, whatever they hold. In
 // the PV product such keys meet P = 0, and 0 x NaN is NaN: value slots with a key that some row
-// of the block does not see pass through two warps that write zeros over rows no row sees and
-// over non-finite values of rows that only some see (a row that does see such a key has a
+// of the block does not see are put right when they land: zeros over rows no row sees and over
+// non-finite values of rows that only some see (a row that does see such a key has a
 // non-finite score there, which makes its result NaN without the value; a score of -inf gives
 // the key weight 0). Boxes past the last key start at the end of the pool, so TMA fills zeros.
 //
 // Roles (512 threads): warp 0 loads q and keys, warp 2 values; warps 1 and 3 of the even CTA issue
-// QK^T and PV; warps 4-11 softmax, four threads to a row; warps 12-15 value fixes, (E4M3) the split
-// of q, and the epilogue. Every wait is bounded; a stall sets the device error word, and both CTAs drain and
+// QK^T and PV; warps 4-11 softmax, four threads to a row; warps 12-15 (E4M3) the split of q, and the
+// epilogue. Every wait is bounded; a stall sets the device error word, and both CTAs drain and
 // leave through a cluster barrier.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
   __shared__ __align__(16) uint32_t sig_s[4];
   __shared__ uint32_t tmem_base_s, abort_s;
   __shared__ float qf_s[64];                 // E4M3: 2^-e of this CTA's rows
-  __shared__ float mx_s[256], sum_s[256], ref_s[128];
+  __shared__ float mx_s[2][256], sum_s[256], ref_s[128];
 
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -364,8 +364,45 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
       uint32_t slot = 0, ph = 1;
       bool ok = true;
       const uint32_t lb = lead(b_vfull);
-      // a slot with a key that some row does not see is loaded on a barrier of this CTA; the
-      // fixing warps then count its bytes
+      // a slot with a key that some row does not see (in the last one or two tiles of a block) is
+      // loaded on a barrier of this CTA, put right when it has landed, and then counted as full.
+      // Up to two such loads are in flight.
+      uint32_t aux_phase = 0;                             // a bit per slot
+      uint32_t pend_slot[2] = {0, 0};
+      int pend_key[2] = {0, 0}, npend = 0;
+      auto fix_first = [&](const CUnit& U) -> bool {
+        const uint32_t fs = pend_slot[0];
+        const int key0 = pend_key[0];
+        pend_slot[0] = pend_slot[1];
+        pend_key[0] = pend_key[1];
+        --npend;
+        if (!wait_warp(b_aux + 8 * fs, (aux_phase >> fs) & 1)) return false;
+        aux_phase ^= 1u << fs;
+        uint8_t* g = gV + fs * kCSlot;
+        const int from = max(0, U.lo - key0), units = (VK - from) * 8;   // 16-byte units of a piece
+        for (int idx = lane; idx < units; idx += 32) {
+          const int row = from + (idx >> 3);
+          const bool seen = key0 + row < U.hi;
+          uint4 v[VC];
+#pragma unroll
+          for (int x = 0; x < VC; ++x) {
+            uint4* p = reinterpret_cast<uint4*>(g + (x * VK + row) * 128 + (idx & 7) * 16);
+            v[x] = seen ? *p : make_uint4(0, 0, 0, 0);
+            v[x].x = finite_word<FP8>(v[x].x);
+            v[x].y = finite_word<FP8>(v[x].y);
+            v[x].z = finite_word<FP8>(v[x].z);
+            v[x].w = finite_word<FP8>(v[x].w);
+            *p = v[x];
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (el) {
+          fence_acq_rel_cluster();
+          mbar_complete_tx_cluster(lb + 8 * fs, kCSlot);   // this CTA's share is in place
+        }
+        return true;
+      };
       auto load = [&](uint32_t dst, bool fix, int row, int col) {   // col: 128-byte piece of the row
         if (fix) {
           if (FP8) tma_load_2d(dst, &a.tm_v, b_aux + 8 * slot, 128 * col, row);
@@ -390,7 +427,8 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
             const int row = kSub ? __shfl_sync(0xffffffffu, rows, (s * VK + (lane < nv ? i * vbox : 0)) >> 3) : 0;
             key += VK;
             const bool fix = key > U.lo;
-            ok = wait_warp(b_vempty + 8 * slot, ph);
+            if (fix && npend == 2) ok = fix_first(U);
+            ok = ok && wait_warp(b_vempty + 8 * slot, ph);
             if (!ok) break;
             const uint32_t dst = sV + slot * kCSlot;
             if (el) {
@@ -405,6 +443,10 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
               __syncwarp();
               if (lane < nv) load(dst + (uint32_t)(c * VK + i * vbox) * 128u, fix, row, c0 + c);
             }
+            if (fix) {
+              pend_slot[npend] = slot;
+              pend_key[npend++] = key - VK;
+            }
             if (++slot == kVRing) {
               slot = 0;
               ph ^= 1;
@@ -413,6 +455,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
           if (!ok) break;
           rows = next_rows;
         }
+        while (ok && npend > 0) ok = fix_first(U);
       }
       if (*abort_flag) {
         const uint64_t t0 = global_timer_ns();
@@ -545,7 +588,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
     const int row = t & 63, half = (t >> 6) & 1, quarter = t >> 7;   // row of this CTA; keys 128 half + 64 quarter ..
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const float c0 = a.softmax_scale * (FP8 ? __ldg(a.kv_scale) : 1.0f) * kCLog2e;
-    uint32_t n = 0, uc = 0, us = 0;
+    uint32_t n = 0, uc = 0, us = 0, xp = 0;
     bool fail = false, stop = false;
     for (int u = u0; u < u1 && !stop; ++u) {
       const CUnit U = load_cunit(a, u);
@@ -570,30 +613,32 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         const int mine = vis - tile * kChunkTile - 128 * half - 64 * quarter;   // keys of this thread its row sees
         // pass 1: the largest score
         float mx = -INFINITY;
-        {
+        const bool none = __all_sync(0xffffffffu, mine <= 0);    // no row of the warp sees its keys here
+        if (!none) {
           float s[64];
 #pragma unroll
           for (int i = 0; i < 4; ++i) tmem_ld16(ts + 16 * i, s + 16 * i);
           tmem_wait_ld();
+          if (c < 0.f) {
+#pragma unroll
+            for (int x = 0; x < 64; ++x) s[x] = -s[x];
+          }
           if (mine < 64) {
 #pragma unroll
-            for (int x = 0; x < 64; ++x) s[x] = x < mine ? s[x] * c : -INFINITY;
-            mx = max64(s);
-          } else if (c >= 0.f) {
-            mx = max64(s) * c;
-          } else {
-#pragma unroll
-            for (int x = 0; x < 64; ++x) s[x] *= c;
-            mx = max64(s);
+            for (int x = 0; x < 64; ++x) s[x] = x < mine ? s[x] : -INFINITY;
           }
+          mx = max64(s);
+          if (mx != -INFINITY) mx *= fabsf(c);
         }
         float alpha = 1.f;
-        bool rescale = false;
-        if (named_bar_or(sbar, 256, fail || mx > ref + Cfg::kRescaleLog2)) {
+        bool rescale = false, move = k == 0;
+        if (!move) move = named_bar_or(sbar, 256, fail || mx > ref + Cfg::kRescaleLog2);
+        if (move) {
+          mx_s[xp][t] = mx;
           if (named_bar_or(sbar, 256, fail)) { stop = true; break; }
-          mx_s[t] = mx;
-          named_bar_sync(sbar, 256);
-          const float nm = fmaxf(fmaxf(ref, fmaxf(mx, mx_s[t ^ 64])), fmaxf(mx_s[t ^ 128], mx_s[t ^ 192]));
+          const float* m = mx_s[xp];
+          const float nm = fmaxf(fmaxf(ref, fmaxf(mx, m[t ^ 64])), fmaxf(m[t ^ 128], m[t ^ 192]));
+          xp ^= 1;
           alpha = nm == -INFINITY ? 1.f : ex2_approx(ref - nm);
           ref = nm;
           sum *= alpha;
@@ -602,6 +647,10 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         // pass 2: P, packed
         const float off = (ref == -INFINITY ? 0.f : ref) - Cfg::kPOffLog2;
         uint32_t pw[32];        // bf16: key pairs; E4M3: hi bytes (words 0-15), lo bytes (16-31)
+        if (none) {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) pw[x] = 0u;
+        } else
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float s[32];
@@ -693,15 +742,14 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
       if (T > 0) ++uc;
     }
   } else {
-    // ================================================================== q terms, value fixes, epilogue
+    // ================================================================== q terms, epilogue
     regs_raise<216>();
     constexpr uint32_t ebar = 2;
     const int t = threadIdx.x - 384;
     const int row = t & 63, half = t >> 6;     // epilogue: this thread's row and value columns 256 half ..
     const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
     const float kvs = FP8 ? __ldg(a.kv_scale) : 1.0f;
-    uint32_t rv = 0, uq = 0, aux_phase = 0;    // value slots so far; units; a phase bit per slot
-    uint32_t n = 0, us = 0;
+    uint32_t n = 0, us = 0, uq = 0;
     bool fail = false;
     // E4M3: the 64 rows of this CTA, bf16 as TMA landed them, become q' = q 2^e (the row's largest
     // |q| in [128, 256)) as E4M3 hi and lo in place: every 1 KB group of 8 rows x 64 columns becomes
@@ -765,47 +813,8 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
       ++uq;
       return true;
     };
-    // value slots with a key that some row of the block does not see (the last one or two tiles of
-    // a block). False after a failed wait.
-    auto fix_values = [&](const CUnit& U) -> bool {
-      for (int tile = U.tb; tile < U.te; ++tile) {
-        const int ns = value_slots<VK>(U.hi, tile);
-        const int s0 = max(0, (U.lo - tile * kChunkTile) / VK);      // the first such slot
-        for (int s = s0; s < ns; ++s) {
-          const int key0 = tile * kChunkTile + s * VK;
-          const uint32_t slot = (rv + s) % kVRing;
-          const bool mine = wait(b_aux + 8 * slot, (aux_phase >> slot) & 1);
-          aux_phase ^= 1u << slot;
-          if (named_bar_or(ebar, 128, !mine)) return false;
-          uint8_t* g = gV + slot * kCSlot;
-#pragma unroll
-          for (int idx = t; idx < kCSlot / 16; idx += 128) {
-            const int key = key0 + (idx >> 3) % VK;
-            if (key < U.lo) continue;
-            uint4* p = reinterpret_cast<uint4*>(g + idx * 16);
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (key < U.hi) {
-              v = *p;
-              v.x = finite_word<FP8>(v.x);
-              v.y = finite_word<FP8>(v.y);
-              v.z = finite_word<FP8>(v.z);
-              v.w = finite_word<FP8>(v.w);
-            }
-            *p = v;
-          }
-          fence_proxy_async_smem();
-          named_bar_sync(ebar, 128);
-          if (t == 0) {
-            fence_acq_rel_cluster();
-            mbar_complete_tx_cluster(lead(b_vfull + 8 * slot), kCSlot);   // this CTA's share is in place
-          }
-        }
-        rv += ns;
-      }
-      return true;
-    };
-    // q of the first unit; then per unit its value fixes, q of the next one (whose load waits for
-    // this unit's QK^T only), and its results
+    // E4M3: q of the first unit; then per unit q of the next one (whose load waits for this unit's
+    // QK^T only) and its results
     int nu = u0;                               // E4M3: the next unit whose q is to be split
     auto split_next = [&]() -> bool {
       if (!FP8) return true;
@@ -822,7 +831,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
     for (int u = u0; u < u1 && ok; ++u) {
       const CUnit U = load_cunit(a, u);
       const int T = U.te - U.tb;
-      if (T > 0) ok = fix_values(U) && split_next();
+      if (T > 0) ok = split_next();
       if (!ok) break;
       n += T;
       fail |= !wait(b_stat, us & 1);
