@@ -292,20 +292,39 @@ def cache_write(latent: torch.Tensor, rope: torch.Tensor, slot_mapping: torch.Te
         raise MLAError(st, "mla_cache_write")
 
 
-def _on_current_device(*tensors) -> None:
-    """The library launches on the current device and reads these as its pointers."""
-    cuda = [t for t in tensors if t is not None]
-    if any(not t.is_cuda for t in cuda):
-        raise ValueError("every tensor must be on the GPU")
-    if any(t.device.index != torch.cuda.current_device() for t in cuda):
-        raise ValueError("every tensor must be on the current device")
+def _addresses(stream, *tensors):
+    """(stream handle, addresses of the tensors). The library launches on the current device and
+    dereferences these there, so all of them have to live on it. (The checks of the calls below
+    cost as much as a small kernel: they look at each property once.)"""
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise ValueError("every tensor must be on the GPU")
+    dev = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("every tensor must be on the current device")
+    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return handle, [None if t is None else t.data_ptr() for t in tensors]
+
+
+def _allocated(stream, shape, dtype, device) -> torch.Tensor:
+    """A tensor of the current stream's that a kernel on `stream` uses, whenever it is freed."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream())
+        t.record_stream(stream)
+    return t
 
 
 def _rows_of(t: torch.Tensor, n: int, width: int, name: str) -> int:
     """Row stride of a bf16 [n, width] tensor whose rows are contiguous and 16-byte aligned."""
-    if t.dtype != torch.bfloat16 or t.shape != (n, width) or (n > 0 and t.stride(1) != 1):
+    if t.dtype is not torch.bfloat16 or t.shape != (n, width):
         raise ValueError(f"{name} must be a bf16 [N, {width}] tensor with contiguous rows")
-    stride = t.stride(0) if n > 1 else width
+    stride, inner = t.stride()
+    if n > 0 and inner != 1:
+        raise ValueError(f"{name} must be a bf16 [N, {width}] tensor with contiguous rows")
+    if n <= 1:
+        stride = width
     if stride < width or stride % 8 != 0:
         raise ValueError(f"the rows of {name} must be apart by a multiple of 8 elements, {width} at least")
     return stride
@@ -333,7 +352,7 @@ def rope_cache_write(latent: torch.Tensor, rope: torch.Tensor, positions: torch.
         raise ValueError("kv_cache must be a contiguous [Np, P, 576] tensor")
     Np, P, _ = kv_cache.shape
     kvd = _kv_dtype_of(kv_cache)
-    if kvd == KV_FP8_E4M3 and (kv_scale is None or kv_scale.dtype != torch.float32):
+    if kvd == KV_FP8_E4M3 and (kv_scale is None or kv_scale.dtype != torch.float32 or kv_scale.numel() < 1):
         raise ValueError("the FP8 cache needs kv_scale as a float32 device tensor")
     if (q_rope is None) != (q is None):
         raise ValueError("q_rope and q are given together or not at all")
@@ -350,13 +369,11 @@ def rope_cache_write(latent: torch.Tensor, rope: torch.Tensor, positions: torch.
             raise ValueError("q_rope's tokens and heads must be apart by a multiple of 8 elements")
     if device_error is not None and device_error.dtype not in (torch.int32, torch.uint32):
         raise ValueError("device_error must be a 32-bit integer tensor")
-    _on_current_device(latent, rope, positions, cos_sin, slot_mapping, kv_cache, q_rope, q, device_error,
-                       kv_scale if kvd == KV_FP8_E4M3 else None)
-    st = lib().mla_rope_cache_write(_ptr(latent), ls, _ptr(rope), rs, _ptr(positions), _ptr(cos_sin), cos_sin.shape[0],
-                                    int(bool(interleaved)), _ptr(slot_mapping), n, _ptr(kv_cache), Np, P, kvd,
-                                    _ptr(kv_scale) if kvd == KV_FP8_E4M3 else None,
-                                    _ptr(q_rope) if n > 0 else None, qt, qh, H, _ptr(q) if n > 0 else None,
-                                    _ptr(device_error), _stream(stream))
+    handle, at = _addresses(stream, latent, rope, positions, cos_sin, slot_mapping, kv_cache,
+                            kv_scale if kvd == KV_FP8_E4M3 else None, q_rope if n > 0 else None, q if n > 0 else None,
+                            device_error)
+    st = lib().mla_rope_cache_write(at[0], ls, at[1], rs, at[2], at[3], cos_sin.shape[0], 1 if interleaved else 0, at[4], n,
+                                    at[5], Np, P, kvd, at[6], at[7], qt, qh, H, at[8], at[9], handle)
     if st != MLA_OK:
         raise MLAError(st, "mla_rope_cache_write")
 
@@ -399,25 +416,26 @@ def chunk_attention(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.
     if seq_lens.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != B or cu_q_lens.shape != (B + 1,):
         raise ValueError("block_table must be [B, MB], seq_lens [B] and cu_q_lens [B + 1]")
     kvd = _kv_dtype_of(kv_cache)
-    if kvd == KV_FP8_E4M3 and (kv_scale is None or kv_scale.dtype != torch.float32):
+    if kvd == KV_FP8_E4M3 and (kv_scale is None or kv_scale.dtype != torch.float32 or kv_scale.numel() < 1):
         raise ValueError("the FP8 cache needs kv_scale as a float32 device tensor")
-    if out is None:
-        out = torch.empty((T, H, D_V), dtype=torch.bfloat16, device=q.device)
-    elif out.dtype != torch.bfloat16 or out.shape != (T, H, D_V) or not out.is_contiguous():
+    if out is not None and (out.dtype != torch.bfloat16 or out.shape != (T, H, D_V) or not out.is_contiguous()):
         raise ValueError("out must be a contiguous bf16 [T, H, 512] tensor")
-    if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    elif lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous():
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [T, H] tensor")
-    _on_current_device(q, kv_cache, block_table, seq_lens, cu_q_lens, out, lse, workspace,
-                       kv_scale if kvd == KV_FP8_E4M3 else None)
+    scale = kv_scale if kvd == KV_FP8_E4M3 else None
     params = make_chunk_params(B, T, H, P, Np, block_table.shape[1], max_seq_len, kvd, causal)
+    handle, at = _addresses(stream, q, kv_cache, block_table, seq_lens, cu_q_lens, scale, out, lse, workspace)
+    if out is None:
+        out = _allocated(stream, (T, H, D_V), torch.bfloat16, q.device)
+        at[6] = out.data_ptr()
+    if lse is None:
+        lse = _allocated(stream, (T, H), torch.float32, q.device)
+        at[7] = lse.data_ptr()
     if workspace is None:
-        workspace = alloc_chunk_workspace(params, q.device)
-    st = lib().mla_chunk_attention(ctypes.byref(params), _ptr(q), _ptr(kv_cache), _ptr(block_table), _ptr(seq_lens),
-                                   _ptr(cu_q_lens), ctypes.c_float(softmax_scale),
-                                   _ptr(kv_scale) if kvd == KV_FP8_E4M3 else None, _ptr(out), _ptr(lse),
-                                   _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+        workspace = _allocated(stream, (chunk_workspace_size(params),), torch.uint8, q.device)
+        at[8] = workspace.data_ptr()
+    st = lib().mla_chunk_attention(ctypes.byref(params), at[0], at[1], at[2], at[3], at[4], softmax_scale, at[5], at[6],
+                                   at[7], at[8], workspace.numel() * workspace.element_size(), handle)
     if st != MLA_OK:
         raise MLAError(st, "mla_chunk_attention")
     return out, lse
@@ -428,20 +446,22 @@ def merge_states(out_a: torch.Tensor, lse_a: torch.Tensor, out_b: torch.Tensor, 
     """Join two attention results over disjoint keys: out_* [..., 512] bf16 and lse_* [...]
     float32 as decode() and chunk_attention() return them. out and lse may be given, in place
     of one of the inputs among others. Returns (out, lse)."""
-    shape = tuple(lse_a.shape)
-    if out is None:
-        out = torch.empty_like(out_a)
-    if lse is None:
-        lse = torch.empty_like(lse_a)
-    for name, t in (("out_a", out_a), ("out_b", out_b), ("out", out)):
-        if t.dtype != torch.bfloat16 or tuple(t.shape) != shape + (D_V,) or not t.is_contiguous():
+    shape = lse_a.shape
+    full = shape + (D_V,)
+    for name, t in (("out_a", out_a), ("out_b", out_b), ("out", out_a if out is None else out)):
+        if t.dtype is not torch.bfloat16 or t.shape != full or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous bf16 [..., 512] tensor of the shape of lse_a")
-    for name, t in (("lse_a", lse_a), ("lse_b", lse_b), ("lse", lse)):
-        if t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous():
+    for name, t in (("lse_a", lse_a), ("lse_b", lse_b), ("lse", lse_a if lse is None else lse)):
+        if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous float32 tensor of one shape")
-    _on_current_device(out_a, lse_a, out_b, lse_b, out, lse)
-    st = lib().mla_merge_states(_ptr(out_a), _ptr(lse_a), _ptr(out_b), _ptr(lse_b), lse_a.numel(), _ptr(out), _ptr(lse),
-                                _stream(stream))
+    handle, at = _addresses(stream, out_a, lse_a, out_b, lse_b, out, lse)
+    if out is None:
+        out = _allocated(stream, full, torch.bfloat16, out_a.device)
+        at[4] = out.data_ptr()
+    if lse is None:
+        lse = _allocated(stream, shape, torch.float32, out_a.device)
+        at[5] = lse.data_ptr()
+    st = lib().mla_merge_states(at[0], at[1], at[2], at[3], lse_a.numel(), at[4], at[5], handle)
     if st != MLA_OK:
         raise MLAError(st, "mla_merge_states")
     return out, lse

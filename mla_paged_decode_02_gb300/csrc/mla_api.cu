@@ -549,7 +549,7 @@ MLA_EXPORT mla_status mla_chunk_attention(const mla_chunk_params* p, const void*
   sa.causal = p->causal;
   sa.max_len = (int)std::min<int64_t>(cap, p->max_seq_len);
   sa.workers = pairs;
-  sa.setup = 1;
+  sa.setup = 2;
   sa.tokens = p->num_tokens;
   sa.max_units = w.max_units;
   ChunkArgs ca;

@@ -152,6 +152,16 @@ __device__ __forceinline__ uint32_t finite_word(uint32_t w) {
   return w;
 }
 
+// whether all values of 16 bytes are finite: no exponent (bf16) or magnitude (E4M3) is all ones
+template <bool FP8>
+__device__ __forceinline__ bool finite_words(const uint4& v) {
+  // adding one to an all-ones field carries into the bit above it, which the mask has cleared
+  constexpr uint32_t kMask = FP8 ? 0x7F7F7F7Fu : 0x7F807F80u, kOne = FP8 ? 0x01010101u : 0x00800080u;
+  constexpr uint32_t kCarry = FP8 ? 0x80808080u : 0x80008000u;
+  const uint32_t c = (((v.x & kMask) + kOne) | ((v.y & kMask) + kOne)) | (((v.z & kMask) + kOne) | ((v.w & kMask) + kOne));
+  return (c & kCarry) == 0u;
+}
+
 // One lane of a converged warp. The issuing warps stay converged around it, their barrier waits
 // and descriptor arithmetic warp-uniform.
 __device__ __forceinline__ bool elect_one() {
@@ -379,21 +389,26 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         if (!wait_warp(b_aux + 8 * fs, (aux_phase >> fs) & 1)) return false;
         aux_phase ^= 1u << fs;
         uint8_t* g = gV + fs * kCSlot;
-        const int from = max(0, U.lo - key0), units = (VK - from) * 8;   // 16-byte units of a piece
-        for (int idx = lane; idx < units; idx += 32) {
-          const int row = from + (idx >> 3);
-          const bool seen = key0 + row < U.hi;
-          uint4 v[VC];
+        // rows [lo, hi) of the slot keep their finite values, rows from hi on become zeros
+        const int lo = max(0, U.lo - key0), hi = min(VK, U.hi - key0);
+        for (int idx = lane; idx < (hi - lo) * 8; idx += 32) {
 #pragma unroll
           for (int x = 0; x < VC; ++x) {
-            uint4* p = reinterpret_cast<uint4*>(g + (x * VK + row) * 128 + (idx & 7) * 16);
-            v[x] = seen ? *p : make_uint4(0, 0, 0, 0);
-            v[x].x = finite_word<FP8>(v[x].x);
-            v[x].y = finite_word<FP8>(v[x].y);
-            v[x].z = finite_word<FP8>(v[x].z);
-            v[x].w = finite_word<FP8>(v[x].w);
-            *p = v[x];
+            uint4* p = reinterpret_cast<uint4*>(g + (x * VK + lo + (idx >> 3)) * 128 + (idx & 7) * 16);
+            uint4 v = *p;
+            if (!finite_words<FP8>(v)) {
+              v.x = finite_word<FP8>(v.x);
+              v.y = finite_word<FP8>(v.y);
+              v.z = finite_word<FP8>(v.z);
+              v.w = finite_word<FP8>(v.w);
+              *p = v;
+            }
           }
+        }
+        for (int idx = lane; idx < (VK - hi) * 8; idx += 32) {
+#pragma unroll
+          for (int x = 0; x < VC; ++x)
+            *reinterpret_cast<uint4*>(g + (x * VK + hi + (idx >> 3)) * 128 + (idx & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
