@@ -162,6 +162,12 @@ __device__ __forceinline__ bool finite_words(const uint4& v) {
   return (c & kCarry) == 0u;
 }
 
+// 32 bytes of a thread in one store
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+}
+
 // One lane of a converged warp. The issuing warps stay converged around it, their barrier waits
 // and descriptor arithmetic warp-uniform.
 __device__ __forceinline__ bool elect_one() {
@@ -626,7 +632,8 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         tc_fence_after();
         const uint32_t ts = tmem + lane_addr + (n & 1) * 128 + 64 * quarter;
         const int mine = vis - tile * kChunkTile - 128 * half - 64 * quarter;   // keys of this thread its row sees
-        // pass 1: the largest score
+        // pass 1: the largest score. Scores stay raw (times the sign of their factor) and are scaled
+        // after the reference is subtracted, so that the difference of large ones is exact.
         float mx = -INFINITY;
         const bool none = __all_sync(0xffffffffu, mine <= 0);    // no row of the warp sees its keys here
         if (!none) {
@@ -643,24 +650,25 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
             for (int x = 0; x < 64; ++x) s[x] = x < mine ? s[x] : -INFINITY;
           }
           mx = max64(s);
-          if (mx != -INFINITY) mx *= fabsf(c);
         }
         float alpha = 1.f;
         bool rescale = false, move = k == 0;
-        if (!move) move = named_bar_or(sbar, 256, fail || mx > ref + Cfg::kRescaleLog2);
+        if (!move)
+          move = named_bar_or(sbar, 256,
+                              fail || (mx > ref && (ref == -INFINITY || (mx - ref) * fabsf(c) > Cfg::kRescaleLog2)));
         if (move) {
           mx_s[xp][t] = mx;
           if (named_bar_or(sbar, 256, fail)) { stop = true; break; }
           const float* m = mx_s[xp];
           const float nm = fmaxf(fmaxf(ref, fmaxf(mx, m[t ^ 64])), fmaxf(m[t ^ 128], m[t ^ 192]));
           xp ^= 1;
-          alpha = nm == -INFINITY ? 1.f : ex2_approx(ref - nm);
+          alpha = ref == -INFINITY ? 0.f : ex2_approx((ref - nm) * fabsf(c));   // none seen before: O and sum are 0
           ref = nm;
           sum *= alpha;
           rescale = k > 0;
         }
         // pass 2: P, packed
-        const float off = (ref == -INFINITY ? 0.f : ref) - Cfg::kPOffLog2;
+        const float off = ref == -INFINITY ? 0.f : c < 0.f ? ref : -ref;
         uint32_t pw[32];        // bf16: key pairs; E4M3: hi bytes (words 0-15), lo bytes (16-31)
         if (none) {
 #pragma unroll
@@ -672,7 +680,10 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
           tmem_ld32(ts + 32 * i, s);
           tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 32; x += 2) fma2(s[x], s[x + 1], c, -off);
+          for (int x = 0; x < 32; x += 2) {
+            add2(s[x], s[x + 1], off, off);
+            fma2(s[x], s[x + 1], c, Cfg::kPOffLog2);
+          }
           if (mine >= 32 * i + 32) {
 #pragma unroll
             for (int x = 0; x < 32; ++x) s[x] = ex2_approx(s[x]);
@@ -751,7 +762,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
       // the row's reference and this thread's sum, for the epilogue
       if (us > 0) fail |= !wait(b_statfree, (us - 1) & 1);
       sum_s[t] = sum;
-      if (t < 128) ref_s[t] = ref;
+      if (t < 128) ref_s[t] = ref == -INFINITY ? ref : ref * fabsf(c);
       mbar_arrive(b_stat);
       ++us;
       if (T > 0) ++uc;
@@ -864,9 +875,12 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         if (T > 0) {
           tmem_ld32(tmem + lane_addr + kCOCol + 32 * i, o);
           tmem_wait_ld();
-        }
 #pragma unroll
-        for (int x = 0; x < 32; ++x) o[x] = sum == 0.f ? 0.f : o[x] * inv;
+          for (int x = 0; x < 32; ++x) o[x] *= inv;         // a row that sees no key has O = 0
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = 0.f;
+        }
       };
       // O has been read: the next unit's first PV may overwrite it
       auto release_o = [&]() {
@@ -893,11 +907,24 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
           }
         }
         release_o();
-        if (keep) {
-          __nv_bfloat16* dst = a.out + orow * kDV + 256 * half;
+        {
+          // neighbouring lanes swap halves of 64 bytes, so that a pair writes 64 bytes of one row
+          const bool odd = (lane & 1) != 0;
+          const bool keep2 = __shfl_xor_sync(0xffffffffu, keep ? 1 : 0, 1) != 0;
+          __nv_bfloat16* dst = a.out + (orow - (odd ? 1 : 0)) * kDV + 256 * half + (odd ? 16 : 0);
+          const bool k0 = odd ? keep2 : keep, k1 = odd ? keep : keep2;
 #pragma unroll
-          for (int x = 0; x < 32; ++x)
-            reinterpret_cast<uint4*>(dst)[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+          for (int x = 0; x < 8; ++x) {
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const uint32_t mine = odd ? w[16 * x + 8 + y] : w[16 * x + y], other = odd ? w[16 * x + y] : w[16 * x + 8 + y];
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, other, 1);
+              w[16 * x + y] = odd ? got : mine;
+              w[16 * x + 8 + y] = odd ? mine : got;
+            }
+            if (k0) store32(dst + 32 * x, w + 16 * x);
+            if (k1) store32(dst + kDV + 32 * x, w + 16 * x + 8);
+          }
         }
       } else {
 #pragma unroll 1

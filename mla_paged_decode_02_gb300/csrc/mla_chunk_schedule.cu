@@ -26,6 +26,7 @@ __device__ __forceinline__ int clamp_len(int L, int max_len) { return L < 0 ? 0 
 __global__ void __launch_bounds__(kSchedThreads) chunk_schedule_kernel(ChunkSchedArgs a) {
   __shared__ int64_t scan_tmp[32];
   const int tid = threadIdx.x;
+  griddep_wait();                          // the lengths and the workspace may be the work before's
   griddep_launch_dependents();
   // 1. blocks per sequence, and the checks of the inputs only the device can see
   const int B = a.B;
@@ -164,6 +165,7 @@ __global__ void __launch_bounds__(kSchedThreads) chunk_schedule_kernel(ChunkSche
 __global__ void __launch_bounds__(256) chunk_combine_kernel(ChunkCombineArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t gtid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, gstride = (int64_t)gridDim.x * blockDim.x;
+  griddep_wait();
   if ((a.hdr[0] & MLA_DEVERR_CU_Q) == 0) {
     for (int64_t i = gtid; i < (int64_t)a.B * a.MB; i += gstride) {
       const int b = (int)(i / a.MB), j = (int)(i - (int64_t)b * a.MB);
@@ -216,13 +218,29 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(ChunkCombineArgs a) 
 }
 
 cudaError_t launch_chunk_schedule(const ChunkSchedArgs& a, cudaStream_t s) {
-  chunk_schedule_kernel<<<1, kSchedThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kSchedThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_schedule_kernel, a);
 }
 
 cudaError_t launch_chunk_combine(const ChunkCombineArgs& a, int grid, cudaStream_t s) {
-  chunk_combine_kernel<<<grid, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_combine_kernel, a);
 }
 
 }  // namespace mla
