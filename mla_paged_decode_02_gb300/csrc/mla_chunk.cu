@@ -152,6 +152,38 @@ __device__ __forceinline__ uint32_t finite_word(uint32_t w) {
   return w;
 }
 
+// 32 bytes of a thread in one store
+__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+}
+
+// The rest of a wait that was not over at the first look, out of line: some thirty waits share the
+// instruction cache. A wait that fails also raises the peer's abort flag, so that its waits end.
+__device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, uint32_t abort_s, uint32_t peer, uint32_t* err,
+                                         uint64_t limit_ns) {
+  volatile uint32_t* flag = reinterpret_cast<volatile uint32_t*>(__cvta_shared_to_generic(abort_s));
+  const bool ok = mbar_wait(bar, parity, flag, err, MLA_DEVERR_TIMEOUT, limit_ns);
+  if (!ok) st_cluster_u32(map_to_rank(abort_s, peer), 1u);
+  return ok;
+}
+
+// 64 bytes (16 words) of the rows of two neighbouring lanes: they swap halves, so that a pair
+// writes 64 contiguous bytes of the even lane's row and then of the odd lane's. `p` points to the
+// even lane's row, plus 32 bytes in the odd lane; keep0, keep1: whether those rows are stored.
+// (Each lane writing 16 bytes of its own row at a time kept the load/store path, which the barriers
+// of all roles share, busy for 3 us per unit.)
+__device__ __forceinline__ void store_pair64(uint8_t* p, size_t row_bytes, uint32_t* w, bool odd, bool keep0, bool keep1) {
+#pragma unroll
+  for (int y = 0; y < 8; ++y) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w[y] : w[8 + y], 1);
+    if (odd) w[y] = got;
+    else w[8 + y] = got;
+  }
+  if (keep0) store32(p, w);
+  if (keep1) store32(p + row_bytes, w + 8);
+}
+
 // whether all values of 16 bytes are finite: no exponent (bf16) or magnitude (E4M3) is all ones
 template <bool FP8>
 __device__ __forceinline__ bool finite_words(const uint4& v) {
@@ -160,12 +192,6 @@ __device__ __forceinline__ bool finite_words(const uint4& v) {
   constexpr uint32_t kCarry = FP8 ? 0x80808080u : 0x80008000u;
   const uint32_t c = (((v.x & kMask) + kOne) | ((v.y & kMask) + kOne)) | (((v.z & kMask) + kOne) | ((v.w & kMask) + kOne));
   return (c & kCarry) == 0u;
-}
-
-// 32 bytes of a thread in one store
-__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-               :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
 }
 
 // One lane of a converged warp. The issuing warps stay converged around it, their barrier waits
@@ -301,7 +327,10 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
   };
 
   // the same by every lane of a warp that stays converged
-  auto wait_warp = [&](uint32_t bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
+  auto wait_warp = [&](uint32_t bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) ||
+                                       wait_longer(bar, parity, smem_u32(&abort_s), peer, err, a.wait_limit_ns));
+  };
 
   // The launch gives every thread 128 registers. The epilogue's threads hold 256 columns of a row
   // as bf16: 72 + 2 x 112 + 216 = 4 x 128.
@@ -684,13 +713,12 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
             add2(s[x], s[x + 1], off, off);
             fma2(s[x], s[x + 1], c, Cfg::kPOffLog2);
           }
-          if (mine >= 32 * i + 32) {
+          if (mine < 32 * i + 32) {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) s[x] = ex2_approx(s[x]);
-          } else {
-#pragma unroll
-            for (int x = 0; x < 32; ++x) s[x] = 32 * i + x < mine ? ex2_approx(s[x]) : 0.f;
+            for (int x = 0; x < 32; ++x) s[x] = 32 * i + x < mine ? s[x] : -INFINITY;
           }
+#pragma unroll
+          for (int x = 0; x < 32; ++x) s[x] = ex2_approx(s[x]);
           sum += sum32(s);                               // the normaliser sums the unrounded values
           if constexpr (FP8) {
 #pragma unroll
@@ -805,7 +833,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         int e = 0;
         if (mx > 0.f) e = min(max(7 - ((int)((__float_as_uint(mx) >> 23) & 0xFFu) - 127), -126), 126);
         const float f = __uint_as_float((uint32_t)(e + 127) << 23);
-#pragma unroll 3
+#pragma unroll 1
         for (int c = 0; c < 9; ++c) {
           uint8_t* blk = block_of(c);
           uint4 v[2];
@@ -871,6 +899,8 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
       const bool keep = br < U.nrows;
       const float inv = sum == 0.f ? 0.f : kvs / sum;          // a row that sees no key: zeros
       const int64_t orow = (int64_t)U.row0 + br;
+      const int odd = lane & 1;
+      const bool keep0 = br - odd < U.nrows, keep1 = br - odd + 1 < U.nrows;   // the pair's rows
       auto load_o = [&](int i, float* o) {       // 32 columns, normalised
         if (T > 0) {
           tmem_ld32(tmem + lane_addr + kCOCol + 32 * i, o);
@@ -907,36 +937,20 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
           }
         }
         release_o();
-        {
-          // neighbouring lanes swap halves of 64 bytes, so that a pair writes 64 bytes of one row
-          const bool odd = (lane & 1) != 0;
-          const bool keep2 = __shfl_xor_sync(0xffffffffu, keep ? 1 : 0, 1) != 0;
-          __nv_bfloat16* dst = a.out + (orow - (odd ? 1 : 0)) * kDV + 256 * half + (odd ? 16 : 0);
-          const bool k0 = odd ? keep2 : keep, k1 = odd ? keep : keep2;
+        uint8_t* p = reinterpret_cast<uint8_t*>(a.out + (orow - odd) * kDV + 256 * half) + 32 * odd;
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              const uint32_t mine = odd ? w[16 * x + 8 + y] : w[16 * x + y], other = odd ? w[16 * x + y] : w[16 * x + 8 + y];
-              const uint32_t got = __shfl_xor_sync(0xffffffffu, other, 1);
-              w[16 * x + y] = odd ? got : mine;
-              w[16 * x + 8 + y] = odd ? mine : got;
-            }
-            if (k0) store32(dst + 32 * x, w + 16 * x);
-            if (k1) store32(dst + kDV + 32 * x, w + 16 * x + 8);
-          }
-        }
+        for (int x = 0; x < 8; ++x) store_pair64(p + 64 * x, kDV * 2, w + 16 * x, odd, keep0, keep1);
       } else {
+        uint8_t* p = reinterpret_cast<uint8_t*>(a.part_o + ((int64_t)U.slot * kChunkRows + br - odd) * kDV + 256 * half) + 32 * odd;
 #pragma unroll 1
         for (int i = 0; i < 8; ++i) {
           float o[32];
           load_o(i, o);
-          if (keep) {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + ((int64_t)U.slot * kChunkRows + br) * kDV + 256 * half + 32 * i);
+          uint32_t w[32];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-          }
-          __syncwarp();
+          for (int x = 0; x < 32; ++x) w[x] = __float_as_uint(o[x]);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) store_pair64(p + 128 * i + 64 * x, kDV * 4, w + 16 * x, odd, keep0, keep1);
         }
         release_o();
       }
