@@ -372,7 +372,8 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
           const int next_rows = tile + 1 < U.te ? tile_row(a, U, tile + 1, lane) : 0;
           const int r0 = __shfl_sync(0xffffffffu, rows, 16 * (int)rank), r1 = __shfl_sync(0xffffffffu, rows, 16 * (int)rank + 8);
           const int row = __shfl_sync(0xffffffffu, rows, 16 * (int)rank + (lane < nk ? lane * (kbox >> 3) : 0));
-          for (int c = 0; c < KS; ++c) {
+  #pragma unroll 1
+        for (int c = 0; c < KS; ++c) {
             ok = wait_warp(b_kempty + 8 * slot, ph);
             if (!ok) break;
             const uint32_t dst = sK + slot * kCSlot, bar = lb + 8 * slot;
@@ -410,49 +411,8 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
       bool ok = true;
       const uint32_t lb = lead(b_vfull);
       // a slot with a key that some row does not see (in the last one or two tiles of a block) is
-      // loaded on a barrier of this CTA, put right when it has landed, and then counted as full.
-      // Up to two such loads are in flight.
+      // loaded on a barrier of this CTA, put right when it has landed, and then counted as full
       uint32_t aux_phase = 0;                             // a bit per slot
-      uint32_t pend_slot[2] = {0, 0};
-      int pend_key[2] = {0, 0}, npend = 0;
-      auto fix_first = [&](const CUnit& U) -> bool {
-        const uint32_t fs = pend_slot[0];
-        const int key0 = pend_key[0];
-        pend_slot[0] = pend_slot[1];
-        pend_key[0] = pend_key[1];
-        --npend;
-        if (!wait_warp(b_aux + 8 * fs, (aux_phase >> fs) & 1)) return false;
-        aux_phase ^= 1u << fs;
-        uint8_t* g = gV + fs * kCSlot;
-        // rows [lo, hi) of the slot keep their finite values, rows from hi on become zeros
-        const int lo = max(0, U.lo - key0), hi = min(VK, U.hi - key0);
-        for (int idx = lane; idx < (hi - lo) * 8; idx += 32) {
-#pragma unroll
-          for (int x = 0; x < VC; ++x) {
-            uint4* p = reinterpret_cast<uint4*>(g + (x * VK + lo + (idx >> 3)) * 128 + (idx & 7) * 16);
-            uint4 v = *p;
-            if (!finite_words<FP8>(v)) {
-              v.x = finite_word<FP8>(v.x);
-              v.y = finite_word<FP8>(v.y);
-              v.z = finite_word<FP8>(v.z);
-              v.w = finite_word<FP8>(v.w);
-              *p = v;
-            }
-          }
-        }
-        for (int idx = lane; idx < (VK - hi) * 8; idx += 32) {
-#pragma unroll
-          for (int x = 0; x < VC; ++x)
-            *reinterpret_cast<uint4*>(g + (x * VK + hi + (idx >> 3)) * 128 + (idx & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (el) {
-          fence_acq_rel_cluster();
-          mbar_complete_tx_cluster(lb + 8 * fs, kCSlot);   // this CTA's share is in place
-        }
-        return true;
-      };
       auto load = [&](uint32_t dst, bool fix, int row, int col) {   // col: 128-byte piece of the row
         if (fix) {
           if (FP8) tma_load_2d(dst, &a.tm_v, b_aux + 8 * slot, 128 * col, row);
@@ -472,13 +432,13 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
           const int n = value_slots<VK>(U.hi, tile);
           int key = tile * kChunkTile;
           const int i = lane % nvr, c = lane / nvr;       // kSub: this lane's box i of piece c
+#pragma unroll 1
           for (int s = 0; s < n; ++s) {
             const int r0 = __shfl_sync(0xffffffffu, rows, s * VK >> 3);
             const int row = kSub ? __shfl_sync(0xffffffffu, rows, (s * VK + (lane < nv ? i * vbox : 0)) >> 3) : 0;
             key += VK;
             const bool fix = key > U.lo;
-            if (fix && npend == 2) ok = fix_first(U);
-            ok = ok && wait_warp(b_vempty + 8 * slot, ph);
+            ok = wait_warp(b_vempty + 8 * slot, ph);
             if (!ok) break;
             const uint32_t dst = sV + slot * kCSlot;
             if (el) {
@@ -494,8 +454,38 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
               if (lane < nv) load(dst + (uint32_t)(c * VK + i * vbox) * 128u, fix, row, c0 + c);
             }
             if (fix) {
-              pend_slot[npend] = slot;
-              pend_key[npend++] = key - VK;
+              const int first_key = key - VK;
+              ok = wait_warp(b_aux + 8 * slot, (aux_phase >> slot) & 1);
+              if (!ok) break;
+              aux_phase ^= 1u << slot;
+              uint8_t* g = gV + slot * kCSlot;
+              // rows [lo, hi) of the slot keep their finite values, rows from hi on become zeros
+              const int lo = max(0, U.lo - first_key), hi = min(VK, U.hi - first_key);
+              for (int idx = lane; idx < (hi - lo) * 8; idx += 32) {
+#pragma unroll
+                for (int x = 0; x < VC; ++x) {
+                  uint4* p = reinterpret_cast<uint4*>(g + (x * VK + lo + (idx >> 3)) * 128 + (idx & 7) * 16);
+                  uint4 v = *p;
+                  if (!finite_words<FP8>(v)) {
+                    v.x = finite_word<FP8>(v.x);
+                    v.y = finite_word<FP8>(v.y);
+                    v.z = finite_word<FP8>(v.z);
+                    v.w = finite_word<FP8>(v.w);
+                    *p = v;
+                  }
+                }
+              }
+              for (int idx = lane; idx < (VK - hi) * 8; idx += 32) {
+#pragma unroll
+                for (int x = 0; x < VC; ++x)
+                  *reinterpret_cast<uint4*>(g + (x * VK + hi + (idx >> 3)) * 128 + (idx & 7) * 16) = make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (el) {
+                fence_acq_rel_cluster();
+                mbar_complete_tx_cluster(lb + 8 * slot, kCSlot);   // this CTA's share is in place
+              }
             }
             if (++slot == kVRing) {
               slot = 0;
@@ -505,7 +495,6 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
           if (!ok) break;
           rows = next_rows;
         }
-        while (ok && npend > 0) ok = fix_first(U);
       }
       if (*abort_flag) {
         const uint64_t t0 = global_timer_ns();
@@ -530,6 +519,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
           for (int tile = U.tb; tile < U.te && ok; ++tile, ++n) {
             const uint32_t d = tmem + (n & 1) * 128;
             ok = wait_warp(b_sempty + 8 * (n & 1), ((n >> 1) & 1) ^ 1);
+#pragma unroll 1
             for (int c = 0; c < KS && ok; ++c) {
               ok = wait_warp(b_kfull + 8 * slot, ph);
               if (!ok) break;
@@ -586,6 +576,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
             if (tile == U.tb) ok = wait_warp(b_oempty, (uc & 1) ^ 1);
             // by halves of the tile's keys, whose P is written and released apart: the way from one
             // PV over its completion, the next P and the signal back is hidden by the other half
+#pragma unroll 1
             for (int s = 0; s < kHalfSlots * 2 && ok; ++s) {
               if (s % kHalfSlots == 0) {
                 ok = wait_warp(b_p + 8 * (s / kHalfSlots), n & 1);
