@@ -858,26 +858,21 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
       ++uq;
       return true;
     };
-    // E4M3: q of the first unit; then per unit q of the next one (whose load waits for this unit's
-    // QK^T only) and its results
-    int nu = u0;                               // E4M3: the next unit whose q is to be split
-    auto split_next = [&]() -> bool {
-      if (!FP8) return true;
-      for (; nu < u1; ++nu) {
-        const CUnit N = load_cunit(a, nu);
-        if (N.te != N.tb) {
-          ++nu;
-          return split_q();
-        }
-      }
-      return true;
-    };
-    bool ok = split_next();
-    for (int u = u0; u < u1 && ok; ++u) {
-      const CUnit U = load_cunit(a, u);
+    // E4M3: q of the first unit before anything else, then before a unit's results q of the next
+    // one, whose load waits for the unit's QK^T only (one loop, so that the split is there once)
+    int nu = u0;                               // the next unit whose q may have to be split
+    for (int u = FP8 ? u0 - 1 : u0; u < u1; ++u) {
+      const CUnit U = load_cunit(a, max(u, u0));
       const int T = U.te - U.tb;
-      if (T > 0) ok = split_next();
-      if (!ok) break;
+      if (FP8 && (u < u0 || T > 0)) {
+        bool found = false;
+        for (; nu < u1 && !found; ++nu) {
+          const CUnit N = load_cunit(a, nu);
+          found = N.te != N.tb;
+        }
+        if (found && !split_q()) break;
+      }
+      if (u < u0) continue;
       n += T;
       fail |= !wait(b_stat, us & 1);
       const float ref = ref_s[t], sum = (sum_s[t] + sum_s[t ^ 64]) + (sum_s[t + 128] + sum_s[(t ^ 64) + 128]);

@@ -158,6 +158,58 @@ __global__ void __launch_bounds__(kSchedThreads) chunk_schedule_kernel(ChunkSche
   }
 }
 
+// Few cut rows (four warps exist for each): a warp per 128 columns of a row, lane s holding the
+// weight of piece s, four pieces read at a time. The call on 16 blocks cut into 6 pieces each takes
+// 64.5 us so and 66.5 us with a warp per row; with 76 cut blocks a warp per row is 1 us faster.
+__device__ __forceinline__ void merge_few_rows(const ChunkCombineArgs& a, int64_t tasks, int64_t warp) {
+  const int lane = threadIdx.x & 31;
+  if (warp >= tasks * 4) return;
+  const int4 st = a.split_list[warp / (kChunkRows * 4)];
+  const int r = (int)(warp >> 2) % kChunkRows, col = ((int)warp & 3) * 128 + lane * 4;
+  if (r >= st.y) return;
+  const int ns = st.z;
+  const float* plse = a.part_lse + (int64_t)st.w * kChunkRows + r;
+  const float* po = a.part_o + ((int64_t)st.w * kChunkRows + r) * kDV + col;
+  float m = -INFINITY;
+  for (int s = lane; s < ns; s += 32) m = fmaxf(m, plse[(int64_t)s * kChunkRows]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float wsum = 0.f;
+  for (int s0 = 0; s0 < ns; s0 += 32) {
+    const int mine = s0 + lane;
+    const float ls = mine < ns ? plse[(int64_t)mine * kChunkRows] : -INFINITY;
+    const float w = ls == -INFINITY ? 0.f : __expf(ls - m);
+    const int n = min(32, ns - s0);
+    for (int s = 0; s < n; s += 4) {
+      float4 v[4];
+      float ww[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        ww[k] = s + k < n ? __shfl_sync(0xffffffffu, w, s + k) : 0.f;
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        // a NaN weight is read: it makes the row NaN
+        if (ww[k] != 0.f) v[k] = *reinterpret_cast<const float4*>(po + (int64_t)(s0 + s + k) * kChunkRows * kDV);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        wsum += ww[k];
+        acc.x += ww[k] * v[k].x;
+        acc.y += ww[k] * v[k].y;
+        acc.z += ww[k] * v[k].z;
+        acc.w += ww[k] * v[k].w;
+      }
+    }
+  }
+  const float inv = wsum == 0.f ? 0.f : 1.f / wsum;     // a row that sees no key: zeros
+  const __nv_bfloat162 h0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+  const __nv_bfloat162 h1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  const int64_t row = (int64_t)st.x + r;
+  *reinterpret_cast<uint2*>(a.out + row * kDV + col) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
+  if (lane == 0 && (warp & 3) == 0) a.lse[row] = wsum == 0.f ? -INFINITY : m + logf(wsum);
+}
+
 // Merges the pieces of cut blocks, a warp per (block, row): lse = log sum_s exp(lse_s),
 // out = sum_s exp(lse_s - lse) O_s; a piece in which the row sees no key has lse_s = -inf and
 // weight 0. Lane l owns output columns 16 l ..; also reports block-table entries outside the
@@ -176,6 +228,10 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(ChunkCombineArgs a) 
     }
   }
   const int64_t tasks = (int64_t)a.hdr[2] * kChunkRows;
+  if (tasks * 4 <= gstride >> 5) {
+    merge_few_rows(a, tasks, gtid >> 5);
+    return;
+  }
   for (int64_t task = gtid >> 5; task < tasks; task += gstride >> 5) {
     const int4 st = a.split_list[task / kChunkRows];
     const int r = (int)(task % kChunkRows);
