@@ -17,9 +17,9 @@
 // softmax stays inside the CTA (four threads compare maxima), and P needs no exchange.
 // Tensor memory per CTA: S 2 x 128 columns, O 2 x 128.
 //
-// Shared memory per CTA: 64 query rows (72 KB), P (64 rows x 256 keys, 32 KB), a ring of four
-// 16 KB key slots (128 keys x 128 bytes of the row) and one of three 16 KB value slots (this
-// CTA's 256 columns of 32 or, E4M3, 64 keys). The 512-byte value pieces come from L2: the peer has
+// Shared memory per CTA: 64 query rows (72 KB), P (64 rows x 256 keys, 32 KB), and seven 16 KB slots
+// in two rings: keys (128 keys x 128 bytes of the row) and values (this CTA's 256 columns of 32 or,
+// E4M3, 64 keys). The 512-byte value pieces come from L2: the peer has
 // just read those keys.
 //
 // Two issuing warps, each with a ring and a producer, so that QK^T of tile n + 1 (of the next unit
@@ -51,8 +51,7 @@
 namespace mla {
 namespace {
 
-constexpr int kKRing = 4;                        // key slots
-constexpr int kVRing = 3;                        // value slots
+constexpr int kCSlots = 7;                       // key and value slots
 constexpr int kCSlot = 16384;
 constexpr int kCQChunk = 8192;                   // 64 rows x 64 columns bf16
 constexpr int kCQBytes = 9 * kCQChunk;
@@ -60,7 +59,7 @@ constexpr int kCPBytes = 64 * kChunkTile * 2;    // bf16, or E4M3 hi and lo
 constexpr int kCThreads = 512;
 constexpr int kCTmemCols = 512;
 constexpr int kCOCol = 256;                      // O at columns 256 + 128 j
-constexpr int kCDynBytes = 1024 + kCQBytes + kCPBytes + (kKRing + kVRing) * kCSlot;
+constexpr int kCDynBytes = 1024 + kCQBytes + kCPBytes + kCSlots * kCSlot;
 constexpr int kCSmemLimit = 232448;
 constexpr int kCStaticBudget = 6144;
 static_assert(kCDynBytes + kCStaticBudget <= kCSmemLimit, "shared memory budget");
@@ -72,6 +71,9 @@ struct ChunkCfg {
   static constexpr int kKeySlots = FP8 ? 5 : 9;          // 128 bytes of the key row each
   static constexpr int kSlotKeys = FP8 ? 64 : 32;        // keys of a value slot
   static constexpr int kValueChunks = FP8 ? 2 : 4;       // 128-byte pieces of its rows
+  // a tile takes 9 key and 8 value slots (bf16) or 5 and 4; the better split of the seven, measured
+  // against 4 + 3 and 3 + 4: bf16 prompts 188 -> 181 us, E4M3 mixed step 102 against 106 us
+  static constexpr int kKRing = FP8 ? 4 : 3, kVRing = kCSlots - kKRing;
   static constexpr float kRescaleLog2 = FP8 ? 4.f : 8.f;
   static constexpr float kPOffLog2 = FP8 ? 4.f : 0.f;
   static_assert(kSlotKeys * kValueChunks * 128 == kCSlot, "value slot");
@@ -111,9 +113,9 @@ __device__ __forceinline__ int value_slots(int hi, int tile) {
   return left >= kChunkTile ? kChunkTile / kSlotKeys : (left + kSlotKeys - 1) / kSlotKeys;
 }
 
-// First cache row of the 8 keys 8 lane .. of a tile (page_rows below turns it into boxes): the
-// pool's end (a box there is filled with zeros) past the keys the block sees; a block-table
-// entry outside the pool reads page 0 (the combine kernel reports it).
+// First cache row of the 8 keys 8 lane .. of a tile, for the boxes that start there: past the keys
+// the block sees the pool's end (TMA fills such a box with zeros); a block-table entry outside the
+// pool reads page 0 (the combine kernel reports it).
 __device__ __forceinline__ int tile_row(const ChunkArgs& a, const CUnit& U, int tile, int lane) {
   const int tok = tile * kChunkTile + 8 * lane;
   if (tok >= U.hi) return a.total_rows;
@@ -130,6 +132,13 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       :: "r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(c0), "r"(c1) : "memory");
 }
 
+// An arrival at the cluster's even CTA with the default ordering (release at CTA scope): what it
+// announces lies in the arriving CTA's shared memory, was put there before a proxy fence and a
+// barrier, and is read there, by the arriving SM's tensor core. A release at cluster scope, which
+// also waits for the thread's outstanding global traffic, made the mixed step 6% slower.
+__device__ __forceinline__ void mbar_arrive_cluster_cta(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(bar_cluster) : "memory");
+}
 // An arrival at the cluster's even CTA that publishes no writes (what it releases was only read).
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar_cluster) : "memory");
@@ -243,6 +252,7 @@ template <bool FP8, bool kSub>
 __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_constant__ ChunkArgs a) {
   using Cfg = ChunkCfg<FP8>;
   constexpr int KS = Cfg::kKeySlots, VK = Cfg::kSlotKeys, VC = Cfg::kValueChunks;
+  constexpr int kKRing = Cfg::kKRing, kVRing = Cfg::kVRing;
   extern __shared__ uint8_t dsmem_raw[];
   __shared__ __align__(8) uint64_t bar_kfull[kKRing], bar_kempty[kKRing], bar_vfull[kVRing], bar_vempty[kVRing], bar_aux[kVRing];
   __shared__ __align__(8) uint64_t bar_qfull, bar_qempty, bar_qraw, bar_qsc, bar_qfree;
@@ -483,7 +493,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
               fence_proxy_async_smem();
               __syncwarp();
               if (el) {
-                fence_acq_rel_cluster();
+                __threadfence_block();                              // as mbar_arrive_cluster_cta
                 mbar_complete_tx_cluster(lb + 8 * slot, kCSlot);   // this CTA's share is in place
               }
             }
@@ -774,7 +784,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         fail |= named_bar_or(4 + half, 128, fail);
         if (!fail && (t & 191) == 0) {
           if (leader) mbar_arrive(b_p + 8 * half);
-          else mbar_arrive_cluster(lead(b_p + 8 * half));
+          else mbar_arrive_cluster_cta(lead(b_p + 8 * half));
         }
       }
       if (stop) break;
