@@ -296,13 +296,11 @@ def _addresses(stream, *tensors):
     """(stream handle, addresses of the tensors). The library launches on the current device and
     dereferences these there, so all of them have to live on it. (The checks of the calls below
     cost as much as a small kernel: they look at each property once.)"""
+    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
     for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise ValueError("every tensor must be on the GPU")
-    dev = torch._C._cuda_getDevice()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("every tensor must be on the current device")
+        if t is not None and t.get_device() != dev:            # -1: not on a GPU
+            raise ValueError("every tensor must be on the current device" if t.is_cuda else
+                             "every tensor must be on the GPU")
     handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
     return handle, [None if t is None else t.data_ptr() for t in tensors]
 
@@ -343,14 +341,20 @@ def rope_cache_write(latent: torch.Tensor, rope: torch.Tensor, positions: torch.
     n = latent.shape[0]
     ls = _rows_of(latent, n, 512, "latent")
     rs = _rows_of(rope, n, 64, "rope")
-    for name, t in (("positions", positions), ("slot_mapping", slot_mapping)):
-        if t.dtype != torch.int64 or t.shape != (n,) or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous int64 [N] tensor")
-    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.shape[1] != 64 or not cos_sin.is_contiguous():
+    i64 = torch.int64
+    if positions.dtype is not i64 or positions.shape != (n,) or not positions.is_contiguous() or \
+            slot_mapping.dtype is not i64 or slot_mapping.shape != (n,) or not slot_mapping.is_contiguous():
+        raise ValueError("positions and slot_mapping must be contiguous int64 [N] tensors")
+    if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be a contiguous float32 [max_pos, 64] tensor")
-    if kv_cache.dim() != 3 or kv_cache.shape[2] != D_QK or not kv_cache.is_contiguous():
+    max_pos, width = cos_sin.shape
+    if width != 64:
+        raise ValueError("cos_sin must be a contiguous float32 [max_pos, 64] tensor")
+    if kv_cache.dim() != 3 or not kv_cache.is_contiguous():
         raise ValueError("kv_cache must be a contiguous [Np, P, 576] tensor")
-    Np, P, _ = kv_cache.shape
+    Np, P, width = kv_cache.shape
+    if width != D_QK:
+        raise ValueError("kv_cache must be a contiguous [Np, P, 576] tensor")
     kvd = _kv_dtype_of(kv_cache)
     if kvd == KV_FP8_E4M3 and (kv_scale is None or kv_scale.dtype != torch.float32 or kv_scale.numel() < 1):
         raise ValueError("the FP8 cache needs kv_scale as a float32 device tensor")
@@ -358,13 +362,20 @@ def rope_cache_write(latent: torch.Tensor, rope: torch.Tensor, positions: torch.
         raise ValueError("q_rope and q are given together or not at all")
     H, qt, qh = 0, 0, 0
     if q is not None:
-        if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[0] != n or q.shape[2] != D_QK or not q.is_contiguous():
+        if q.dtype is not torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
             raise ValueError("q must be a contiguous bf16 [N, H, 576] tensor")
-        H = q.shape[1]
-        if q_rope.dtype != torch.bfloat16 or q_rope.shape != (n, H, 64) or (q_rope.numel() > 0 and q_rope.stride(2) != 1):
+        qn, H, width = q.shape
+        if qn != n or width != D_QK:
+            raise ValueError("q must be a contiguous bf16 [N, H, 576] tensor")
+        if q_rope.dtype is not torch.bfloat16 or q_rope.shape != (n, H, 64):
             raise ValueError("q_rope must be a bf16 [N, H, 64] tensor with contiguous last dimension")
-        qt = q_rope.stride(0) if n > 1 else 0
-        qh = q_rope.stride(1) if H > 1 else 0
+        qt, qh, inner = q_rope.stride()
+        if inner != 1 and n > 0 and H > 0:
+            raise ValueError("q_rope must be a bf16 [N, H, 64] tensor with contiguous last dimension")
+        if n <= 1:
+            qt = 0
+        if H <= 1:
+            qh = 0
         if H < 1 or qt % 8 != 0 or qh % 8 != 0:
             raise ValueError("q_rope's tokens and heads must be apart by a multiple of 8 elements")
     if device_error is not None and device_error.dtype not in (torch.int32, torch.uint32):
@@ -372,7 +383,7 @@ def rope_cache_write(latent: torch.Tensor, rope: torch.Tensor, positions: torch.
     handle, at = _addresses(stream, latent, rope, positions, cos_sin, slot_mapping, kv_cache,
                             kv_scale if kvd == KV_FP8_E4M3 else None, q_rope if n > 0 else None, q if n > 0 else None,
                             device_error)
-    st = lib().mla_rope_cache_write(at[0], ls, at[1], rs, at[2], at[3], cos_sin.shape[0], 1 if interleaved else 0, at[4], n,
+    st = lib().mla_rope_cache_write(at[0], ls, at[1], rs, at[2], at[3], max_pos, 1 if interleaved else 0, at[4], n,
                                     at[5], Np, P, kvd, at[6], at[7], qt, qh, H, at[8], at[9], handle)
     if st != MLA_OK:
         raise MLAError(st, "mla_rope_cache_write")
@@ -448,12 +459,12 @@ def merge_states(out_a: torch.Tensor, lse_a: torch.Tensor, out_b: torch.Tensor, 
     of one of the inputs among others. Returns (out, lse)."""
     shape = lse_a.shape
     full = shape + (D_V,)
-    for name, t in (("out_a", out_a), ("out_b", out_b), ("out", out_a if out is None else out)):
+    for t in (out_a, out_b) if out is None else (out_a, out_b, out):
         if t.dtype is not torch.bfloat16 or t.shape != full or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous bf16 [..., 512] tensor of the shape of lse_a")
-    for name, t in (("lse_a", lse_a), ("lse_b", lse_b), ("lse", lse_a if lse is None else lse)):
+            raise ValueError("out_a, out_b and out must be contiguous bf16 [..., 512] tensors of the shape of lse_a")
+    for t in (lse_a, lse_b) if lse is None else (lse_a, lse_b, lse):
         if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous float32 tensor of one shape")
+            raise ValueError("lse_a, lse_b and lse must be contiguous float32 tensors of one shape")
     handle, at = _addresses(stream, out_a, lse_a, out_b, lse_b, out, lse)
     if out is None:
         out = _allocated(stream, full, torch.bfloat16, out_a.device)
