@@ -12,7 +12,8 @@
 // Memory bound: 1.2 KB in and as much (or half) out per token, and 256 bytes per head. A warp
 // takes one task: a token's cache row (72 16-byte groups), or 32 heads of its query rope
 // parts, where 4 lanes share a head (16 values each) and a lane keeps its 8 cosines and sines
-// in registers over the heads.
+// in registers over the heads. 4096 tokens x 128 heads, E4M3: 26.5 us for 142 MB (5.4 TB/s; 16 or 64
+// heads per task, more resident warps and streaming hints change nothing).
 #include <cuda_fp8.h>
 #include "mla_internal.h"
 #include "mla_rope.h"
