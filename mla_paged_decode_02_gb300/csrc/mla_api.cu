@@ -554,7 +554,6 @@ MLA_EXPORT mla_status mla_chunk_attention(const mla_chunk_params* p, const void*
   // with 16 heads: 226, 179, 188 us for 0, 1, 2 (bf16)
   sa.setup = fp8 ? 2 : 1;
   sa.tokens = p->num_tokens;
-  sa.max_units = w.max_units;
   ChunkArgs ca;
   std::memset(&ca, 0, sizeof(ca));
   const int64_t rows = (int64_t)p->num_pages * p->page_size;
@@ -602,7 +601,6 @@ MLA_EXPORT mla_status mla_chunk_attention(const mla_chunk_params* p, const void*
   cc.P = p->page_size;
   cc.num_pages = p->num_pages;
   cc.max_len = sa.max_len;
-  cc.tokens = p->num_tokens;
   cc.split_list = sa.split_list;
   cc.part_o = ca.part_o;
   cc.part_lse = ca.part_lse;

@@ -57,7 +57,6 @@ struct ChunkSchedArgs {
   ChunkUnit* units;
   int32_t B, H, causal, max_len, workers, setup;
   int32_t tokens;
-  int64_t max_units;
 };
 
 struct ChunkArgs {
@@ -89,7 +88,7 @@ struct ChunkCombineArgs {
   const int32_t* block_table;
   const int32_t* seq_lens;
   const int32_t* cu_q;
-  int32_t B, MB, P, num_pages, max_len, tokens;
+  int32_t B, MB, P, num_pages, max_len;
   const int4* split_list;
   const float* part_o;
   const float* part_lse;
