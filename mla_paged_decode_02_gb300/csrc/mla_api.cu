@@ -575,6 +575,7 @@ MLA_EXPORT mla_status mla_chunk_attention(const mla_chunk_params* p, const void*
   ca.cta_first = sa.cta_first;
   ca.err = sa.hdr;
   ca.out = static_cast<__nv_bfloat16*>(out);
+  ca.out_wide = aligned(out, 32) ? 1 : 0;
   ca.lse = lse;
   ca.part_o = reinterpret_cast<float*>(ws + w.po_off);
   ca.part_lse = reinterpret_cast<float*>(ws + w.plse_off);

@@ -166,10 +166,16 @@ __device__ __forceinline__ uint32_t finite_word(uint32_t w) {
   return w;
 }
 
-// 32 bytes of a thread in one store
-__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-               :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+// 32 bytes of a thread: one store where `wide` (the address is a multiple of 32), else two of 16
+__device__ __forceinline__ void store32(void* p, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+  } else {
+    uint4* q = reinterpret_cast<uint4*>(p);
+    q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
 // The rest of a wait that was not over at the first look, out of line: some thirty waits share the
@@ -188,15 +194,16 @@ __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, uint32_t
 // (With each lane writing 16 bytes of its own row at a time, the first tile of the next unit ran about
 // 3 us late, and 8 prompts of 16 heads took 234 us, so 222; the likely reason is the load/store
 // path, which the barriers of all roles share.)
-__device__ __forceinline__ void store_pair64(uint8_t* p, size_t row_bytes, uint32_t* w, bool odd, bool keep0, bool keep1) {
+__device__ __forceinline__ void store_pair64(uint8_t* p, size_t row_bytes, uint32_t* w, bool odd, bool keep0, bool keep1,
+                                             bool wide) {
 #pragma unroll
   for (int y = 0; y < 8; ++y) {
     const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w[y] : w[8 + y], 1);
     if (odd) w[y] = got;
     else w[8 + y] = got;
   }
-  if (keep0) store32(p, w);
-  if (keep1) store32(p + row_bytes, w + 8);
+  if (keep0) store32(p, w, wide);
+  if (keep1) store32(p + row_bytes, w + 8, wide);
 }
 
 // whether all values of 16 bytes are finite: no exponent (bf16) or magnitude (E4M3) is all ones
@@ -941,7 +948,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         release_o();
         uint8_t* p = reinterpret_cast<uint8_t*>(a.out + (orow - odd) * kDV + 256 * half) + 32 * odd;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) store_pair64(p + 64 * x, kDV * 2, w + 16 * x, odd, keep0, keep1);
+        for (int x = 0; x < 8; ++x) store_pair64(p + 64 * x, kDV * 2, w + 16 * x, odd, keep0, keep1, a.out_wide != 0);
       } else {
         uint8_t* p = reinterpret_cast<uint8_t*>(a.part_o + ((int64_t)U.slot * kChunkRows + br - odd) * kDV + 256 * half) + 32 * odd;
 #pragma unroll 1
@@ -952,7 +959,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
 #pragma unroll
           for (int x = 0; x < 32; ++x) w[x] = __float_as_uint(o[x]);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) store_pair64(p + 128 * i + 64 * x, kDV * 4, w + 16 * x, odd, keep0, keep1);
+          for (int x = 0; x < 2; ++x) store_pair64(p + 128 * i + 64 * x, kDV * 4, w + 16 * x, odd, keep0, keep1, true);
         }
         release_o();
       }

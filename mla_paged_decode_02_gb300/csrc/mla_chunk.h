@@ -77,6 +77,7 @@ struct ChunkArgs {
   int32_t H, P, MB, num_pages, causal;
   int32_t total_rows;        // num_pages * P: a box that starts here reads zeros
   int32_t k_box, v_box;      // rows of one key / value box
+  int32_t out_wide;          // out is 32-byte aligned (else 16): the stores that are made
   float softmax_scale;
   uint64_t wait_limit_ns;
   int32_t test_stall;

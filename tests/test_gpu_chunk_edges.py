@@ -115,3 +115,22 @@ def test_one_query_rope_part_for_all_heads_and_tokens():
         api.rope_cache_write(lat, rope, pos, cs, torch.arange(n, device="cuda"), cache, q_rope=q_rope, q=q)
         got.append(q)
     assert torch.equal(got[0], got[1]) and (got[0][..., :512] == 0).all() and got[0][..., 512:].abs().sum() > 0
+
+
+@pytest.mark.parametrize("kv", [BF, F8])
+@pytest.mark.parametrize("lens", [[(6, 300), (1, 90)], [(1, 9000)]])
+def test_an_output_that_starts_between_two_32_byte_boundaries(kv, lens):
+    """out needs 16-byte alignment only: a contiguous view that starts 8 elements into a buffer, for
+    blocks that are written directly and for blocks that are cut and merged."""
+    H = 16
+    c = ChunkCase(lens, H, 64, kv, pad=1, seed=46)
+    n = c.T * H * 512
+    flat = torch.full((n + 24,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = flat[8:8 + n].view(c.T, H, 512)
+    assert out.data_ptr() % 32 == 16
+    c.run(out=out, lse=torch.full((c.T, H), -3.5, dtype=torch.float32, device="cuda"))
+    c.check()
+    assert (flat[:8] == 7.0).all() and (flat[8 + n:] == 7.0).all()
+    aligned = ChunkCase(lens, H, 64, kv, pad=1, seed=46)
+    aligned.run()
+    assert torch.equal(aligned.out, c.out) and torch.equal(aligned.lse, c.lse)
