@@ -245,6 +245,10 @@ size_t mla_chunk_workspace_size(const mla_chunk_params* p, int32_t num_sms);
  * sees the first L_b - n_b + 1 + i keys when causal, else all L_b (a shared prefix). A row that
  * sees no key gets out 0 and lse -inf; rows of q that belong to no sequence are left as they
  * are in out and lse. Keys a row does not see may hold anything, NaN and infinities included.
+ * Softmax weights are rounded before the product with the values: to bf16 with the bf16 cache;
+ * with the FP8 cache to 8 significant bits where they are at least 2^-10 of the largest weight
+ * among the 2048 keys around (fewer bits down to 2^-21 of it, 0 below). Their sum, and lse, are
+ * of the unrounded weights.
  *   q            [T, H, 576] bf16;  out [T, H, 512] bf16 (both 16-byte aligned);
  *                lse [T, H] float32, natural log
  *   cu_q_lens    [B + 1] int32, ascending, within [0, T] (else MLA_DEVERR_CU_Q, nothing written)

@@ -258,6 +258,8 @@ __device__ __forceinline__ void umma_commit(uint32_t bar) {
 // B major bit 16, N>>3 at [17,23), M>>4 at [24,29)).
 // ab_bf16: 1 = bf16 operands, 0 = fp16 (kind::f16) or E4M3 (kind::f8f6f4).
 // a_mn / b_mn: 1 = MN-major, 0 = K-major.
+// kind::f8f6f4 takes the formats of A and B apart: kIdescE5M2A makes A's E5M2.
+constexpr uint32_t kIdescE5M2A = 1u << 7;
 __host__ __device__ constexpr uint32_t make_idesc(uint32_t m, uint32_t n, uint32_t ab_bf16,
                                                   uint32_t a_mn, uint32_t b_mn) {
   return (1u << 4) | (ab_bf16 << 7) | (ab_bf16 << 10) | (a_mn << 15) | (b_mn << 16) |
@@ -294,6 +296,24 @@ __device__ __forceinline__ uint32_t split_e4m3x2(float x0, float x1) {
       "sub.rn.f16x2 r, h, t;\n\t"
       "cvt.rn.satfinite.e4m3x2.f16x2 hb, t;\n\t"
       "cvt.rn.satfinite.e4m3x2.f16x2 lb, r;\n\t"
+      "mov.b32 %0, {hb, lb};\n\t}"
+      : "=r"(out) : "f"(x0), "f"(x1));
+  return out;
+}
+
+// x0, x1 (0 <= x <= 448) as an E4M3 term hi and an E5M2 term lo with hi + lo ~ x: hi is the fp16
+// rounding h of x rounded to E4M3, lo what hi leaves of h (exact in fp16) rounded to E5M2. Off by
+// at most 2^-8 x (and 2^-11 x for h) where hi is a normal number, x >= 2^-6; below that by at most
+// 2^-14, x / 8 and, for x < 2^-14, 2^-17: E5M2 keeps three significant bits down to 2^-14, where an
+// E4M3 lo ends at 2^-9. Returns hi in bits 0-15 and lo in bits 16-31, as split_e4m3x2.
+__device__ __forceinline__ uint32_t split_e4m3_e5m2x2(float x0, float x1) {
+  uint32_t out;
+  asm("{\n\t.reg .b32 h, t, r;\n\t.reg .b16 hb, lb;\n\t"
+      "cvt.rn.f16x2.f32 h, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 hb, h;\n\t"
+      "cvt.rn.f16x2.e4m3x2 t, hb;\n\t"
+      "sub.rn.f16x2 r, h, t;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f16x2 lb, r;\n\t"
       "mov.b32 %0, {hb, lb};\n\t}"
       : "=r"(out) : "f"(x0), "f"(x1));
   return out;
