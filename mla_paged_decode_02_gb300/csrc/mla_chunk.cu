@@ -34,12 +34,12 @@
 // the reference; smaller ones are off by at most 2^-18 of it and by 1/8 of themselves, and end at
 // 2^-21. The normaliser sums the unrounded weights, so what P loses the result loses: with a
 // reference that only rises, one strong early key over a long even context would leave most of the
-// weight in terms of few bits. So every 8 tiles the reference also moves down, to the largest
-// score of those 2048 keys, when that lies more than 2^4 below it; O and l grow instead (float32
-// holds the 2^60 that the reference may fall in all). Each key's P is then precise next to the
-// largest of its 2048 keys, and so are sums over any number of them: relative errors of 0.1 to
-// 0.8 in the result became 0.002 to 0.004 (tests: strong keys 6 to 13 natural-log units above 32 K
-// and 128 K others). 32 K keys x 128 heads take 1489 us so, 1480 with two E4M3 terms and no way down.
+// weight in terms of few bits. So every 4 tiles the reference also moves down, to the largest
+// score of those 1024 keys, when that lies more than 2^4 below it; O and l grow instead (float32
+// holds the 2^60 that the reference may fall in all). Few keys' weights are then of few bits, however
+// many there are: with strong keys 6 to 13 natural-log units above 32 K and 128 K others the 2-norm of
+// the error was 0.05 to 0.86 of the result and is 0.002 to 0.004. 32 K keys x 128 heads, 1465 -> 1482 us;
+// looking every 8 tiles, 1480 us and errors up to 0.007.
 //
 // Masks. Scores of keys a row does not see are selected away by index, whatever they hold. In
 // the PV product such keys meet P = 0, and 0 x NaN is NaN: value slots with a key that some row
@@ -93,8 +93,7 @@ struct ChunkCfg {
   static constexpr float kPOffLog2 = FP8 ? 4.f : 0.f;
   // E4M3: every kWindow tiles the reference also moves down to the largest score of those tiles,
   // if that is more than kLowerLog2 below it, but to no more than kSpanLog2 below its highest value.
-  // Scores that spread by 3.5 natural-log units move it about once in 50 tiles.
-  static constexpr int kWindow = 8;
+  static constexpr int kWindow = 4;
   static constexpr float kLowerLog2 = 4.f, kSpanLog2 = 60.f;
   static_assert(kSlotKeys * kValueChunks * 128 == kCSlot, "value slot");
 };
@@ -714,7 +713,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         }
         float alpha = 1.f;
         bool rescale = false, move = k == 0;
-        const bool look = FP8 && k % Cfg::kWindow == Cfg::kWindow - 1;
+        const bool look = FP8 && k % Cfg::kWindow == Cfg::kWindow - 1 && k + 1 < T;
         if (FP8) {
           recent = fmaxf(recent, mx);
           if (look) mx = recent;
@@ -728,7 +727,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
           if (named_bar_or(sbar, 256, fail)) { stop = true; break; }
           const float* m = mx_s[xp];
           const float rm = fmaxf(fmaxf(mx, m[t ^ 64]), fmaxf(m[t ^ 128], m[t ^ 192]));
-          float nm = fmaxf(ref, rm);
+          float nm = look && (rm - ref) * fabsf(c) <= Cfg::kRescaleLog2 ? ref : fmaxf(ref, rm);
           xp ^= 1;
           if (look && rm != -INFINITY && (ref - rm) * fabsf(c) > Cfg::kLowerLog2)
             nm = fminf(ref, fmaxf(rm, top_s[t] - Cfg::kSpanLog2 / fabsf(c)));
