@@ -42,6 +42,15 @@
  *   of a device error word; mla_decode_check() reads it. Such entries are not
  *   dereferenced out of bounds.
  * - Asynchronous CUDA faults surface at the caller's next synchronisation.
+ *
+ * Rounding of the softmax weights
+ * -------------------------------
+ * Their sum, and lse, are of the unrounded weights; the product with the values rounds them: to
+ * bf16 with the bf16 cache. With the FP8 cache a weight keeps 8 significant bits where it is at
+ * least 2^-4 of the largest among itself and the 4096 keys before it, fewer where it is smaller,
+ * and none below 2^-13 of that (or 2^-60 of the row's largest). So a long even context behind a
+ * strong key keeps its weight, whatever its length; lost are only weights that are small next to
+ * a near one.
  */
 #ifndef MLA_H_
 #define MLA_H_
@@ -245,10 +254,7 @@ size_t mla_chunk_workspace_size(const mla_chunk_params* p, int32_t num_sms);
  * sees the first L_b - n_b + 1 + i keys when causal, else all L_b (a shared prefix). A row that
  * sees no key gets out 0 and lse -inf; rows of q that belong to no sequence are left as they
  * are in out and lse. Keys a row does not see may hold anything, NaN and infinities included.
- * Softmax weights are rounded before the product with the values: to bf16 with the bf16 cache;
- * with the FP8 cache to 8 significant bits where they are at least 2^-10 of the largest weight
- * among the 2048 keys around (fewer bits down to 2^-21 of it, 0 below). Their sum, and lse, are
- * of the unrounded weights.
+ * Softmax weights are rounded before the product with the values as in mla_decode.
  *   q            [T, H, 576] bf16;  out [T, H, 512] bf16 (both 16-byte aligned);
  *                lse [T, H] float32, natural log
  *   cu_q_lens    [B + 1] int32, ascending, within [0, T] (else MLA_DEVERR_CU_Q, nothing written)

@@ -29,7 +29,8 @@
 //               buffer and every key slot in program order.
 //   warp 3      PV issuer (one thread): per tile P^T, then the four value chunk pairs.
 //   FP8 cache (384 threads): the MMAs read the E4M3 cache bytes as TMA landed them
-//   (kind::f8f6f4), q and P entering as two E4M3 terms each (hi and lo).
+//   (kind::f8f6f4), q entering as two E4M3 terms (hi and lo), P as an E4M3 and a smaller
+//   term with a wider range.
 //   16 or 32 rows:
 //   warp 2      key-stage producer (one thread; the warp zeroes tail rows): each tile's
 //               128 whole 576-byte rows into one of two stages, once the PV MMAs of the
@@ -46,8 +47,9 @@
 //   both:
 //   warps 4-7   softmax (one thread per key of the tile = one TMEM lane): scale, causal
 //               mask, online softmax with a lazily-rescaled running max (the reference
-//               max moves only when a score exceeds it by more than 2^8 (FP8: 2^4), so
-//               O^T is rescaled rarely; the final normalisation uses the same reference,
+//               max moves up only when a score exceeds it by more than 2^8 (FP8: 2^4) and,
+//               FP8, down only when a tile stays far below it, so O^T is rescaled rarely;
+//               the final normalisation uses the same reference,
 //               so the result is exact), P^T to shared memory; epilogue (O^T / l ->
 //               output or split partial plus LSE).
 //
@@ -133,10 +135,20 @@ struct Cfg {
   static constexpr int NVS = kValueStages > 0 ? kValueStages : 1;   // barrier arrays
   static constexpr int kKLoaders = FP8 ? 4 : 1;         // arrivals that fill a K slot
   static constexpr int kVLoaders = 1;
-  // FP8: P is computed times 2^kPOffLog2 and written as exact E4M3 hi and lo parts; the
+  // FP8: P is computed times 2^kPOffLog2 and written as two parts: an E4M3 hi and what it leaves,
+  // lo, as E4M3 times 2^5 where the parts have accumulators of their own, else as E5M2; the
   // reference max moves once a score exceeds it by kRescale (log2 units), so P < 2^8 fits
   static constexpr float kPOffLog2 = FP8 ? 4.f : 0.f;
   static constexpr float kRescale = FP8 ? 4.f : kRescaleLog2;
+  // FP8: every kWindow tiles the reference also moves down, if the tile's largest score lies more
+  // than kLowerLog2 below it: to kAboveLog2 above that score, kSpanLog2 at most below its highest.
+  // The normaliser sums the unrounded weights, so that weights too small for the parts are missing
+  // from the result: behind one strong early key the even rest of a long context would be (5 to
+  // 88% of the result for the tests' inputs, 0.2 to 0.5% so). 128 sequences x 4096 keys: 82 -> 84, 96 -> 99 and
+  // 247 -> 251 us for 16, 32 and 64 rows, 1 to 2 us of it the parts and the rest the look at a tile's
+  // maxima, every 8 tiles; with 64 rows every 16 (255 against 260 us) and not in a unit's last tile (251).
+  static constexpr int kWindow = kRawRows ? 8 : 16;
+  static constexpr float kLowerLog2 = 6.f, kAboveLog2 = 2.f, kSpanLog2 = 60.f;
   static_assert(!FP8 || kKTmemBase + NK * kKTmemSlotCols <= 512, "tensor memory budget");
   static_assert(kSlotsPerTile * KC == 9, "a tile is 9 chunks");
   static constexpr int kDynBytes = 1024 + kQBytes + kNumP * kPBytes + (FP8 ? 0 : NK * kKSlotBytes) +
@@ -264,6 +276,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
   __shared__ uint32_t tmem_base_s;
   __shared__ uint32_t abort_s;
   __shared__ __align__(16) float mref_s[RC];
+  __shared__ float top_s[FP8 ? RC : 1];      // a row's highest reference of the unit
   __shared__ float alpha_s[RC], tot_s[RC];
   __shared__ int nvis_s[RC];
   __shared__ __align__(16) float qf_s[RC], rowc_s[RC];   // FP8, 16-32 rows: 2^-e of q, score factors
@@ -608,7 +621,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
                   const uint64_t ad = as + (uint64_t)((2 * pin * 512 + kk * 4 * kVC * 512) >> 4);
                   const uint64_t bd = bh + (uint64_t)((kk * 32 * RC) >> 4);
                   umma_f8(d, ad, bd, idesc_pv, !(k == 0 && kk == 0));        // V . P hi
-                  umma_f8(d, ad, bd + (uint64_t)((128 * RC) >> 4), idesc_pv, 1u);   // V . P lo
+                  umma_f8(d, ad, bd + (uint64_t)((128 * RC) >> 4), idesc_pv | kIdescE5M2B, 1u);   // V . P lo
                 }
               }
               umma_commit(b_vsempty + 8 * st);
@@ -662,6 +675,7 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
       // index), else L; only tiles that reach past L - s_q + 1 (or L) need the mask
       if (t < RC) {
         mref_s[t] = -INFINITY;
+        if (FP8) top_s[t] = -INFINITY;
         nvis_s[t] = a.causal ? min(U.L, U.L - a.s_q + 1 + (row0 + t) / a.H) : U.L;
       }
       const int mask_from = a.causal ? U.L - a.s_q + 1 : U.L;
@@ -749,27 +763,39 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
           }
         }
         bool rescale = false;
-        if (named_bar_or(kSoftmaxBar, 128, need)) {
+        const bool look = FP8 && k % C::kWindow == C::kWindow - 1 && (RC < 64 || k + 1 < T);
+        if (named_bar_or(kSoftmaxBar, 128, need || look)) {
 #pragma unroll
           for (int r = 0; r < RC; ++r) {
             const int m = __reduce_max_sync(0xffffffffu, ordered(s[r]));
             if (lane == (r & 31)) wmax_s[w4 * RC + r] = unordered(m);
           }
           named_bar_sync(kSoftmaxBar, 128);
+          bool moved = true;
           if (t < RC) {
             const float old = mref_s[t];
-            const float nm = fmaxf(fmaxf(old, fmaxf(wmax_s[t], wmax_s[RC + t])),
-                                   fmaxf(wmax_s[2 * RC + t], wmax_s[3 * RC + t]));
+            const float tm = fmaxf(fmaxf(wmax_s[t], wmax_s[RC + t]), fmaxf(wmax_s[2 * RC + t], wmax_s[3 * RC + t]));
+            float nm = fmaxf(old, tm);
+            if (FP8) {
+              if (look && tm <= old + C::kRescale) nm = old;
+              if (look && tm != -INFINITY && old - tm > C::kLowerLog2)
+                nm = fminf(old, fmaxf(tm + C::kAboveLog2, top_s[t] - C::kSpanLog2));
+              top_s[t] = fmaxf(top_s[t], nm);
+            }
             alpha_s[t] = nm == -INFINITY ? 1.f : ex2_approx(old - nm);
             mref_s[t] = nm;
+            moved = nm != old;
+          } else {
+            moved = false;
           }
-          named_bar_sync(kSoftmaxBar, 128);
+          if (FP8) moved = named_bar_or(kSoftmaxBar, 128, moved);
+          else named_bar_sync(kSoftmaxBar, 128);
 #pragma unroll
           for (int r = 0; r < RC; ++r) lsum[r] *= alpha_s[r];
-          rescale = k > 0;
+          rescale = k > 0 && (!FP8 || moved);
         }
         // P^T row of this key, in registers until its buffer is free. bf16: RC / 2 words of
-        // pairs. FP8: P times 2^4 as E4M3 hi bytes (words 0 .. RC / 4 - 1) and lo bytes
+        // pairs. FP8: P times 2^4 as hi bytes (words 0 .. RC / 4 - 1) and lo bytes
         // (the rest), four rows per word.
         uint32_t pw[RC / 2];
 #pragma unroll
@@ -783,7 +809,8 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
             lsum[r + i] += pr[i];   // the normaliser sums the unrounded probabilities
           }
           if constexpr (FP8) {
-            const uint32_t o0 = split_e4m3x2(pr[0], pr[1]), o1 = split_e4m3x2(pr[2], pr[3]);
+            const uint32_t o0 = C::kRawRows ? split_e4m3_lo32x2(pr[0], pr[1]) : split_e4m3_e5m2x2(pr[0], pr[1]);
+            const uint32_t o1 = C::kRawRows ? split_e4m3_lo32x2(pr[2], pr[3]) : split_e4m3_e5m2x2(pr[2], pr[3]);
             pw[r / 4] = __byte_perm(o0, o1, 0x5410);
             pw[RC / 4 + r / 4] = __byte_perm(o0, o1, 0x7632);
           } else {
@@ -881,12 +908,12 @@ decode_kernel(const __grid_constant__ DecodeArgs a) {
           float o[16];
           tmem_ld16(tmem + lane_addr + C::kOBase + jt * C::kNC + 16 * c, o);
           if constexpr (C::kRawRows) {
-            // plus the lo part's columns RC + 16 c ..
+            // plus the lo part's columns RC + 16 c .., which are kSplitLoScale times as large
             float o2[16];
             tmem_ld16(tmem + lane_addr + C::kOBase + jt * C::kNC + RC + 16 * c, o2);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] += o2[i];
+            for (int i = 0; i < 16; ++i) o[i] += o2[i] * (1.f / kSplitLoScale);
           }
           tmem_wait_ld();
 #pragma unroll

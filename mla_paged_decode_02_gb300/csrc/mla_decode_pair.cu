@@ -25,15 +25,19 @@
 // The FP8 cache. The MMAs read the E4M3 bytes of the cache as TMA lands them (kind::f8f6f4,
 // E4M3 x E4M3 with float32 accumulation; the product of two E4M3 values is exact in
 // float32), so no thread converts a key or a value. The other operand of an MMA must then be
-// E4M3 as well; q and P are each written as two E4M3 terms whose sum keeps the precision
+// E4M3 (or E5M2) as well; q and P are each written as two terms whose sum keeps the precision
 // the result needs:
 //   q: this CTA's 64 rows of a unit are scaled per row by a power of two 2^e that puts the
 //      row's largest |q| in [128, 256), and q' = q 2^e is stored as hi = e4m3(q') and
 //      lo = e4m3(q' - hi). For a bf16 q the sum is exact wherever lo stays a normal E4M3
 //      number (|q'| >= 2^-2); smaller entries are off by at most 2^-10 in q' units (2^-17 of
 //      the row's largest). S = K.hi + K.lo, and the softmax multiplies row r by 2^-e_r.
-//   P: computed times 2^4 (so at most 2^8 with the lazy rescale threshold of 2^4 below) and
-//      split the same way from its fp16 rounding: about 8 significant bits, as bf16 P has.
+//   P: computed times 2^4 (so at most 2^8 with the lazy rescale threshold of 2^4 below); its fp16
+//      rounding is stored as hi = e4m3(P) and lo = e5m2(P - hi): 8 significant bits down to 2^-10 of
+//      the reference, as bf16 P has, fewer down to 2^-21, where an E4M3 lo would end at 2^-14.
+//      Every 8 super-tiles the reference also moves down to near the tile's largest score, so that
+//      the many small weights behind one strong key keep their bits: the normaliser sums the
+//      unrounded weights, and what P loses would be missing from the result.
 // Each MMA of the bf16 kernel (K = 16) thus becomes two of K = 32: the same tensor time for
 // half the bytes.
 //
@@ -113,6 +117,11 @@ struct PairCfg {
   static constexpr int kBlockBytes = kSlotBytes;        // bf16: one 64-key value block per slot
   static constexpr float kRescaleLog2 = FP8 ? 4.f : 8.f;  // lazy rescale threshold (log2 units)
   static constexpr float kPOffLog2 = FP8 ? 4.f : 0.f;     // P is computed times 2^kPOffLog2
+  // FP8: every kWindow super-tiles the reference also moves down, if the tile's largest score lies
+  // more than kLowerLog2 below it: to kAboveLog2 above that score, kSpanLog2 at most below its
+  // highest value
+  static constexpr int kWindow = 8;
+  static constexpr float kLowerLog2 = 6.f, kAboveLog2 = 2.f, kSpanLog2 = 60.f;
   static_assert(FP8 || 4 * 8 * kRowBytes * 8 == kBlockBytes, "value block layout");
   static_assert(FP8 || kKeyChunks * 8 * kRowBytes == 2048, "key slot group stride");
   static_assert(kKeySlots * kKeyChunks >= 9, "a tile is 9 chunks");
@@ -235,6 +244,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) decode_pair_kernel(const __gr
   __shared__ uint32_t tmem_base_s, abort_s;
   __shared__ __align__(16) float xbuf[2][2][68];     // [warpgroup][parity]: word 0 flag, words 4..67 values
   __shared__ __align__(16) float mref_s[2][64];
+  __shared__ float top_s[2][FP8 ? 64 : 1];   // a row's highest reference of the unit
   __shared__ __align__(16) float rowc_s[2][64];     // FP8: score factor of each row (log2 units)
   __shared__ float qf_s[64];                        // FP8: 2^-e of this CTA's 64 query rows
   __shared__ float alpha_s[2][64], own_s[2][64];
@@ -718,7 +728,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) decode_pair_kernel(const __gr
                   const uint64_t aj = ad + (uint64_t)((1024 * j + 8192 * kk) >> 4);
                   const uint64_t bk = bd + (uint64_t)((2048 * kk) >> 4);
                   umma_pair_f8(tmem + kOCol + 128 * j, aj, bk, idesc_pv, !(pv.first && kb == 0 && kk == 0));
-                  umma_pair_f8(tmem + kOCol + 128 * j, aj, bk + (8192 >> 4), idesc_pv, 1u);
+                  umma_pair_f8(tmem + kOCol + 128 * j, aj, bk + (8192 >> 4), idesc_pv | kIdescE5M2B, 1u);
                 }
               umma_pair_commit(b_empty + 8 * slot);
               ++r;
@@ -972,6 +982,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) decode_pair_kernel(const __gr
       const int row0 = U.g * 128 + 64 * wg;        // first row of this warpgroup in the sequence
       if (t < 64) {
         mref[t] = -INFINITY;
+        if (FP8) top_s[wg][t] = -INFINITY;
         nvis_s[wg][t] = a.causal ? min(U.L, U.L - a.s_q + 1 + (row0 + t) / a.H) : U.L;
       }
       if constexpr (FP8) {
@@ -1049,7 +1060,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) decode_pair_kernel(const __gr
         // the barrier also orders every thread's S^T reads before the even CTA's signal; the
         // odd CTA's S^T reads precede its P^T signal, which the MMA issuer awaits before it
         // reuses the buffer two tiles later
-        const bool need_local = named_bar_or(bar, 128, need);
+        const bool look = FP8 && k % Cfg::kWindow == Cfg::kWindow - 1;    // the same in both CTAs
+        const bool need_local = named_bar_or(bar, 128, need || look);
         if (leader && t == 0) mbar_arrive(b_sempty + 8 * sb);
         if (need_local) {
           // column maxima of the warp's 32 keys for all 64 rows at once (reduce-scatter,
@@ -1067,18 +1079,28 @@ __global__ void __launch_bounds__(kPairThreads, 1) decode_pair_kernel(const __gr
         const bool need_peer = __float_as_uint(px[0]) != 0u;
         bool rescale = false;
         if (need_local || need_peer) {
+          bool moved = false;
           if (t < 64) {
             const float old = mref[t];
-            float nm = old;
-            if (need_local) nm = fmaxf(nm, own_s[wg][t]);
-            if (need_peer) nm = fmaxf(nm, px[4 + t]);
+            float tm = -INFINITY;
+            if (need_local) tm = own_s[wg][t];
+            if (need_peer) tm = fmaxf(tm, px[4 + t]);
+            float nm = fmaxf(old, tm);
+            if (FP8) {
+              if (look && tm <= old + Cfg::kRescaleLog2) nm = old;
+              if (look && tm != -INFINITY && old - tm > Cfg::kLowerLog2)
+                nm = fminf(old, fmaxf(tm + Cfg::kAboveLog2, top_s[wg][t] - Cfg::kSpanLog2));
+              top_s[wg][t] = fmaxf(top_s[wg][t], nm);
+            }
             alpha_s[wg][t] = nm == -INFINITY ? 1.f : ex2_approx(old - nm);
             mref[t] = nm;
+            moved = nm != old;
           }
-          named_bar_sync(bar, 128);
+          if (FP8) moved = named_bar_or(bar, 128, moved);
+          else named_bar_sync(bar, 128);
 #pragma unroll
           for (int r = 0; r < 64; ++r) lsum[r] *= alpha_s[wg][r];
-          rescale = k > 0;
+          rescale = k > 0 && (!FP8 || moved);
         }
         // bf16: 32 words of P^T pairs. FP8: P times 2^4, its hi bytes (words 0-15) and lo
         // bytes (words 16-31), four rows per word
@@ -1095,7 +1117,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) decode_pair_kernel(const __gr
             lsum[r + i] += p[i];                 // the normaliser sums the unrounded values
           }
           if constexpr (FP8) {
-            const uint32_t o0 = split_e4m3x2(p[0], p[1]), o1 = split_e4m3x2(p[2], p[3]);
+            const uint32_t o0 = split_e4m3_e5m2x2(p[0], p[1]), o1 = split_e4m3_e5m2x2(p[2], p[3]);
             pw[r / 4] = __byte_perm(o0, o1, 0x5410);
             pw[16 + r / 4] = __byte_perm(o0, o1, 0x7632);
           } else {

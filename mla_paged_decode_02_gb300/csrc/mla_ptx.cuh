@@ -258,8 +258,8 @@ __device__ __forceinline__ void umma_commit(uint32_t bar) {
 // B major bit 16, N>>3 at [17,23), M>>4 at [24,29)).
 // ab_bf16: 1 = bf16 operands, 0 = fp16 (kind::f16) or E4M3 (kind::f8f6f4).
 // a_mn / b_mn: 1 = MN-major, 0 = K-major.
-// kind::f8f6f4 takes the formats of A and B apart: kIdescE5M2A makes A's E5M2.
-constexpr uint32_t kIdescE5M2A = 1u << 7;
+// kind::f8f6f4 takes the formats of A and B apart: these make A's or B's E5M2.
+constexpr uint32_t kIdescE5M2A = 1u << 7, kIdescE5M2B = 1u << 10;
 __host__ __device__ constexpr uint32_t make_idesc(uint32_t m, uint32_t n, uint32_t ab_bf16,
                                                   uint32_t a_mn, uint32_t b_mn) {
   return (1u << 4) | (ab_bf16 << 7) | (ab_bf16 << 10) | (a_mn << 15) | (b_mn << 16) |
@@ -314,6 +314,24 @@ __device__ __forceinline__ uint32_t split_e4m3_e5m2x2(float x0, float x1) {
       "cvt.rn.f16x2.e4m3x2 t, hb;\n\t"
       "sub.rn.f16x2 r, h, t;\n\t"
       "cvt.rn.satfinite.e5m2x2.f16x2 lb, r;\n\t"
+      "mov.b32 %0, {hb, lb};\n\t}"
+      : "=r"(out) : "f"(x0), "f"(x1));
+  return out;
+}
+
+// The same with lo as E4M3 times 2^5, for terms that accumulate apart: off by at most 2^-9 x (and
+// 2^-11 x) where hi is a normal number and by 2^-15 below.
+constexpr float kSplitLoScale = 32.f;
+__device__ __forceinline__ uint32_t split_e4m3_lo32x2(float x0, float x1) {
+  uint32_t out;
+  asm("{\n\t.reg .b32 h, t, r, c;\n\t.reg .b16 hb, lb;\n\t"
+      "cvt.rn.f16x2.f32 h, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 hb, h;\n\t"
+      "cvt.rn.f16x2.e4m3x2 t, hb;\n\t"
+      "sub.rn.f16x2 r, h, t;\n\t"
+      "mov.b32 c, 0x50005000;\n\t"
+      "mul.rn.f16x2 r, r, c;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 lb, r;\n\t"
       "mov.b32 %0, {hb, lb};\n\t}"
       : "=r"(out) : "f"(x0), "f"(x1));
   return out;

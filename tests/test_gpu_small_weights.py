@@ -100,6 +100,13 @@ def chunk(c, copies):
                                i32(list(range(copies + 1))), SCALE, c.scale, max_seq_len=c.L)
 
 
+def decode(c, copies):
+    q = c.q[None, None].expand(copies, -1, -1, -1).contiguous()
+    out, lse = api.decode(q, c.cache, c.table.expand(copies, -1).contiguous(), i32([c.L] * copies), SCALE, c.scale,
+                          max_seq_len=c.L)
+    return out[:, 0], lse[:, 0]
+
+
 def wave(H):
     """Scores that wander over 2 to 60 natural-log units."""
     L = 65536
@@ -136,3 +143,21 @@ def test_chunk_attention_with_scores_that_fall_and_rise():
     c = wave(16)
     for copies in (1, 90):
         c.check(*chunk(c, copies))
+
+
+@pytest.mark.parametrize("spread", [0.0, 1.0])
+@pytest.mark.parametrize("where", ["first", "middle", "last", "often"])
+@pytest.mark.parametrize("L", [32768, 131072])
+@pytest.mark.parametrize("H,copies", [(16, 1), (16, 170), (32, 170), (64, 1), (64, 170), (128, 1), (128, 90)])
+def test_decode(H, copies, L, where, spread):
+    """16, 32 and 64 heads (one SM each) and 128 (SM pairs), cut sequences and whole ones."""
+    c = Sink(L, H, place(L, where), spread, seed=L + copies + H)
+    c.check(*decode(c, copies))
+
+
+@pytest.mark.parametrize("H,copies", [(16, 170), (32, 170), (64, 170), (128, 90)])
+def test_decode_with_far_keys_and_wandering_scores(H, copies):
+    c = Sink(32768, H, [3], 1.0, seed=5, gaps=(40.0, 400.0))
+    c.check(*decode(c, copies))
+    c = wave(H)
+    c.check(*decode(c, copies))
