@@ -151,14 +151,13 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       :: "r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(c0), "r"(c1) : "memory");
 }
 
-// An arrival at the cluster's even CTA with the default ordering (release at CTA scope): what it
-// announces lies in the arriving CTA's shared memory, was put there before a proxy fence and a
-// barrier, and is read there, by the arriving SM's tensor core. A release at cluster scope, which
-// also waits for the thread's outstanding global traffic, made the mixed step 6% slower.
-__device__ __forceinline__ void mbar_arrive_cluster_cta(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(bar_cluster) : "memory");
+// Releases earlier writes to this CTA's shared memory, this thread's and those it has acquired, to
+// the cluster: what the odd CTA puts there for the MMAs that the even CTA issues. A release at cluster
+// scope of all memory, which waits for global traffic too, made the mixed step 8% slower.
+__device__ __forceinline__ void fence_release_shared() {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
 }
-// An arrival at the cluster's even CTA that publishes no writes (what it releases was only read).
+// An arrival at the cluster's even CTA that publishes nothing but what a fence before it released.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar_cluster) : "memory");
 }
@@ -190,6 +189,24 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* w, bool wide) {
     q[0] = make_uint4(w[0], w[1], w[2], w[3]);
     q[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
+}
+
+// A first look that acquires at cluster scope, and the rest of such a wait (as wait_longer): for the
+// issuing warps, whose MMAs read what threads of both CTAs wrote.
+__device__ __forceinline__ bool mbar_look_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\t"
+               "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+               "selp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __noinline__ bool wait_longer_cluster(uint32_t bar, uint32_t parity, uint32_t abort_s, uint32_t peer,
+                                                 uint32_t* err, uint64_t limit_ns) {
+  volatile uint32_t* flag = reinterpret_cast<volatile uint32_t*>(__cvta_shared_to_generic(abort_s));
+  const bool ok = mbar_wait_cluster(bar, parity, flag, err, MLA_DEVERR_TIMEOUT, limit_ns);
+  if (!ok) st_cluster_u32(map_to_rank(abort_s, peer), 1u);
+  return ok;
 }
 
 // The rest of a wait that was not over at the first look, out of line: some thirty waits share the
@@ -284,7 +301,6 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
   __shared__ __align__(8) uint64_t bar_kfull[kKRing], bar_kempty[kKRing], bar_vfull[kVRing], bar_vempty[kVRing], bar_aux[kVRing];
   __shared__ __align__(8) uint64_t bar_qfull, bar_qempty, bar_qraw, bar_qsc, bar_qfree;
   __shared__ __align__(8) uint64_t bar_sfull[2], bar_sempty[2], bar_p[2], bar_pv[2], bar_oempty, bar_stat, bar_statfree, bar_drain, bar_never;
-  __shared__ __align__(16) uint32_t sig_s[4];
   __shared__ uint32_t tmem_base_s, abort_s;
   __shared__ float qf_s[64];                 // E4M3: 2^-e of this CTA's rows
   __shared__ float mx_s[2][256], sum_s[256], ref_s[128];
@@ -324,7 +340,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
       mbar_init(b_vempty + 8 * i, 1);
       mbar_init(b_aux + 8 * i, 1);        // a slot that is fixed before it counts as full
     }
-    mbar_init(b_qfull, 1);                // bf16: as b_kfull; E4M3: the converters of both CTAs
+    mbar_init(b_qfull, FP8 ? 2 : 1);      // bf16: as b_kfull; E4M3: the converters of both CTAs
     mbar_init(b_qempty, 1);
     mbar_init(b_qraw, 1);
     mbar_init(b_qsc, 1);
@@ -368,6 +384,12 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
   auto wait_warp = [&](uint32_t bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, mbar_try_wait(bar, parity) ||
                                        wait_longer(bar, parity, smem_u32(&abort_s), peer, err, a.wait_limit_ns));
+  };
+
+  // the same for what the other CTA's threads wrote
+  auto wait_issue = [&](uint32_t bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_look_cluster(bar, parity) ||
+                                       wait_longer_cluster(bar, parity, smem_u32(&abort_s), peer, err, a.wait_limit_ns));
   };
 
   // The launch gives every thread 128 registers. The epilogue's threads hold 256 columns of a row
@@ -521,7 +543,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
               fence_proxy_async_smem();
               __syncwarp();
               if (el) {
-                __threadfence_block();                              // as mbar_arrive_cluster_cta
+                fence_release_shared();
                 mbar_complete_tx_cluster(lb + 8 * slot, kCSlot);   // this CTA's share is in place
               }
             }
@@ -553,7 +575,7 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         for (int u = u0; u < u1 && ok; ++u) {
           const CUnit U = load_cunit(a, u);
           if (U.te == U.tb) continue;
-          ok = wait_warp(b_qfull, uc & 1);
+          ok = wait_issue(b_qfull, uc & 1);
           for (int tile = U.tb; tile < U.te && ok; ++tile, ++n) {
             const uint32_t d = tmem + (n & 1) * 128;
             ok = wait_warp(b_sempty + 8 * (n & 1), ((n >> 1) & 1) ^ 1);
@@ -617,11 +639,11 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
 #pragma unroll 1
             for (int s = 0; s < kHalfSlots * 2 && ok; ++s) {
               if (s % kHalfSlots == 0) {
-                ok = wait_warp(b_p + 8 * (s / kHalfSlots), n & 1);
+                ok = wait_issue(b_p + 8 * (s / kHalfSlots), n & 1);
                 if (!ok) break;
               }
               if (s < ns) {
-                ok = wait_warp(b_vfull + 8 * slot, ph);
+                ok = wait_issue(b_vfull + 8 * slot, ph);
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t vd = dV0 + (uint64_t)(slot * (kCSlot >> 4));
@@ -826,8 +848,12 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
         // a failed wait is carried to the next barrier of all 256 threads
         fail |= named_bar_or(4 + half, 128, fail);
         if (!fail && (t & 191) == 0) {
-          if (leader) mbar_arrive(b_p + 8 * half);
-          else mbar_arrive_cluster_cta(lead(b_p + 8 * half));
+          if (leader) {
+            mbar_arrive(b_p + 8 * half);
+          } else {
+            fence_release_shared();
+            mbar_arrive_cluster_relaxed(lead(b_p + 8 * half));
+          }
         }
       }
       if (stop) break;
@@ -904,9 +930,13 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
       named_bar_sync(ebar, 128);
       if (t == 0) {
         mbar_arrive(b_qsc);
-        // the issuer needs both CTAs' terms: the odd CTA signals by st.async
-        if (leader) mbar_arrive_expect_tx(b_qfull, 16);
-        else st_async_v4(lead(smem_u32(sig_s)), make_uint4(0u, 0u, 0u, 0u), lead(b_qfull));
+        // the issuer needs both CTAs' terms
+        if (leader) {
+          mbar_arrive(b_qfull);
+        } else {
+          fence_release_shared();
+          mbar_arrive_cluster_relaxed(lead(b_qfull));
+        }
       }
       ++uq;
       return true;
