@@ -433,6 +433,8 @@ def chunk_attention(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.
         raise ValueError("out must be a contiguous bf16 [T, H, 512] tensor")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [T, H] tensor")
+    if workspace is not None and not workspace.is_contiguous():     # its size is taken from its elements
+        raise ValueError("workspace must be contiguous")
     scale = kv_scale if kvd == KV_FP8_E4M3 else None
     params = make_chunk_params(B, T, H, P, Np, block_table.shape[1], max_seq_len, kvd, causal)
     handle, at = _addresses(stream, q, kv_cache, block_table, seq_lens, cu_q_lens, scale, out, lse, workspace)

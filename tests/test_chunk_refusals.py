@@ -149,3 +149,12 @@ def test_merge_tensors():
             api.merge_states(**d)
     with pytest.raises(ValueError, match="GPU"):
         api.merge_states(oa, la, oa, la)
+
+
+def test_a_workspace_whose_elements_share_memory():
+    """An expanded tensor has as many elements as the call needs and the memory of one."""
+    q, kv = bf(10, 4, 576), bf(6, 64, 576)
+    bt, sl, cu = torch.zeros((2, 3), dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 28), torch.zeros(1 << 20, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            api.chunk_attention(q, kv, bt, sl, cu, 0.1, max_seq_len=100, workspace=ws)
