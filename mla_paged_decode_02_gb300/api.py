@@ -391,6 +391,8 @@ def rope_cache_write(latent: torch.Tensor, rope: torch.Tensor, positions: torch.
 
 def make_chunk_params(batch, num_tokens, num_heads, page_size, num_pages, max_blocks_per_seq, max_seq_len,
                       kv_dtype, causal=True) -> ChunkParams:
+    if max_seq_len > 0x7FFFFFFF:             # the structure's field would keep its low 32 bits
+        raise ValueError("max_seq_len must be at most 2^20")
     return ChunkParams(int(batch), int(num_tokens), int(num_heads), int(page_size), int(num_pages),
                        int(max_blocks_per_seq), int(max_seq_len), int(kv_dtype), int(bool(causal)))
 

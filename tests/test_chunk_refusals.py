@@ -158,3 +158,13 @@ def test_a_workspace_whose_elements_share_memory():
     for ws in (torch.zeros(1, dtype=torch.uint8).expand(1 << 28), torch.zeros(1 << 20, dtype=torch.uint8)[::2]):
         with pytest.raises(ValueError, match="workspace"):
             api.chunk_attention(q, kv, bt, sl, cu, 0.1, max_seq_len=100, workspace=ws)
+
+
+def test_a_length_bound_beyond_32_bits():
+    """The parameter structure holds 32 bits: 2^32 + 100 must not become 100."""
+    q, kv = bf(10, 4, 576), bf(6, 64, 576)
+    bt, sl, cu = torch.zeros((2, 3), dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="max_seq_len"):
+        api.chunk_attention(q, kv, bt, sl, cu, 0.1, max_seq_len=(1 << 32) + 100)
+    with pytest.raises(ValueError, match="max_seq_len"):
+        api.make_chunk_params(2, 10, 4, 64, 6, 3, (1 << 32) + 100, api.KV_BF16)
