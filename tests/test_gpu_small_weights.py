@@ -161,3 +161,46 @@ def test_decode_with_far_keys_and_wandering_scores(H, copies):
     c.check(*decode(c, copies))
     c = wave(H)
     c.check(*decode(c, copies))
+
+
+def causal_check(c, q, out, lse):
+    """Rows of the last n tokens, each over the keys up to its own."""
+    n = q.shape[0]
+    v = c.k[:, :512]
+    sums = torch.cat([torch.zeros((1, 512), dtype=torch.float64, device="cuda"), v.abs().cumsum(0)])
+    most = (sums[2048:] - sums[:-2048]).amax(0)
+    for i in range(n):
+        vis = c.L - n + 1 + i
+        s = (q[i].double() @ c.k[:vis].T) * SCALE
+        rl = torch.logsumexp(s, dim=1)
+        w = torch.exp(s - rl[:, None])
+        r, A = w @ v[:vis], w @ v[:vis].abs()
+        err = (out[i].double() - r).abs()
+        bound = 1.05 * (2.0 ** -8 * (A + r.abs()) + 2.0 ** -11 * A + 2.0 ** -18 * w[:, c.strong].sum(1, keepdim=True) * most) + 1e-6
+        assert (err <= bound).all(), (i, (err - bound).max().item())
+        assert (lse[i].double() - rl).abs().max().item() <= LSE_ABS[F8]
+
+
+@pytest.mark.parametrize("where", ["first", "middle"])
+@pytest.mark.parametrize("H,n,copies", [(16, 150, 1), (16, 150, 6), (3, 300, 4), (128, 9, 10)])
+def test_chunk_attention_of_many_causal_tokens(H, n, copies, where):
+    """Rows that see different numbers of keys share a block, and its last tiles are masked."""
+    c = Sink(9001, H, place(9001, where), 1.0, seed=n + H)
+    gain = torch.linspace(0.7, 1.2, n, device="cuda")[:, None, None]
+    q = (c.q.float()[None] * gain).to(torch.bfloat16)
+    out, lse = api.chunk_attention(q.repeat(copies, 1, 1), c.cache, c.table.expand(copies, -1).contiguous(),
+                                   i32([c.L] * copies), i32([n * b for b in range(copies + 1)]), SCALE, c.scale, max_seq_len=c.L)
+    for b in range(copies):
+        causal_check(c, q, out[n * b:n * (b + 1)], lse[n * b:n * (b + 1)])
+
+
+@pytest.mark.parametrize("where", ["first", "middle"])
+@pytest.mark.parametrize("H,n,copies", [(8, 2, 170), (16, 2, 170), (16, 4, 170), (128, 3, 90), (128, 3, 1)])
+def test_decode_of_several_tokens(H, n, copies, where):
+    c = Sink(9001, H, place(9001, where), 1.0, seed=n + H + 1)
+    gain = torch.linspace(0.7, 1.2, n, device="cuda")[:, None, None]
+    q = (c.q.float()[None] * gain).to(torch.bfloat16)
+    out, lse = api.decode(q[None].repeat(copies, 1, 1, 1), c.cache, c.table.expand(copies, -1).contiguous(),
+                          i32([c.L] * copies), SCALE, c.scale, max_seq_len=c.L)
+    for b in range(0, copies, 13):
+        causal_check(c, q, out[b], lse[b])
