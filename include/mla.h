@@ -254,7 +254,9 @@ size_t mla_chunk_workspace_size(const mla_chunk_params* p, int32_t num_sms);
  * sees the first L_b - n_b + 1 + i keys when causal, else all L_b (a shared prefix). A row that
  * sees no key gets out 0 and lse -inf; rows of q that belong to no sequence are left as they
  * are in out and lse. Keys a row does not see may hold anything, NaN and infinities included.
- * Softmax weights are rounded before the product with the values as in mla_decode.
+ * Softmax weights are rounded before the product with the values as in mla_decode. A key that a
+ * row sees with a score of -infinity has weight 0; if its value is not finite as well, the row's
+ * result may be NaN or leave the key out.
  *   q            [T, H, 576] bf16;  out [T, H, 512] bf16 (both 16-byte aligned);
  *                lse [T, H] float32, natural log
  *   cu_q_lens    [B + 1] int32, ascending, within [0, T] (else MLA_DEVERR_CU_Q, nothing written)

@@ -551,7 +551,8 @@ MLA_EXPORT mla_status mla_chunk_attention(const mla_chunk_params* p, const void*
   sa.workers = pairs;
   // a block's set-up (its q, the softmax before the first PV, its results) costs about 0.6 tiles
   // with the bf16 cache, more with E4M3, whose q is split first; prompts of 150 to 2000 tokens
-  // with 16 heads: 226, 179, 188 us for 0, 1, 2 (bf16)
+  // with 16 heads: 226, 179, 188 us for 0, 1, 2 (bf16), 324, 227 to 273, 206 to 217, 212 to 258 for
+  // 0, 1, 2, 3 (E4M3; the mixed step 99, 99, 98, 99, single tokens alone 64, 61, 63, 64)
   sa.setup = fp8 ? 2 : 1;
   sa.tokens = p->num_tokens;
   ChunkArgs ca;

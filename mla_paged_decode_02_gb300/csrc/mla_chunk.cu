@@ -19,8 +19,7 @@
 //
 // Shared memory per CTA: 64 query rows (72 KB), P (64 rows x 256 keys, 32 KB), and seven 16 KB slots
 // in two rings: keys (128 keys x 128 bytes of the row) and values (this CTA's 256 columns of 32 or,
-// E4M3, 64 keys). The 512-byte value pieces come from L2: the peer has
-// just read those keys.
+// E4M3, 64 keys). The 512-byte value pieces come from L2: the peer has just read those keys.
 //
 // Two issuing warps, each with a ring and a producer, so that QK^T of tile n + 1 (of the next unit
 // too) overlaps the softmax and PV of tile n. They stay converged, every lane waiting and one
@@ -38,8 +37,9 @@
 // score of those 1024 keys, when that lies more than 2^4 below it; O and l grow instead (float32
 // holds the 2^60 that the reference may fall in all). Few keys' weights are then of few bits, however
 // many there are: with strong keys 6 to 13 natural-log units above 32 K and 128 K others the 2-norm of
-// the error was 0.05 to 0.86 of the result and is 0.002 to 0.004. 32 K keys x 128 heads, 1465 -> 1482 us;
-// looking every 8 tiles, 1480 us and errors up to 0.007.
+// the error is 0.002 to 0.004 of the result (0.05 to 0.86 with two E4M3 terms and a reference that only
+// rises). 128-token pieces x 128 heads over 32 K keys take 1482 us so and 1465 without; looking every 8
+// tiles, 1480 us and errors up to 0.007.
 //
 // Masks. Scores of keys a row does not see are selected away by index, whatever they hold. In
 // the PV product such keys meet P = 0, and 0 x NaN is NaN: value slots with a key that some row
@@ -53,10 +53,15 @@
 // epilogue. Every wait is bounded; a stall sets the device error word, and both CTAs drain and
 // leave through a cluster barrier.
 //
-// Bound by the tensor cores: 512 tokens x 128 heads over 8 K keys, bf16, 618 us cold (1950 TFLOP/s,
-// tensor cycles 88% busy) and 0.64-0.74 ms one after another under the power limit; 32 K keys,
-// E4M3, 1295 us cold (93%). Short causal blocks are bound by what a block adds at its ends: 8 prompts
-// of 150 to 2000 tokens x 16 heads, 14 blocks per pair, 170 us (58%).
+// Ordering between the CTAs. What a thread of the odd CTA writes for the MMAs (P, value slots put
+// right, the terms of q) it releases at cluster scope, and the issuing warps acquire at that scope.
+// Signals that a tensor-memory buffer was read are relaxed: they publish no memory, and the reads
+// have completed (tcgen05.wait::ld) before them.
+//
+// Bound by the tensor cores: 512 tokens x 128 heads over 8 K keys, bf16, 627 us cold (1920 TFLOP/s,
+// tensor cycles 88% busy) and 0.70-0.73 ms one after another under the power limit; 128-token
+// pieces x 128 heads over 32 K keys, E4M3, 1316 us cold (93%). Short causal blocks are bound by what a
+// block adds at its ends: 8 prompts of 150 to 2000 tokens x 16 heads, 14 blocks per pair, 169 us (58%).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include "mla_chunk.h"
@@ -87,7 +92,8 @@ struct ChunkCfg {
   static constexpr int kSlotKeys = FP8 ? 64 : 32;        // keys of a value slot
   static constexpr int kValueChunks = FP8 ? 2 : 4;       // 128-byte pieces of its rows
   // a tile takes 9 key and 8 value slots (bf16) or 5 and 4; the better split of the seven, measured
-  // against 4 + 3 and 3 + 4: bf16 prompts 188 -> 181 us, E4M3 mixed step 102 against 106 us
+  // against 4 + 3 and 3 + 4: bf16 prompts 188 -> 181 us; E4M3 mixed step 98 against 103 us, prompts
+  // 206 to 217 against 240, single tokens alone 63 against 66, 32 K keys x 128 heads 1453 against 1474
   static constexpr int kKRing = FP8 ? 4 : 3, kVRing = kCSlots - kKRing;
   static constexpr float kRescaleLog2 = FP8 ? 4.f : 8.f;
   static constexpr float kPOffLog2 = FP8 ? 4.f : 0.f;
@@ -165,7 +171,7 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// zero over the non-finite values of 16 bytes
+// zero over the non-finite values of 4 bytes
 template <bool FP8>
 __device__ __forceinline__ uint32_t finite_word(uint32_t w) {
   if (FP8) {
@@ -432,8 +438,8 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
           const int next_rows = tile + 1 < U.te ? tile_row(a, U, tile + 1, lane) : 0;
           const int r0 = __shfl_sync(0xffffffffu, rows, 16 * (int)rank), r1 = __shfl_sync(0xffffffffu, rows, 16 * (int)rank + 8);
           const int row = __shfl_sync(0xffffffffu, rows, 16 * (int)rank + (lane < nk ? lane * (kbox >> 3) : 0));
-  #pragma unroll 1
-        for (int c = 0; c < KS; ++c) {
+#pragma unroll 1
+          for (int c = 0; c < KS; ++c) {
             ok = wait_warp(b_kempty + 8 * slot, ph);
             if (!ok) break;
             const uint32_t dst = sK + slot * kCSlot, bar = lb + 8 * slot;
