@@ -157,17 +157,6 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
       :: "r"(dst), "l"(reinterpret_cast<uint64_t>(m)), "r"(bar_cluster), "r"(c0), "r"(c1) : "memory");
 }
 
-// Releases earlier writes to this CTA's shared memory, this thread's and those it has acquired, to
-// the cluster: what the odd CTA puts there for the MMAs that the even CTA issues. A release at cluster
-// scope of all memory, which waits for global traffic too, made the mixed step 8% slower.
-__device__ __forceinline__ void fence_release_shared() {
-  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
-}
-// An arrival at the cluster's even CTA that publishes nothing but what a fence before it released.
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar_cluster) : "memory");
-}
-
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 

@@ -237,7 +237,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) decode_pair_kernel(const __gr
   // factors written and read
   __shared__ __align__(8) uint64_t bar_qraw, bar_qready, bar_qsc, bar_qfree;
   __shared__ __align__(8) uint64_t bar_ktfull, bar_ktempty;   // FP8: the key tile
-  __shared__ __align__(16) uint32_t sig_s[4];        // landing place of the odd CTA's 16-byte signals
   __shared__ __align__(8) uint64_t bar_sfull[2], bar_sempty[2], bar_pfull, bar_pin, bar_pvdone, bar_oempty;
   __shared__ __align__(8) uint64_t bar_x[2][2];
   __shared__ __align__(8) uint64_t bar_drain, bar_never;
@@ -293,7 +292,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) decode_pair_kernel(const __gr
     mbar_init(b_qfull, 1);                // bf16: the even CTA's arrival, with both CTAs' bytes
     mbar_init(b_qempty, 1);
     mbar_init(b_qraw, 1);                 // FP8: this CTA's producer, with its bytes
-    mbar_init(b_qready, 1);               // FP8: the even CTA's converters, expecting the odd CTA's 16-byte signal
+    mbar_init(b_qready, 2);               // FP8: the converters of both CTAs
     mbar_init(b_qsc, 1);                  // FP8: this CTA's converters
     mbar_init(b_qfree, 1);                // FP8: the softmax warpgroup of this CTA's rows
     mbar_init(b_ktfull, 1);               // FP8: the even CTA's producer, with both CTAs' bytes
@@ -333,6 +332,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) decode_pair_kernel(const __gr
   auto fail_peer = [&]() { st_cluster_u32(map_to_rank(smem_u32(&abort_s), peer), 1u); };
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
     const bool ok = mbar_wait(bar, parity, abort_flag, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns);
+    if (!ok) fail_peer();
+    return ok;
+  };
+
+  // the same for what threads of the other CTA wrote
+  auto wait_cluster = [&](uint32_t bar, uint32_t parity) -> bool {
+    const bool ok = mbar_wait_cluster(bar, parity, abort_flag, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns);
     if (!ok) fail_peer();
     return ok;
   };
@@ -704,7 +710,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) decode_pair_kernel(const __gr
           uint32_t uc;
         } prev{0, -1, false, 0};
         auto issue_pv = [&](const Prev& pv) -> bool {
-          if (!wait(b_pfull, pvn & 1)) return false;
+          if (!wait_cluster(b_pfull, pvn & 1)) return false;
           if (FP8) fence_proxy_async_smem();   // P^T rows that came from the peer by st.async
           if (pv.first && !wait(b_oempty, (pv.uc & 1) ^ 1)) return false;
           if constexpr (FP8) {
@@ -714,7 +720,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) decode_pair_kernel(const __gr
               if (valid <= 0) break;
               const int ksteps = valid >= 64 ? 2 : (valid + 31) / 32;
               const uint32_t slot = r % kVRing;
-              if (!wait(b_full + 8 * slot, (r / kVRing) & 1)) return false;
+              if (!wait_cluster(b_full + 8 * slot, (r / kVRing) & 1)) return false;
               tc_fence_after();
               const uint64_t ad = dV0 + (uint64_t)((slot * kVBlockBytes) >> 4);
               // P^T of block kb: key half kb / 2, keys 64 (kb % 2) .. of it; lo 8 KB after hi
@@ -743,7 +749,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) decode_pair_kernel(const __gr
             if (valid <= 0) break;
             const int ksteps = valid >= 64 ? 4 : (valid + 15) / 16;
             const uint32_t slot = r % kRing;
-            if (!wait(b_full + 8 * slot, (r / kRing) & 1)) return false;
+            if (!wait_cluster(b_full + 8 * slot, (r / kRing) & 1)) return false;
             tc_fence_after();
             const uint64_t ad = dV0 + (uint64_t)((slot * kSlotBytes) >> 4);
             const uint64_t bd = dP0 + (uint64_t)((64 * kb * 128) >> 4);
@@ -765,7 +771,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) decode_pair_kernel(const __gr
         };
         for (int u = u0; u < u1 && ok; ++u, ++uc) {
           const PUnit U = load_punit(a, u);
-          ok = wait(FP8 ? b_qready : b_qfull, uc & 1);   // FP8: hi and lo written in both CTAs
+          // FP8: hi and lo written in both CTAs
+          ok = FP8 ? wait_cluster(b_qready, uc & 1) : wait(b_qfull, uc & 1);
           for (int k = 0; k < U.te - U.tb && ok; ++k, ++n) {
             const uint32_t sb = n & 1, sph = (n >> 1) & 1;   // S^T buffer
             ok = wait(b_sempty + 8 * sb, sph ^ 1);
@@ -890,9 +897,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) decode_pair_kernel(const __gr
         named_bar_sync(cbar, 64);
         if (threadIdx.x == 64) {
           mbar_arrive(b_qsc);
-          // the even CTA's MMA issuer needs both CTAs' Q: the odd CTA signals by st.async
-          if (leader) mbar_arrive_expect_tx(b_qready, 16);
-          else st_async_v4(lead(smem_u32(sig_s)), make_uint4(0u, 0u, 0u, 0u), lead(b_qready));
+          // the even CTA's MMA issuer needs both CTAs' Q
+          if (leader) {
+            mbar_arrive(b_qready);
+          } else {
+            fence_release_shared();
+            mbar_arrive_cluster_relaxed(lead(b_qready));
+          }
         }
       }
     }

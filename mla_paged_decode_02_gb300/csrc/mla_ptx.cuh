@@ -486,6 +486,16 @@ __device__ __forceinline__ void mbar_complete_tx_cluster(uint32_t bar_cluster, u
                : "memory");
 }
 __device__ __forceinline__ void fence_acq_rel_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+// Releases earlier writes to this CTA's shared memory, this thread's and those it has acquired, to
+// the cluster: what the odd CTA puts there for the MMAs that the even CTA issues. A release at cluster
+// scope of all memory, which waits for global traffic too, made the mixed step 8% slower.
+__device__ __forceinline__ void fence_release_shared() {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
+// An arrival at the cluster's even CTA that publishes nothing but what a fence before it released.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(bar_cluster) : "memory");
+}
 }  // namespace mla
 
 namespace mla {
