@@ -480,7 +480,7 @@ __device__ __forceinline__ void umma_pair_commit(uint32_t bar) {
 
 namespace mla {
 // Counts `tx` bytes as arrived on an mbarrier of either CTA without an arrival; the caller
-// orders its earlier writes first (fence_acq_rel_cluster).
+// orders its earlier writes first (fence_acq_rel_cluster or fence_release_shared).
 __device__ __forceinline__ void mbar_complete_tx_cluster(uint32_t bar_cluster, uint32_t tx) {
   asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" :: "r"(bar_cluster), "r"(tx)
                : "memory");
