@@ -186,16 +186,8 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* w, bool wide) {
   }
 }
 
-// A first look that acquires at cluster scope, and the rest of such a wait (as wait_longer): for the
-// issuing warps, whose MMAs read what threads of both CTAs wrote.
-__device__ __forceinline__ bool mbar_look_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\t"
-               "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-               "selp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
-  return ok != 0;
-}
+// The rest of a wait that acquires at cluster scope (as wait_longer): for the issuing warps, whose MMAs
+// read what threads of both CTAs wrote.
 __device__ __noinline__ bool wait_longer_cluster(uint32_t bar, uint32_t parity, uint32_t abort_s, uint32_t peer,
                                                  uint32_t* err, uint64_t limit_ns) {
   volatile uint32_t* flag = reinterpret_cast<volatile uint32_t*>(__cvta_shared_to_generic(abort_s));

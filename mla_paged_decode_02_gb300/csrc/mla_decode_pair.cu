@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) decode_pair_kernel(const __gr
         auto issue_pv = [&](const Prev& pv) -> bool {
           if (!wait_cluster(b_pfull, pvn & 1)) return false;
           if (FP8) fence_proxy_async_smem();   // P^T rows that came from the peer by st.async
-          if (pv.first && !wait(b_oempty, (pv.uc & 1) ^ 1)) return false;
+          if (pv.first && !wait_cluster(b_oempty, (pv.uc & 1) ^ 1)) return false;
           if constexpr (FP8) {
             // value blocks of 64 keys from the ring of two
             for (int kb = 0; kb < 4; ++kb) {
@@ -772,14 +772,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) decode_pair_kernel(const __gr
         for (int u = u0; u < u1 && ok; ++u, ++uc) {
           const PUnit U = load_punit(a, u);
           // FP8: hi and lo written in both CTAs
-          ok = FP8 ? wait_cluster(b_qready, uc & 1) : wait(b_qfull, uc & 1);
+          ok = wait_cluster(FP8 ? b_qready : b_qfull, uc & 1);
           for (int k = 0; k < U.te - U.tb && ok; ++k, ++n) {
             const uint32_t sb = n & 1, sph = (n >> 1) & 1;   // S^T buffer
-            ok = wait(b_sempty + 8 * sb, sph ^ 1);
+            ok = wait_cluster(b_sempty + 8 * sb, sph ^ 1);
             const uint32_t d = tmem + sb * 128;
             if constexpr (FP8) {
               // the whole key tile: 9 chunks x 2 K steps, each K . hi then K . lo
-              ok = ok && wait(b_ktfull, nkt & 1);
+              ok = ok && wait_cluster(b_ktfull, nkt & 1);
               if (!ok) break;
               tc_fence_after();
 #pragma unroll
@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) decode_pair_kernel(const __gr
             for (int ks = 0; !FP8 && ks < kKeySlots && ok; ++ks) {
               const int nc = 9 - KC * ks < KC ? 9 - KC * ks : KC;   // chunks KC ks .. (the last slot: 8)
               const uint32_t slot = r % kRing;
-              ok = wait(b_full + 8 * slot, (r / kRing) & 1);
+              ok = wait_cluster(b_full + 8 * slot, (r / kRing) & 1);
               if (!ok) break;
               tc_fence_after();
               const uint64_t ad = dK0 + (uint64_t)(slot * (kSlotBytes >> 4));

@@ -384,10 +384,19 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
                : "=r"(ok) : "r"(bar), "r"(parity), "r"(hint_ns) : "memory");
   return ok != 0;
 }
+// The same without a time of its own: the first look of a wait.
+__device__ __forceinline__ bool mbar_look_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\t"
+               "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+               "selp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
                                                   uint32_t* err_word, uint32_t timeout_bit,
                                                   uint64_t limit_ns = kWaitLimitNs) {
-  if (mbar_try_wait_cluster(bar, parity, 0)) return true;
+  if (mbar_look_cluster(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   for (;;) {
     if (mbar_try_wait_cluster(bar, parity, kSleepHintNs)) return true;
