@@ -375,8 +375,10 @@ __global__ void __launch_bounds__(kCThreads, 1) chunk_kernel(const __grid_consta
 
   // the same for what the other CTA's threads wrote
   auto wait_issue = [&](uint32_t bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_look_cluster(bar, parity) ||
-                                       wait_longer_cluster(bar, parity, smem_u32(&abort_s), peer, err, a.wait_limit_ns));
+    const bool ok = __all_sync(0xffffffffu, mbar_look_cluster(bar, parity) ||
+                                                wait_longer_cluster(bar, parity, smem_u32(&abort_s), peer, err, a.wait_limit_ns));
+    fence_acquire_shared();
+    return ok;
   };
 
   // The launch gives every thread 128 registers. The epilogue's threads hold 256 columns of a row

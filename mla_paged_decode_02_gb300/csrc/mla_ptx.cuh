@@ -375,20 +375,28 @@ __device__ __forceinline__ void mbar_arrive_expect_tx_cluster(uint32_t bar_clust
   asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;"
                :: "r"(bar_cluster), "r"(tx) : "memory");
 }
-// A parity wait that acquires at cluster scope (for data another CTA wrote before arriving).
+// Acquires what other CTAs of the cluster released in shared memory, after a relaxed wait has seen
+// their arrival. An acquire of all memory in every wait of the issuing threads cost 0.5 to 1%
+// (128-head bf16 batch 363.3 us, 8 bf16 prompts of the chunk attention 180.0); this one 361.1 and 178.6,
+// no more than waits at CTA scope.
+__device__ __forceinline__ void fence_acquire_shared() {
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+}
+// A look at a parity for at most `hint_ns` (for data another CTA wrote before arriving: relaxed, the
+// acquire is a fence after it).
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity, uint32_t hint_ns) {
   uint32_t ok;
   asm volatile("{\n\t.reg .pred p;\n\t"
-               "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+               "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
                "selp.u32 %0, 1, 0, p;\n\t}"
                : "=r"(ok) : "r"(bar), "r"(parity), "r"(hint_ns) : "memory");
   return ok != 0;
 }
-// The same without a time of its own: the first look of a wait.
+// The same without a time of its own, the first look of a wait.
 __device__ __forceinline__ bool mbar_look_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile("{\n\t.reg .pred p;\n\t"
-               "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+               "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
                "selp.u32 %0, 1, 0, p;\n\t}"
                : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
@@ -396,10 +404,16 @@ __device__ __forceinline__ bool mbar_look_cluster(uint32_t bar, uint32_t parity)
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile uint32_t* abort_flag,
                                                   uint32_t* err_word, uint32_t timeout_bit,
                                                   uint64_t limit_ns = kWaitLimitNs) {
-  if (mbar_look_cluster(bar, parity)) return true;
+  if (mbar_look_cluster(bar, parity)) {
+    fence_acquire_shared();
+    return true;
+  }
   const uint64_t t0 = global_timer_ns();
   for (;;) {
-    if (mbar_try_wait_cluster(bar, parity, kSleepHintNs)) return true;
+    if (mbar_try_wait_cluster(bar, parity, kSleepHintNs)) {
+      fence_acquire_shared();
+      return true;
+    }
     if (*abort_flag) return false;
     if (global_timer_ns() - t0 > limit_ns) {
       *abort_flag = 1u;
