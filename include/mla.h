@@ -87,8 +87,8 @@ typedef enum { MLA_KV_BF16 = 0, MLA_KV_FP8_E4M3 = 1 } mla_kv_dtype;
 #define MLA_DEVERR_Q_RANGE       0x4u   /* FP8 cache, 33-64 rows: |q| above the float16 range */
 #define MLA_DEVERR_TIMEOUT       0x8u   /* a bounded pipeline wait expired */
 #define MLA_DEVERR_SLOT          0x10u  /* cache write: slot >= num_pages*page_size */
-#define MLA_DEVERR_CU_Q          0x20u  /* chunk attention: cu_q_lens do not ascend within the rows of q */
-#define MLA_DEVERR_POSITION      0x40u  /* rotating cache write: position >= max_pos */
+#define MLA_DEVERR_CU_Q          0x20u  /* ragged batches: cu_q_lens do not ascend within the rows of q */
+#define MLA_DEVERR_POSITION      0x40u  /* rotating cache writes: position >= max_pos */
 
 typedef struct mla_decode_params {
   int32_t batch;               /* B >= 1 */
@@ -285,6 +285,119 @@ mla_status mla_chunk_attention(const mla_chunk_params* p, const void* q, const v
 mla_status mla_merge_states(const void* out_a, const float* lse_a, const void* out_b,
                             const float* lse_b, int64_t num_rows, void* out, float* lse,
                             mla_stream_t stream);
+
+/* ---- Block-sparse attention: attention to the blocks that a cheap score selects ---------
+ * A model with an indexer keeps, beside the latent cache, a cache of small index keys: 128
+ * E4M3 values and a float32 scale for each token, in pages like the latent cache's (the same block
+ * table serves both). Each new token scores the blocks of its context with its index queries, the
+ * best blocks are selected, and the token attends to those alone. A block is `block_size` tokens
+ * of a sequence: a multiple of 8 that divides the page, so that it lies in one page. */
+
+/* Cache write of new tokens' index keys, and their index queries, with the position rotation on
+ * the way. Of a row x of 128 (a key, or one head of a query) the last 64 values are turned as in
+ * mla_rope_cache_write; then scale = max(max|x| / 448, 2^-126) and code = e4m3(x / scale), IEEE
+ * float32 quotients, rounded to nearest even. A row with a value that is not finite gets a NaN scale
+ * (and never a score above -infinity).
+ *   keys          rows of 128 bf16, key_stride elements apart (a multiple of 8), 16-byte aligned
+ *   positions, cos_sin, max_pos, interleaved, slot_mapping   as mla_rope_cache_write; slots >= 0
+ *                 are distinct
+ *   index_cache   [Np, P, 128] e4m3fn bytes;  index_scale [Np, P] float32: the key's, by slot
+ *   queries       128 bf16 at token t and head h: q_token_stride t + q_head_stride h elements on
+ *                 (strides a multiple of 8);  weights [N, num_heads] float32
+ *   q_index       [N, num_heads, 128] e4m3fn bytes;  q_weights [N, num_heads] float32: the head's
+ *                 weight times its query's scale. All four NULL: no queries. 1..128 heads
+ *   device_error  as mla_rope_cache_write
+ * One launch on `stream`; no synchronisation. */
+mla_status mla_index_cache_write(const void* keys, int64_t key_stride, const int64_t* positions,
+                                 const float* cos_sin, int32_t max_pos, int32_t interleaved,
+                                 const int64_t* slot_mapping, int32_t num_tokens,
+                                 void* index_cache, float* index_scale, int32_t num_pages,
+                                 int32_t page_size, const void* queries, int64_t q_token_stride,
+                                 int64_t q_head_stride, const float* weights, int32_t num_heads,
+                                 void* q_index, float* q_weights, uint32_t* device_error,
+                                 mla_stream_t stream);
+
+typedef struct mla_index_params {
+  int32_t batch;               /* B >= 1 sequences */
+  int32_t num_tokens;          /* T, 0..2^20: new tokens, with rows that belong to no sequence */
+  int32_t num_heads;           /* index heads, 1..128 */
+  int32_t page_size;           /* P: a multiple of 8, at most 1024 (else UNSUPPORTED) */
+  int32_t num_pages;           /* Np: pages in the pool */
+  int32_t max_blocks_per_seq;  /* MB: row stride of block_table */
+  int32_t max_seq_len;         /* host-known upper bound on seq_lens[], <= 2^20 */
+  int32_t block_size;          /* a multiple of 8 that divides P (else UNSUPPORTED) */
+  int32_t causal;              /* 0 or 1 */
+} mla_index_params;
+
+/* Scores of the blocks of each new token's context. Sequences, offsets, lengths and the keys
+ * a token sees are as in mla_chunk_attention. With k_j the codes and s_j the scale of key j,
+ *   score_j = s_j sum_h q_weights[t][h] max(0, q_index[t][h] . k_j)
+ *   scores[t][c] = max of score_j over the keys j of block c that token t sees, c < C,
+ * C = ceil(max_seq_len / block_size); -infinity for a block without such a key. A score that is NaN
+ * counts as -infinity. Keys a token does not see may hold anything. Rows that belong to no sequence
+ * are left as they are.
+ *   q_index, index_cache, index_scale   as written by mla_index_cache_write, 16-byte aligned
+ *   scores        [T, C] float32
+ *   device_error  optional device uint32 into which MLA_DEVERR_CU_Q (offsets that do not ascend:
+ *                 what is written is undefined, but within the T rows), MLA_DEVERR_SEQ_LEN (the
+ *                 length is clamped) and MLA_DEVERR_BLOCK_TABLE (page 0 is read) are OR-ed
+ * No synchronisation. */
+mla_status mla_index_scores(const mla_index_params* p, const void* q_index, const float* q_weights,
+                            const void* index_cache, const float* index_scale,
+                            const int32_t* block_table, const int32_t* seq_lens,
+                            const int32_t* cu_q_lens, float* scores, uint32_t* device_error,
+                            mla_stream_t stream);
+
+/* Selects blocks for each new token. A token that sees n keys (as in mla_chunk_attention) has
+ * ceil(n / block_size) blocks, num_blocks at most. Selected are min(top_k, that) of them: its first
+ * keep_first and its latest keep_last blocks (keep_first + keep_last <= top_k), then those with the
+ * largest scores, equal scores (-0 and +0 are) by the lower index, NaN as -infinity. They are written
+ * in ascending order, -1 behind them. Rows that belong to no sequence are left as they are.
+ *   scores        [T, num_blocks] float32, rows scores_stride elements apart; those past a token's
+ *                 blocks are not used
+ *   selected      [T, top_k] int32
+ *   device_error  as mla_index_scores (MLA_DEVERR_CU_Q, MLA_DEVERR_SEQ_LEN)
+ * num_blocks, top_k and block_size up to 2^20. One launch on `stream`; no synchronisation. */
+mla_status mla_select_blocks(const float* scores, int64_t scores_stride, int32_t num_tokens,
+                             int32_t num_blocks, const int32_t* seq_lens, const int32_t* cu_q_lens,
+                             int32_t batch, int32_t block_size, int32_t top_k, int32_t keep_first,
+                             int32_t keep_last, int32_t causal, int32_t* selected,
+                             uint32_t* device_error, mla_stream_t stream);
+
+typedef struct mla_sparse_params {
+  int32_t batch;               /* as mla_index_params, with num_heads query heads: */
+  int32_t num_tokens;
+  int32_t num_heads;           /* H, 1..65536; T * H <= 2^30 */
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t max_blocks_per_seq;
+  int32_t max_seq_len;
+  int32_t block_size;
+  int32_t top_k;               /* entries of a token's list, 1..2^20 */
+  int32_t kv_dtype;            /* mla_kv_dtype */
+  int32_t causal;              /* 0 or 1 */
+} mla_sparse_params;
+
+/* Workspace bytes mla_sparse_attention needs (num_sms <= 0: the current device's count). 0 on
+ * invalid params. Does not depend on the contents of any tensor. */
+size_t mla_sparse_workspace_size(const mla_sparse_params* p, int32_t num_sms);
+
+/* mla_chunk_attention of which each new token sees only the keys of its selected blocks. All heads
+ * of a token share its list. The list is a set: its order does not matter, an index given twice counts
+ * once, and one that names no block with a key the token sees (-1 among them) is left out. A token
+ * without any key gets out 0 and lse -inf.
+ *   selected     [T, top_k] int32, as mla_select_blocks writes it
+ *   workspace    >= mla_sparse_workspace_size(p, 0) bytes, 256-byte aligned; mla_decode_check reads
+ *                its error word. Calls that may overlap on the GPU, captured graphs among them,
+ *                need workspaces of their own.
+ *   the rest     as mla_chunk_attention (device errors too; only pages of selected blocks are read)
+ * Launches a plan, the attention kernel and the merge of split blocks on `stream`; returns without
+ * synchronising. */
+mla_status mla_sparse_attention(const mla_sparse_params* p, const void* q, const void* kv_cache,
+                                const int32_t* block_table, const int32_t* seq_lens,
+                                const int32_t* cu_q_lens, const int32_t* selected,
+                                float softmax_scale, const float* kv_scale, void* out, float* lse,
+                                void* workspace, size_t workspace_bytes, mla_stream_t stream);
 
 /* Decode-kernel timing, for benchmarks and tests. After mla_profile_begin(n), each of the
  * next n mla_decode / mla_decode_noalloc calls in this process records a CUDA event on

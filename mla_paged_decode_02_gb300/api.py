@@ -15,6 +15,7 @@ KV_BF16 = 0
 KV_FP8_E4M3 = 1
 D_QK = 576
 D_V = 512
+D_INDEX = 128
 
 MLA_OK = 0
 STATUS = {0: "MLA_OK", -1: "MLA_ERR_INVALID_ARG", -2: "MLA_ERR_UNSUPPORTED",
@@ -23,7 +24,9 @@ STATUS = {0: "MLA_OK", -1: "MLA_ERR_INVALID_ARG", -2: "MLA_ERR_UNSUPPORTED",
 EXPORTS = ("mla_abi_version", "mla_status_string", "mla_decode_workspace_size", "mla_decode",
            "mla_decode_check", "mla_cache_write", "mla_decode_noalloc", "mla_decode_noalloc_check",
            "mla_profile_begin", "mla_profile_end", "mla_test_set_hooks", "mla_decode_with_cache_write",
-           "mla_rope_cache_write", "mla_chunk_workspace_size", "mla_chunk_attention", "mla_merge_states")
+           "mla_rope_cache_write", "mla_chunk_workspace_size", "mla_chunk_attention", "mla_merge_states",
+           "mla_index_cache_write", "mla_index_scores", "mla_select_blocks", "mla_sparse_workspace_size",
+           "mla_sparse_attention")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmla.so")
@@ -48,6 +51,17 @@ class ChunkParams(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
                 ("max_blocks_per_seq", ctypes.c_int32), ("max_seq_len", ctypes.c_int32),
                 ("kv_dtype", ctypes.c_int32), ("causal", ctypes.c_int32)]
+
+
+class IndexParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "num_tokens", "num_heads", "page_size", "num_pages",
+                                              "max_blocks_per_seq", "max_seq_len", "block_size", "causal")]
+
+
+class SparseParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "num_tokens", "num_heads", "page_size", "num_pages",
+                                              "max_blocks_per_seq", "max_seq_len", "block_size", "top_k", "kv_dtype",
+                                              "causal")]
 
 
 def lib() -> ctypes.CDLL:
@@ -96,6 +110,18 @@ def lib() -> ctypes.CDLL:
                                           vp, sz, vp]
         L.mla_merge_states.restype = i32
         L.mla_merge_states.argtypes = [vp, vp, vp, vp, i64, vp, vp, vp]
+        L.mla_index_cache_write.restype = i32
+        L.mla_index_cache_write.argtypes = [vp, i64, vp, vp, i32, i32, vp, i32, vp, vp, i32, i32, vp, i64, i64, vp, i32,
+                                            vp, vp, vp, vp]
+        L.mla_index_scores.restype = i32
+        L.mla_index_scores.argtypes = [ctypes.POINTER(IndexParams), vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+        L.mla_select_blocks.restype = i32
+        L.mla_select_blocks.argtypes = [vp, i64, i32, i32, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp]
+        L.mla_sparse_workspace_size.restype = sz
+        L.mla_sparse_workspace_size.argtypes = [ctypes.POINTER(SparseParams), i32]
+        L.mla_sparse_attention.restype = i32
+        L.mla_sparse_attention.argtypes = [ctypes.POINTER(SparseParams), vp, vp, vp, vp, vp, vp, ctypes.c_float, vp, vp,
+                                           vp, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -479,4 +505,233 @@ def merge_states(out_a: torch.Tensor, lse_a: torch.Tensor, out_b: torch.Tensor, 
     st = lib().mla_merge_states(at[0], at[1], at[2], at[3], lse_a.numel(), at[4], at[5], handle)
     if st != MLA_OK:
         raise MLAError(st, "mla_merge_states")
+    return out, lse
+
+
+_I32_MAX = 0x7FFFFFFF
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _int32_max(**sizes) -> None:
+    """A structure's or an argument's 32-bit field would keep the low bits of a larger number."""
+    for name, value in sizes.items():
+        if not -_I32_MAX <= value <= _I32_MAX:
+            raise ValueError(f"{name} is out of range")
+
+
+def _ragged(seq_lens, cu_q_lens, block_table=None) -> int:
+    """Checks the offsets, lengths and block table of a ragged batch; its number of sequences."""
+    for name, t in (("seq_lens", seq_lens), ("cu_q_lens", cu_q_lens), ("block_table", block_table)):
+        if t is not None and (t.dtype is not torch.int32 or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous int32 tensor")
+    B = seq_lens.numel()
+    if seq_lens.dim() != 1 or cu_q_lens.shape != (B + 1,):
+        raise ValueError("seq_lens must be [B] and cu_q_lens [B + 1]")
+    if block_table is not None and (block_table.dim() != 2 or block_table.shape[0] != B):
+        raise ValueError("block_table must be [B, MB]")
+    return B
+
+
+def _error_word(device_error) -> None:
+    if device_error is not None and (device_error.dtype not in (torch.int32, torch.uint32) or device_error.numel() < 1):
+        raise ValueError("device_error must be a 32-bit integer tensor")
+
+
+def _index_pool(index_cache, index_scale):
+    """(pages, rows of a page) of an index cache and its scales."""
+    if index_cache.dtype not in _CODES or index_cache.dim() != 3 or index_cache.shape[2] != D_INDEX or \
+            not index_cache.is_contiguous():
+        raise ValueError("index_cache must be a contiguous uint8 or float8_e4m3fn [Np, P, 128] tensor")
+    Np, P, _ = index_cache.shape
+    if index_scale.dtype is not torch.float32 or index_scale.shape != (Np, P) or not index_scale.is_contiguous():
+        raise ValueError("index_scale must be a contiguous float32 [Np, P] tensor")
+    return Np, P
+
+
+def index_cache_write(keys: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor, slot_mapping: torch.Tensor,
+                      index_cache: torch.Tensor, index_scale: torch.Tensor, *, queries: torch.Tensor | None = None,
+                      weights: torch.Tensor | None = None, q_index: torch.Tensor | None = None,
+                      q_weights: torch.Tensor | None = None, interleaved: bool = True,
+                      device_error: torch.Tensor | None = None, stream=None) -> None:
+    """New tokens' index keys [N, 128] bf16, their last 64 values rotated, as E4M3 codes into
+    index_cache [Np, P, 128] and a float32 scale each into index_scale [Np, P], at
+    slot_mapping[t]; and their index queries [N, H, 128] bf16, rotated, as codes into q_index
+    [N, H, 128], with weights [N, H] float32 times each query's scale in q_weights [N, H].
+    positions, cos_sin, slot_mapping and interleaved as rope_cache_write(). keys and queries may be
+    strided views of projections. Negative positions mark padding tokens."""
+    n = keys.shape[0]
+    stride = _rows_of(keys, n, D_INDEX, "keys")
+    i64 = torch.int64
+    if positions.dtype is not i64 or positions.shape != (n,) or not positions.is_contiguous() or \
+            slot_mapping.dtype is not i64 or slot_mapping.shape != (n,) or not slot_mapping.is_contiguous():
+        raise ValueError("positions and slot_mapping must be contiguous int64 [N] tensors")
+    if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or cos_sin.shape[1] != 64 or not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be a contiguous float32 [max_pos, 64] tensor")
+    Np, P = _index_pool(index_cache, index_scale)
+    given = [t is not None for t in (queries, weights, q_index, q_weights)]
+    if any(given) != all(given):
+        raise ValueError("queries, weights, q_index and q_weights are given together or not at all")
+    H, qt, qh = 0, 0, 0
+    if queries is not None:
+        if queries.dtype is not torch.bfloat16 or queries.dim() != 3 or queries.shape[0] != n or queries.shape[2] != D_INDEX:
+            raise ValueError("queries must be a bf16 [N, H, 128] tensor with contiguous last dimension")
+        H = queries.shape[1]
+        qt, qh, inner = queries.stride()
+        if H < 1 or (inner != 1 and n > 0):
+            raise ValueError("queries must be a bf16 [N, H, 128] tensor with contiguous last dimension")
+        if n <= 1:
+            qt = 0
+        if H <= 1:
+            qh = 0
+        if qt % 8 != 0 or qh % 8 != 0:
+            raise ValueError("the tokens and heads of queries must be apart by a multiple of 8 elements")
+        if q_index.dtype not in _CODES or q_index.shape != (n, H, D_INDEX) or not q_index.is_contiguous():
+            raise ValueError("q_index must be a contiguous uint8 or float8_e4m3fn [N, H, 128] tensor")
+        for t in (weights, q_weights):
+            if t.dtype is not torch.float32 or t.shape != (n, H) or not t.is_contiguous():
+                raise ValueError("weights and q_weights must be contiguous float32 [N, H] tensors")
+    _error_word(device_error)
+    if n == 0:
+        queries = weights = q_index = q_weights = None
+    handle, at = _addresses(stream, keys if n > 0 else None, positions, cos_sin, slot_mapping, index_cache, index_scale,
+                            queries, weights, q_index, q_weights, device_error)
+    st = lib().mla_index_cache_write(at[0], stride, at[1], at[2], cos_sin.shape[0], 1 if interleaved else 0, at[3], n,
+                                     at[4], at[5], Np, P, at[6], qt, qh, at[7], H, at[8], at[9], at[10], handle)
+    if st != MLA_OK:
+        raise MLAError(st, "mla_index_cache_write")
+
+
+def index_scores(q_index: torch.Tensor, q_weights: torch.Tensor, index_cache: torch.Tensor, index_scale: torch.Tensor,
+                 block_table: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens: torch.Tensor, *, max_seq_len: int,
+                 block_size: int, causal: bool = True, out: torch.Tensor | None = None,
+                 device_error: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Scores [T, ceil(max_seq_len / block_size)] float32 of the blocks of each new token's context:
+    the largest, over the block's keys that the token sees, of the key's scale times the sum over
+    the index heads of q_weights times the positive part of q_index . key; -inf without such a key.
+    q_index [T, H, 128] and q_weights [T, H] as index_cache_write() leaves them; the ragged batch as
+    chunk_attention(). Rows that belong to no sequence are left as they are in out (uninitialised when
+    it is allocated here)."""
+    if q_index.dtype not in _CODES or q_index.dim() != 3 or q_index.shape[2] != D_INDEX or not q_index.is_contiguous():
+        raise ValueError("q_index must be a contiguous uint8 or float8_e4m3fn [T, H, 128] tensor")
+    T, H, _ = q_index.shape
+    if q_weights.dtype is not torch.float32 or q_weights.shape != (T, H) or not q_weights.is_contiguous():
+        raise ValueError("q_weights must be a contiguous float32 [T, H] tensor")
+    Np, P = _index_pool(index_cache, index_scale)
+    B = _ragged(seq_lens, cu_q_lens, block_table)
+    _error_word(device_error)
+    if max_seq_len < 1 or block_size < 1:
+        raise ValueError("max_seq_len and block_size must be positive")
+    _int32_max(max_seq_len=max_seq_len, block_size=block_size)
+    shape = (T, (max_seq_len + block_size - 1) // block_size)
+    if out is not None and (out.dtype is not torch.float32 or out.shape != shape or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous float32 [T, ceil(max_seq_len / block_size)] tensor")
+    handle, at = _addresses(stream, q_index, q_weights, index_cache, index_scale, block_table, seq_lens, cu_q_lens, out,
+                            device_error)
+    if out is None:
+        out = _allocated(stream, shape, torch.float32, q_index.device)
+        at[7] = out.data_ptr()
+    params = IndexParams(B, T, H, P, Np, block_table.shape[1], max_seq_len, block_size, 1 if causal else 0)
+    st = lib().mla_index_scores(ctypes.byref(params), at[0], at[1], at[2], at[3], at[4], at[5], at[6], at[7], at[8], handle)
+    if st != MLA_OK:
+        raise MLAError(st, "mla_index_scores")
+    return out
+
+
+def select_blocks(scores: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens: torch.Tensor, top_k: int, *, block_size: int,
+                  keep_first: int = 0, keep_last: int = 0, causal: bool = True, out: torch.Tensor | None = None,
+                  device_error: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Selected blocks [T, top_k] int32 of each new token: its first keep_first and latest keep_last
+    blocks, then those with the largest scores (ties to the lower index), ascending, -1 behind them.
+    scores [T, blocks] float32 as index_scores() returns them (rows may be apart). Rows that belong to no
+    sequence are left as they are in out (uninitialised when it is allocated here)."""
+    if scores.dtype is not torch.float32 or scores.dim() != 2:
+        raise ValueError("scores must be a float32 [T, blocks] tensor with contiguous rows")
+    T, C = scores.shape
+    stride, inner = scores.stride()
+    if T > 0 and C > 1 and inner != 1:
+        raise ValueError("scores must be a float32 [T, blocks] tensor with contiguous rows")
+    if T <= 1:
+        stride = max(stride, C)
+    if stride < C:
+        raise ValueError("the rows of scores must not overlap")
+    B = _ragged(seq_lens, cu_q_lens)
+    _error_word(device_error)
+    if top_k < 1 or keep_first < 0 or keep_last < 0 or keep_first + keep_last > top_k:
+        raise ValueError("top_k must be positive and hold keep_first + keep_last blocks")
+    _int32_max(top_k=top_k, block_size=block_size)
+    if out is not None and (out.dtype is not torch.int32 or out.shape != (T, top_k) or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous int32 [T, top_k] tensor")
+    handle, at = _addresses(stream, scores, seq_lens, cu_q_lens, out, device_error)
+    if out is None:
+        out = _allocated(stream, (T, top_k), torch.int32, scores.device)
+        at[3] = out.data_ptr()
+    st = lib().mla_select_blocks(at[0], stride, T, C, at[1], at[2], B, block_size, top_k, keep_first, keep_last,
+                                 1 if causal else 0, at[3], at[4], handle)
+    if st != MLA_OK:
+        raise MLAError(st, "mla_select_blocks")
+    return out
+
+
+def make_sparse_params(batch, num_tokens, num_heads, page_size, num_pages, max_blocks_per_seq, max_seq_len, block_size,
+                       top_k, kv_dtype, causal=True) -> SparseParams:
+    _int32_max(max_seq_len=max_seq_len, block_size=block_size, top_k=top_k)
+    return SparseParams(int(batch), int(num_tokens), int(num_heads), int(page_size), int(num_pages),
+                        int(max_blocks_per_seq), int(max_seq_len), int(block_size), int(top_k), int(kv_dtype),
+                        int(bool(causal)))
+
+
+def sparse_workspace_size(params: SparseParams, num_sms: int = 0) -> int:
+    n = lib().mla_sparse_workspace_size(ctypes.byref(params), int(num_sms))
+    if n == 0:
+        raise MLAError(-1, "mla_sparse_workspace_size")
+    return int(n)
+
+
+def alloc_sparse_workspace(params: SparseParams, device=None) -> torch.Tensor:
+    return torch.empty(sparse_workspace_size(params), dtype=torch.uint8, device=device or "cuda")
+
+
+def sparse_attention(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                     cu_q_lens: torch.Tensor, selected: torch.Tensor, softmax_scale: float,
+                     kv_scale: torch.Tensor | None = None, *, max_seq_len: int, block_size: int, causal: bool = True,
+                     out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None):
+    """chunk_attention() of which each new token sees only the keys of its selected blocks of
+    block_size tokens. selected [T, K] int32, as select_blocks() returns it, is a set for each token:
+    order and repetitions do not matter, entries that name no block with a visible key (-1 among them)
+    are left out. A token without any key gets out 0 and lse -inf. Returns (out, lse)."""
+    if q.dim() != 3 or q.shape[2] != D_QK or q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 [T, H, 576] tensor")
+    T, H, _ = q.shape
+    if kv_cache.dim() != 3 or kv_cache.shape[2] != D_QK or not kv_cache.is_contiguous():
+        raise ValueError("kv_cache must be a contiguous [Np, P, 576] tensor")
+    Np, P, _ = kv_cache.shape
+    B = _ragged(seq_lens, cu_q_lens, block_table)
+    if selected.dtype is not torch.int32 or selected.dim() != 2 or selected.shape[0] != T or not selected.is_contiguous():
+        raise ValueError("selected must be a contiguous int32 [T, K] tensor")
+    kvd = _kv_dtype_of(kv_cache)
+    if kvd == KV_FP8_E4M3 and (kv_scale is None or kv_scale.dtype != torch.float32 or kv_scale.numel() < 1):
+        raise ValueError("the FP8 cache needs kv_scale as a float32 device tensor")
+    if out is not None and (out.dtype != torch.bfloat16 or out.shape != (T, H, D_V) or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous bf16 [T, H, 512] tensor")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, H) or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 [T, H] tensor")
+    if workspace is not None and not workspace.is_contiguous():     # its size is taken from its elements
+        raise ValueError("workspace must be contiguous")
+    scale = kv_scale if kvd == KV_FP8_E4M3 else None
+    params = make_sparse_params(B, T, H, P, Np, block_table.shape[1], max_seq_len, block_size, selected.shape[1], kvd, causal)
+    handle, at = _addresses(stream, q, kv_cache, block_table, seq_lens, cu_q_lens, selected, scale, out, lse, workspace)
+    if out is None:
+        out = _allocated(stream, (T, H, D_V), torch.bfloat16, q.device)
+        at[7] = out.data_ptr()
+    if lse is None:
+        lse = _allocated(stream, (T, H), torch.float32, q.device)
+        at[8] = lse.data_ptr()
+    if workspace is None:
+        workspace = _allocated(stream, (sparse_workspace_size(params),), torch.uint8, q.device)
+        at[9] = workspace.data_ptr()
+    st = lib().mla_sparse_attention(ctypes.byref(params), at[0], at[1], at[2], at[3], at[4], at[5], softmax_scale, at[6],
+                                    at[7], at[8], at[9], workspace.numel() * workspace.element_size(), handle)
+    if st != MLA_OK:
+        raise MLAError(st, "mla_sparse_attention")
     return out, lse

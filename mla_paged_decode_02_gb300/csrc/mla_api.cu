@@ -7,6 +7,7 @@
 #include <vector>
 #include <cudaTypedefs.h>
 #include "mla_chunk.h"
+#include "mla_index.h"
 #include "mla_internal.h"
 #include "mla_ptx.cuh"
 #include "mla_rope.h"
@@ -486,6 +487,78 @@ bool encode_bytes_map(CUtensorMap* m, const void* base, int64_t rows, uint32_t b
   return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box);
 }
 
+// the workspace's part of the scheduler's arguments, and the set-up charge of a block
+ChunkSchedArgs chunk_sched_args(uint8_t* ws, const ChunkWs& w, int H, int tokens, int pairs, bool fp8) {
+  ChunkSchedArgs sa{};
+  sa.hdr = reinterpret_cast<uint32_t*>(ws);
+  sa.gbase = reinterpret_cast<int32_t*>(ws + w.gbase_off);
+  sa.cta_first = reinterpret_cast<int32_t*>(ws + w.cta_off);
+  sa.split_list = reinterpret_cast<int4*>(ws + w.split_off);
+  sa.units = reinterpret_cast<ChunkUnit*>(ws + w.units_off);
+  sa.H = H;
+  sa.workers = pairs;
+  // a block's set-up (its q, the softmax before the first PV, its results) costs about 0.6 tiles
+  // with the bf16 cache, more with E4M3, whose q is split first; prompts of 150 to 2000 tokens
+  // with 16 heads: 226, 179, 188 us for 0, 1, 2 (bf16), 324, 227 to 273, 206 to 217, 212 to 258 for
+  // 0, 1, 2, 3 (E4M3; the mixed step 99, 99, 98, 99, single tokens alone 64, 61, 63, 64)
+  sa.setup = fp8 ? 2 : 1;
+  sa.tokens = tokens;
+  return sa;
+}
+
+// the geometry of a pool of num_pages pages of page_size rows, and its tensor maps
+bool encode_chunk_maps(ChunkArgs* ca, const void* q, int tokens, int H, const void* kv_cache, int num_pages, int page_size,
+                       bool fp8) {
+  const int64_t rows = (int64_t)num_pages * page_size;
+  ca->k_box = box_rows_of(page_size, 64);
+  ca->v_box = box_rows_of(page_size, fp8 ? 64 : 32);
+  ca->H = H;
+  ca->P = page_size;
+  ca->num_pages = num_pages;
+  ca->total_rows = (int32_t)rows;
+  return encode_rows_map(&ca->tm_q, q, (int64_t)tokens * H, 64, 9) &&
+         (fp8 ? encode_bytes_map(&ca->tm_k, kv_cache, rows, ca->k_box) && encode_bytes_map(&ca->tm_v, kv_cache, rows, ca->v_box)
+              : encode_rows_map(&ca->tm_k, kv_cache, rows, ca->k_box, 1) &&
+                    encode_rows_map(&ca->tm_v, kv_cache, rows, ca->v_box, ca->k_box < 64 ? 1 : 4));
+}
+
+// the attention kernel over the units that `sa` names, and the merge of the blocks it cut
+mla_status launch_chunk_pair(ChunkArgs& ca, ChunkCombineArgs& cc, const ChunkSchedArgs& sa, uint8_t* ws, const ChunkWs& w,
+                             float softmax_scale, const float* kv_scale, void* out, float* lse, bool fp8, int pairs, int nsm,
+                             cudaStream_t s) {
+  ca.units = sa.units;
+  ca.cta_first = sa.cta_first;
+  ca.err = sa.hdr;
+  ca.out = static_cast<__nv_bfloat16*>(out);
+  ca.out_wide = aligned(out, 32) ? 1 : 0;
+  ca.lse = lse;
+  ca.part_o = reinterpret_cast<float*>(ws + w.po_off);
+  ca.part_lse = reinterpret_cast<float*>(ws + w.plse_off);
+  ca.kv_scale = kv_scale;
+  ca.softmax_scale = softmax_scale;
+  ca.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  ca.test_stall = g_test_stall.load(std::memory_order_relaxed);
+  if (launch_chunk(ca, fp8, pairs, s) != cudaSuccess) return MLA_ERR_CUDA;
+  cc.hdr = sa.hdr;
+  cc.err = sa.hdr;
+  cc.split_list = sa.split_list;
+  cc.part_o = ca.part_o;
+  cc.part_lse = ca.part_lse;
+  cc.out = ca.out;
+  cc.lse = ca.lse;
+  if (launch_chunk_combine(cc, 8 * nsm, s) != cudaSuccess) return MLA_ERR_CUDA;
+  return MLA_OK;
+}
+
+// per-device attributes of the chunk kernel, once
+cudaError_t prepare_chunk(int dev, bool fp8) {
+  const uint32_t bit = fp8 ? 2u : 1u;
+  if (g_chunk_prepared[dev].load() & bit) return cudaSuccess;
+  const cudaError_t e = chunk_prepare(fp8);
+  if (e == cudaSuccess) g_chunk_prepared[dev].fetch_or(bit);
+  return e;
+}
+
 }  // namespace
 }  // namespace mla
 
@@ -527,74 +600,27 @@ MLA_EXPORT mla_status mla_chunk_attention(const mla_chunk_params* p, const void*
   const ChunkWs w = chunk_ws_layout(p->batch, p->num_tokens, p->num_heads, pairs);
   if (workspace_bytes < w.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
   if (!get_encoder()) return MLA_ERR_CUDA;
-  const uint32_t bit = fp8 ? 2u : 1u;
-  if (!(g_chunk_prepared[dev].load() & bit)) {
-    if (chunk_prepare(fp8) != cudaSuccess) return MLA_ERR_CUDA;
-    g_chunk_prepared[dev].fetch_or(bit);
-  }
+  if (prepare_chunk(dev, fp8) != cudaSuccess) return MLA_ERR_CUDA;
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int64_t cap = (int64_t)p->max_blocks_per_seq * p->page_size;
-  ChunkSchedArgs sa{};
+  ChunkSchedArgs sa = chunk_sched_args(ws, w, p->num_heads, p->num_tokens, pairs, fp8);
   sa.seq_lens = seq_lens;
   sa.cu_q = cu_q_lens;
-  sa.hdr = reinterpret_cast<uint32_t*>(ws);
-  sa.gbase = reinterpret_cast<int32_t*>(ws + w.gbase_off);
-  sa.cta_first = reinterpret_cast<int32_t*>(ws + w.cta_off);
-  sa.split_list = reinterpret_cast<int4*>(ws + w.split_off);
-  sa.units = reinterpret_cast<ChunkUnit*>(ws + w.units_off);
   sa.B = p->batch;
-  sa.H = p->num_heads;
   sa.causal = p->causal;
   sa.max_len = (int)std::min<int64_t>(cap, p->max_seq_len);
-  sa.workers = pairs;
-  // a block's set-up (its q, the softmax before the first PV, its results) costs about 0.6 tiles
-  // with the bf16 cache, more with E4M3, whose q is split first; prompts of 150 to 2000 tokens
-  // with 16 heads: 226, 179, 188 us for 0, 1, 2 (bf16), 324, 227 to 273, 206 to 217, 212 to 258 for
-  // 0, 1, 2, 3 (E4M3; the mixed step 99, 99, 98, 99, single tokens alone 64, 61, 63, 64)
-  sa.setup = fp8 ? 2 : 1;
-  sa.tokens = p->num_tokens;
   ChunkArgs ca;
   std::memset(&ca, 0, sizeof(ca));
-  const int64_t rows = (int64_t)p->num_pages * p->page_size;
-  ca.k_box = box_rows_of(p->page_size, 64);
-  ca.v_box = box_rows_of(p->page_size, fp8 ? 64 : 32);
-  if (any) {
-    if (!encode_rows_map(&ca.tm_q, q, (int64_t)p->num_tokens * p->num_heads, 64, 9)) return MLA_ERR_INVALID_ARG;
-    const bool ok =
-        fp8 ? encode_bytes_map(&ca.tm_k, kv_cache, rows, ca.k_box) && encode_bytes_map(&ca.tm_v, kv_cache, rows, ca.v_box)
-            : encode_rows_map(&ca.tm_k, kv_cache, rows, ca.k_box, 1) &&
-                  encode_rows_map(&ca.tm_v, kv_cache, rows, ca.v_box, ca.k_box < 64 ? 1 : 4);
-    if (!ok) return MLA_ERR_INVALID_ARG;
-  }
+  if (any && !encode_chunk_maps(&ca, q, p->num_tokens, p->num_heads, kv_cache, p->num_pages, p->page_size, fp8))
+    return MLA_ERR_INVALID_ARG;
   if (launch_chunk_schedule(sa, s) != cudaSuccess) return MLA_ERR_CUDA;
   if (!any) return MLA_OK;
-
   ca.block_table = block_table;
-  ca.units = sa.units;
-  ca.cta_first = sa.cta_first;
-  ca.err = sa.hdr;
-  ca.out = static_cast<__nv_bfloat16*>(out);
-  ca.out_wide = aligned(out, 32) ? 1 : 0;
-  ca.lse = lse;
-  ca.part_o = reinterpret_cast<float*>(ws + w.po_off);
-  ca.part_lse = reinterpret_cast<float*>(ws + w.plse_off);
-  ca.kv_scale = kv_scale;
-  ca.H = p->num_heads;
-  ca.P = p->page_size;
   ca.MB = p->max_blocks_per_seq;
-  ca.num_pages = p->num_pages;
   ca.causal = p->causal;
-  ca.total_rows = (int32_t)rows;
-  ca.softmax_scale = softmax_scale;
-  ca.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
-  ca.test_stall = g_test_stall.load(std::memory_order_relaxed);
-  if (launch_chunk(ca, fp8, pairs, s) != cudaSuccess) return MLA_ERR_CUDA;
-
   ChunkCombineArgs cc{};
-  cc.hdr = sa.hdr;
-  cc.err = sa.hdr;
   cc.block_table = block_table;
   cc.seq_lens = seq_lens;
   cc.cu_q = cu_q_lens;
@@ -603,13 +629,7 @@ MLA_EXPORT mla_status mla_chunk_attention(const mla_chunk_params* p, const void*
   cc.P = p->page_size;
   cc.num_pages = p->num_pages;
   cc.max_len = sa.max_len;
-  cc.split_list = sa.split_list;
-  cc.part_o = ca.part_o;
-  cc.part_lse = ca.part_lse;
-  cc.out = ca.out;
-  cc.lse = ca.lse;
-  if (launch_chunk_combine(cc, 8 * nsm, s) != cudaSuccess) return MLA_ERR_CUDA;
-  return MLA_OK;
+  return launch_chunk_pair(ca, cc, sa, ws, w, softmax_scale, kv_scale, out, lse, fp8, pairs, nsm, s);
 }
 
 // ------------------------------------------------------------ rotating append, state merge
@@ -677,4 +697,246 @@ MLA_EXPORT mla_status mla_merge_states(const void* out_a, const float* lse_a, co
       cudaSuccess)
     return MLA_ERR_CUDA;
   return MLA_OK;
+}
+
+// -------------------------------------------------------------------- block-sparse attention
+MLA_EXPORT mla_status mla_index_cache_write(const void* keys, int64_t key_stride, const int64_t* positions,
+                                            const float* cos_sin, int32_t max_pos, int32_t interleaved,
+                                            const int64_t* slot_mapping, int32_t num_tokens, void* index_cache,
+                                            float* index_scale, int32_t num_pages, int32_t page_size,
+                                            const void* queries, int64_t q_token_stride, int64_t q_head_stride,
+                                            const float* weights, int32_t num_heads, void* q_index, float* q_weights,
+                                            uint32_t* device_error, mla_stream_t stream) {
+  if (num_tokens < 0 || num_pages < 1 || page_size < 1 || max_pos < 1) return MLA_ERR_INVALID_ARG;
+  if (interleaved != 0 && interleaved != 1) return MLA_ERR_INVALID_ARG;
+  const bool any = queries != nullptr;
+  if (any != (weights != nullptr) || any != (q_index != nullptr) || any != (q_weights != nullptr)) return MLA_ERR_INVALID_ARG;
+  if (any && num_heads < 1) return MLA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return MLA_OK;
+  if (!keys || !positions || !cos_sin || !slot_mapping || !index_cache || !index_scale) return MLA_ERR_INVALID_ARG;
+  if (!aligned(keys, 16) || !aligned(index_cache, 16) || !aligned(index_scale, 4) || !aligned(cos_sin, 16) ||
+      !aligned(positions, 8) || !aligned(slot_mapping, 8) || !aligned(queries, 16) || !aligned(q_index, 16) ||
+      !aligned(weights, 4) || !aligned(q_weights, 4) || !aligned(device_error, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (key_stride < kDIndex || key_stride % 8 != 0) return MLA_ERR_INVALID_ARG;
+  if (any && (q_token_stride % 8 != 0 || q_head_stride % 8 != 0 || q_token_stride < 0 || q_head_stride < 0))
+    return MLA_ERR_INVALID_ARG;
+  if (any && num_heads > kMaxIndexHeads) return MLA_ERR_UNSUPPORTED;
+  IndexWriteArgs a{};
+  a.keys = static_cast<const __nv_bfloat16*>(keys);
+  a.positions = positions;
+  a.slots = slot_mapping;
+  a.cos_sin = cos_sin;
+  a.queries = static_cast<const __nv_bfloat16*>(queries);
+  a.weights = weights;
+  a.cache = static_cast<uint8_t*>(index_cache);
+  a.scale = index_scale;
+  a.q_index = static_cast<uint8_t*>(q_index);
+  a.q_weights = q_weights;
+  a.err = device_error;
+  a.key_stride = key_stride;
+  a.q_token_stride = q_token_stride;
+  a.q_head_stride = q_head_stride;
+  a.total_slots = (int64_t)num_pages * page_size;
+  a.n = num_tokens;
+  a.H = num_heads;
+  a.max_pos = max_pos;
+  a.interleaved = interleaved;
+  if (launch_index_write(a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_CUDA;
+  return MLA_OK;
+}
+
+namespace mla {
+namespace {
+
+// what the block-sparse calls share: a ragged batch over pages that hold whole blocks
+mla_status check_blocks(const mla_index_params* p) {
+  if (p == nullptr) return MLA_ERR_INVALID_ARG;
+  if (p->batch < 1 || p->num_tokens < 0 || p->num_heads < 1 || p->page_size < 1 || p->num_pages < 1 ||
+      p->max_blocks_per_seq < 1 || p->max_seq_len < 1 || p->block_size < 1)
+    return MLA_ERR_INVALID_ARG;
+  if (p->causal != 0 && p->causal != 1) return MLA_ERR_INVALID_ARG;
+  if (p->page_size % 8 != 0 || p->page_size > 1024) return MLA_ERR_UNSUPPORTED;
+  if (p->block_size % 8 != 0 || p->page_size % p->block_size != 0) return MLA_ERR_UNSUPPORTED;
+  if (p->batch > kMaxBatch || p->max_seq_len > kMaxSeqLen || p->num_tokens > kMaxSparseTokens) return MLA_ERR_UNSUPPORTED;
+  if ((int64_t)p->num_pages * p->page_size >= (int64_t)1 << 31) return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+int blocks_of(int len, int block) { return (len + block - 1) / block; }
+
+}  // namespace
+}  // namespace mla
+
+MLA_EXPORT mla_status mla_index_scores(const mla_index_params* p, const void* q_index, const float* q_weights,
+                                       const void* index_cache, const float* index_scale, const int32_t* block_table,
+                                       const int32_t* seq_lens, const int32_t* cu_q_lens, float* scores,
+                                       uint32_t* device_error, mla_stream_t stream) {
+  const mla_status st = check_blocks(p);
+  if (st != MLA_OK) return st;
+  if (p->num_heads > kMaxIndexHeads) return MLA_ERR_UNSUPPORTED;
+  if (p->num_tokens == 0) return MLA_OK;
+  if (!q_index || !q_weights || !index_cache || !index_scale || !block_table || !seq_lens || !cu_q_lens || !scores)
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned(q_index, 16) || !aligned(q_weights, 4) || !aligned(index_cache, 16) || !aligned(index_scale, 16) ||
+      !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_q_lens, 4) || !aligned(scores, 4) ||
+      !aligned(device_error, 4))
+    return MLA_ERR_INVALID_ARG;
+  IndexScoreArgs a{};
+  a.q = static_cast<const uint8_t*>(q_index);
+  a.w = q_weights;
+  a.cache = static_cast<const uint8_t*>(index_cache);
+  a.scale = index_scale;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.cu_q = cu_q_lens;
+  a.out = scores;
+  a.err = device_error;
+  a.B = p->batch;
+  a.T = p->num_tokens;
+  a.H = p->num_heads;
+  a.P = p->page_size;
+  a.MB = p->max_blocks_per_seq;
+  a.num_pages = p->num_pages;
+  a.max_len = (int)std::min<int64_t>((int64_t)p->max_blocks_per_seq * p->page_size, p->max_seq_len);
+  a.block = p->block_size;
+  a.C = blocks_of(p->max_seq_len, p->block_size);
+  a.causal = p->causal;
+  if (launch_index_scores(a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_CUDA;
+  return MLA_OK;
+}
+
+MLA_EXPORT mla_status mla_select_blocks(const float* scores, int64_t scores_stride, int32_t num_tokens, int32_t num_blocks,
+                                        const int32_t* seq_lens, const int32_t* cu_q_lens, int32_t batch,
+                                        int32_t block_size, int32_t top_k, int32_t keep_first, int32_t keep_last,
+                                        int32_t causal, int32_t* selected, uint32_t* device_error, mla_stream_t stream) {
+  if (num_tokens < 0 || num_blocks < 1 || batch < 1 || block_size < 1 || top_k < 1 || keep_first < 0 || keep_last < 0)
+    return MLA_ERR_INVALID_ARG;
+  if ((int64_t)keep_first + keep_last > top_k || scores_stride < num_blocks) return MLA_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return MLA_ERR_INVALID_ARG;
+  if (batch > kMaxBatch || num_tokens > kMaxSparseTokens || num_blocks > kMaxSeqLen || top_k > kMaxSeqLen ||
+      block_size > kMaxSeqLen)
+    return MLA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return MLA_OK;
+  if (!scores || !seq_lens || !cu_q_lens || !selected) return MLA_ERR_INVALID_ARG;
+  if (!aligned(scores, 4) || !aligned(seq_lens, 4) || !aligned(cu_q_lens, 4) || !aligned(selected, 4) ||
+      !aligned(device_error, 4))
+    return MLA_ERR_INVALID_ARG;
+  SelectArgs a{};
+  a.scores = scores;
+  a.seq_lens = seq_lens;
+  a.cu_q = cu_q_lens;
+  a.out = selected;
+  a.err = device_error;
+  a.stride = scores_stride;
+  a.B = batch;
+  a.T = num_tokens;
+  a.C = num_blocks;
+  a.K = top_k;
+  a.block = block_size;
+  a.keep_first = keep_first;
+  a.keep_last = keep_last;
+  a.causal = causal;
+  if (launch_select_blocks(a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_CUDA;
+  return MLA_OK;
+}
+
+namespace mla {
+namespace {
+
+mla_status check_sparse_params(const mla_sparse_params* p) {
+  if (p == nullptr) return MLA_ERR_INVALID_ARG;
+  const mla_index_params ip{p->batch, p->num_tokens, p->num_heads, p->page_size, p->num_pages, p->max_blocks_per_seq,
+                            p->max_seq_len, p->block_size, p->causal};
+  const mla_status st = check_blocks(&ip);
+  if (st != MLA_OK) return st;
+  if (p->top_k < 1) return MLA_ERR_INVALID_ARG;
+  if (p->kv_dtype != MLA_KV_BF16 && p->kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_INVALID_ARG;
+  if (p->num_heads > kMaxRows || p->top_k > kMaxSeqLen) return MLA_ERR_UNSUPPORTED;
+  if ((int64_t)p->num_tokens * p->num_heads > kMaxChunkRows) return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+// columns of the table of selected blocks
+int sparse_width(const mla_sparse_params* p) { return std::min(p->top_k, blocks_of(p->max_seq_len, p->block_size)); }
+
+}  // namespace
+}  // namespace mla
+
+MLA_EXPORT size_t mla_sparse_workspace_size(const mla_sparse_params* p, int32_t num_sms) {
+  if (check_sparse_params(p) != MLA_OK) return 0;
+  if (num_sms <= 0) {
+    int dev;
+    if (current_device(&dev) != cudaSuccess) return 0;
+    num_sms = sm_count(dev);
+    if (num_sms <= 0) return 0;
+  }
+  if (num_sms < 2) return 0;
+  return sparse_ws_layout(p->num_tokens, p->num_heads, sparse_width(p), num_sms / 2).total;
+}
+
+MLA_EXPORT mla_status mla_sparse_attention(const mla_sparse_params* p, const void* q, const void* kv_cache,
+                                           const int32_t* block_table, const int32_t* seq_lens,
+                                           const int32_t* cu_q_lens, const int32_t* selected, float softmax_scale,
+                                           const float* kv_scale, void* out, float* lse, void* workspace,
+                                           size_t workspace_bytes, mla_stream_t stream) {
+  const mla_status st = check_sparse_params(p);
+  if (st != MLA_OK) return st;
+  const bool fp8 = p->kv_dtype == MLA_KV_FP8_E4M3;
+  const bool any = p->num_tokens > 0;
+  if (!kv_cache || !block_table || !seq_lens || !cu_q_lens || !workspace || (any && (!q || !out || !lse || !selected)))
+    return MLA_ERR_INVALID_ARG;
+  if (fp8 && !kv_scale) return MLA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(block_table, 4) ||
+      !aligned(seq_lens, 4) || !aligned(cu_q_lens, 4) || !aligned(selected, 4) || !aligned(workspace, 256) ||
+      !aligned(kv_scale, 4))
+    return MLA_ERR_INVALID_ARG;
+  if (!(softmax_scale == softmax_scale) || softmax_scale > 3.0e38f || softmax_scale < -3.0e38f)
+    return MLA_ERR_INVALID_ARG;
+  int dev;
+  if (current_device(&dev) != cudaSuccess) return MLA_ERR_CUDA;
+  const int nsm = sm_count(dev);
+  if (nsm <= 0) return MLA_ERR_CUDA;
+  const int pairs = nsm / 2;
+  if (pairs < 1) return MLA_ERR_UNSUPPORTED;
+  const int width = sparse_width(p);
+  const SparseWs w = sparse_ws_layout(p->num_tokens, p->num_heads, width, pairs);
+  if (workspace_bytes < w.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  if (!get_encoder()) return MLA_ERR_CUDA;
+  if (prepare_chunk(dev, fp8) != cudaSuccess) return MLA_ERR_CUDA;
+
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int per_page = p->page_size / p->block_size;
+  SparsePlanArgs pa{};
+  pa.sched = chunk_sched_args(ws, w.chunk, p->num_heads, p->num_tokens, pairs, fp8);
+  pa.sched.B = p->num_tokens;
+  pa.selected = selected;
+  pa.block_table = block_table;
+  pa.seq_lens = seq_lens;
+  pa.cu_q = cu_q_lens;
+  pa.table = reinterpret_cast<int32_t*>(ws + w.table_off);
+  pa.lens = reinterpret_cast<int32_t*>(ws + w.lens_off);
+  pa.flags = reinterpret_cast<uint32_t*>(ws + w.flags_off);
+  pa.B = p->batch;
+  pa.T = p->num_tokens;
+  pa.K = p->top_k;
+  pa.width = width;
+  pa.block = p->block_size;
+  pa.P = p->page_size;
+  pa.MB = p->max_blocks_per_seq;
+  pa.num_pages = p->num_pages;
+  pa.max_len = (int)std::min<int64_t>((int64_t)p->max_blocks_per_seq * p->page_size, p->max_seq_len);
+  pa.causal = p->causal;
+  pa.words = (blocks_of(pa.max_len, p->block_size) + 31) / 32;
+  ChunkArgs ca;
+  std::memset(&ca, 0, sizeof(ca));
+  // to the attention kernel a block is a page, and a token a sequence whose pages are its selected blocks
+  if (any && !encode_chunk_maps(&ca, q, p->num_tokens, p->num_heads, kv_cache, p->num_pages * per_page, p->block_size, fp8))
+    return MLA_ERR_INVALID_ARG;
+  if (launch_sparse_plan(pa, s) != cudaSuccess) return MLA_ERR_CUDA;
+  if (!any) return MLA_OK;
+  ca.block_table = pa.table;
+  ca.MB = width;
+  ca.causal = 0;
+  ChunkCombineArgs cc{};                   // B = 0: the plan has checked the pages
+  return launch_chunk_pair(ca, cc, pa.sched, ws, w.chunk, softmax_scale, kv_scale, out, lse, fp8, pairs, nsm, s);
 }

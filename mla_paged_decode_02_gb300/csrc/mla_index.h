@@ -1,0 +1,86 @@
+// mla_index.h — arguments of the block-sparse operators: index cache write, block scores, block
+// selection, and the plan of the sparse attention. Not part of the public ABI.
+#pragma once
+#include "mla_chunk.h"
+
+namespace mla {
+
+constexpr int kDIndex = 128;              // width of an index key and of an index query head
+constexpr int kMaxIndexHeads = 128;
+constexpr int kMaxSparseTokens = 1 << 20;
+
+struct IndexWriteArgs {
+  const __nv_bfloat16* keys;       // rows of 128, key_stride elements apart
+  const int64_t* positions;
+  const int64_t* slots;
+  const float* cos_sin;            // [max_pos][32 cosines | 32 sines]
+  const __nv_bfloat16* queries;    // 128 values per (token, head) at the two strides; NULL: none
+  const float* weights;            // [n, H]
+  uint8_t* cache;                  // [slots][128] E4M3
+  float* scale;                    // [slots]
+  uint8_t* q_index;                // [n, H, 128] E4M3
+  float* q_weights;                // [n, H]
+  uint32_t* err;
+  int64_t key_stride, q_token_stride, q_head_stride, total_slots;
+  int32_t n, H, max_pos, interleaved, qtasks;
+};
+cudaError_t launch_index_write(IndexWriteArgs a, cudaStream_t s);
+
+struct IndexScoreArgs {
+  const uint8_t* q;                // [T, H, 128] E4M3
+  const float* w;                  // [T, H]
+  const uint8_t* cache;            // [num_pages * P][128] E4M3
+  const float* scale;              // [num_pages * P]
+  const int32_t* block_table;      // [B, MB]
+  const int32_t* seq_lens;
+  const int32_t* cu_q;             // [B + 1]
+  float* out;                      // [T, C]
+  uint32_t* err;
+  int32_t B, T, H, P, MB, num_pages, max_len, block, C, causal;
+};
+cudaError_t launch_index_scores(const IndexScoreArgs& a, cudaStream_t s);
+
+struct SelectArgs {
+  const float* scores;             // rows of C, stride elements apart
+  const int32_t* seq_lens;
+  const int32_t* cu_q;             // [B + 1]
+  int32_t* out;                    // [T, K]
+  uint32_t* err;
+  int64_t stride;
+  int32_t B, T, C, K, block, keep_first, keep_last, causal;
+};
+cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t s);
+
+// The plan of a sparse attention: each token becomes a sequence of its own whose pages are its
+// selected blocks, ascending, for the chunk attention's kernels.
+struct SparsePlanArgs {
+  ChunkSchedArgs sched;            // hdr, gbase, cta_first, split_list, units, H, workers, setup, tokens
+  const int32_t* selected;         // [T, K]
+  const int32_t* block_table;      // [B, MB]
+  const int32_t* seq_lens;
+  const int32_t* cu_q;             // [B + 1]
+  int32_t* table;                  // [T, width]: selected blocks in units of `block` rows of the pool
+  int32_t* lens;                   // [T]: keys of those blocks that the token sees
+  uint32_t* flags;                 // [kPlanCtas]: error bits found by each CTA
+  int32_t B, T, K, width, block, P, MB, num_pages, max_len, causal;
+  int32_t words;                   // 32-bit words of a token's set of blocks
+};
+constexpr int kPlanCtas = 8;       // one cluster
+cudaError_t launch_sparse_plan(const SparsePlanArgs& a, cudaStream_t s);
+
+struct SparseWs {
+  ChunkWs chunk;
+  size_t flags_off, lens_off, table_off, total;
+};
+inline SparseWs sparse_ws_layout(int64_t tokens, int H, int width, int workers) {
+  SparseWs w{};
+  w.chunk = chunk_ws_layout((int)tokens, tokens, H, workers);
+  size_t off = w.chunk.total;
+  w.flags_off = off;  off = align_up(off + sizeof(uint32_t) * kPlanCtas, 256);
+  w.lens_off = off;   off = align_up(off + sizeof(int32_t) * (size_t)tokens, 256);
+  w.table_off = off;  off = align_up(off + sizeof(int32_t) * (size_t)tokens * (size_t)width, 256);
+  w.total = off;
+  return w;
+}
+
+}  // namespace mla
