@@ -763,6 +763,13 @@ mla_status check_blocks(const mla_index_params* p) {
   return MLA_OK;
 }
 int blocks_of(int len, int block) { return (len + block - 1) / block; }
+// rows of 128 bytes
+bool encode_index_map(CUtensorMap* m, const void* base, int64_t rows, uint32_t box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)kDIndex, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)kDIndex};
+  const cuuint32_t box[2] = {(cuuint32_t)kDIndex, box_rows};
+  return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, strides, box);
+}
 
 }  // namespace
 }  // namespace mla
@@ -781,10 +788,21 @@ MLA_EXPORT mla_status mla_index_scores(const mla_index_params* p, const void* q_
       !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_q_lens, 4) || !aligned(scores, 4) ||
       !aligned(device_error, 4))
     return MLA_ERR_INVALID_ARG;
-  IndexScoreArgs a{};
-  a.q = static_cast<const uint8_t*>(q_index);
+  int dev;
+  if (current_device(&dev) != cudaSuccess) return MLA_ERR_CUDA;
+  const int nsm = sm_count(dev);
+  if (nsm <= 0 || !get_encoder()) return MLA_ERR_CUDA;
+  IndexScoreArgs a;
+  std::memset(&a, 0, sizeof(a));
+  const int64_t rows = (int64_t)p->num_pages * p->page_size;
+  a.box_rows = box_rows_of(p->page_size, 128);
+  a.total_rows = (int32_t)rows;
+  if (!encode_index_map(&a.tm_q, q_index, (int64_t)p->num_tokens * p->num_heads, 16) ||
+      !encode_index_map(&a.tm_k, index_cache, rows, (uint32_t)a.box_rows))
+    return MLA_ERR_INVALID_ARG;
+  a.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  a.test_stall = g_test_stall.load(std::memory_order_relaxed);
   a.w = q_weights;
-  a.cache = static_cast<const uint8_t*>(index_cache);
   a.scale = index_scale;
   a.block_table = block_table;
   a.seq_lens = seq_lens;
@@ -801,7 +819,8 @@ MLA_EXPORT mla_status mla_index_scores(const mla_index_params* p, const void* q_
   a.block = p->block_size;
   a.C = blocks_of(p->max_seq_len, p->block_size);
   a.causal = p->causal;
-  if (launch_index_scores(a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_CUDA;
+  const int columns = index_scores_columns(a.T, a.B, a.H);
+  if (launch_index_scores(a, columns, nsm, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_CUDA;
   return MLA_OK;
 }
 

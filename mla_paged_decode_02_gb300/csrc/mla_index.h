@@ -27,9 +27,9 @@ struct IndexWriteArgs {
 cudaError_t launch_index_write(IndexWriteArgs a, cudaStream_t s);
 
 struct IndexScoreArgs {
-  const uint8_t* q;                // [T, H, 128] E4M3
+  CUtensorMap tm_q;                // [T * H rows][128] E4M3, boxes of 16 rows
+  CUtensorMap tm_k;                // [num_pages * P rows][128] E4M3, boxes of box_rows rows
   const float* w;                  // [T, H]
-  const uint8_t* cache;            // [num_pages * P][128] E4M3
   const float* scale;              // [num_pages * P]
   const int32_t* block_table;      // [B, MB]
   const int32_t* seq_lens;
@@ -37,8 +37,15 @@ struct IndexScoreArgs {
   float* out;                      // [T, C]
   uint32_t* err;
   int32_t B, T, H, P, MB, num_pages, max_len, block, C, causal;
+  int32_t box_rows, total_rows;
+  int32_t Hp, TG;                  // columns of a token, tokens of a group
+  int32_t slots, chunks;           // group numbers, stretches of unit_blocks blocks
+  int32_t unit_blocks;
+  int32_t test_stall;
+  uint64_t wait_limit_ns;
 };
-cudaError_t launch_index_scores(const IndexScoreArgs& a, cudaStream_t s);
+int index_scores_columns(int T, int B, int H);
+cudaError_t launch_index_scores(IndexScoreArgs a, int columns, int num_sms, cudaStream_t s);
 
 struct SelectArgs {
   const float* scores;             // rows of C, stride elements apart

@@ -227,6 +227,19 @@ def test_scores_report_device_errors():
     c.check()
 
 
+def test_scores_of_a_stalled_pipeline_time_out_and_the_next_call_is_clean():
+    c = ScoreCase([(3, 3000), (1, 700)], 64, 64, 64, seed=6)
+    api.test_set_hooks(20_000_000, True)
+    try:
+        c.run()
+        torch.cuda.synchronize()
+        assert c.error.item() == 0x8
+    finally:
+        api.test_set_hooks(0, False)
+    c.run()
+    c.check()
+
+
 def test_scores_default_output_strided_streams_and_graph():
     c = ScoreCase([(5, 300), (1, 90)], 64, 64, 32, seed=5)
     c.run()
