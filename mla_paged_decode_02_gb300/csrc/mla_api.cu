@@ -819,8 +819,7 @@ MLA_EXPORT mla_status mla_index_scores(const mla_index_params* p, const void* q_
   a.block = p->block_size;
   a.C = blocks_of(p->max_seq_len, p->block_size);
   a.causal = p->causal;
-  const int columns = index_scores_columns(a.T, a.B, a.H);
-  if (launch_index_scores(a, columns, nsm, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_CUDA;
+  if (launch_index_scores(a, nsm, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return MLA_ERR_CUDA;
   return MLA_OK;
 }
 

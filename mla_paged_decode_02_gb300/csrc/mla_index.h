@@ -38,14 +38,15 @@ struct IndexScoreArgs {
   uint32_t* err;
   int32_t B, T, H, P, MB, num_pages, max_len, block, C, causal;
   int32_t box_rows, total_rows;
-  int32_t Hp, TG;                  // columns of a token, tokens of a group
+  int32_t Hp, TG, sub_tokens;      // columns of a token, tokens of a group and of a sub-group
+  int32_t q_rows, key_slots;       // rows of a query buffer, tiles of keys in shared memory
   int32_t slots, chunks;           // group numbers, stretches of unit_blocks blocks
   int32_t unit_blocks;
+  uint32_t block_inv;              // 2^32 / block, rounded up
   int32_t test_stall;
   uint64_t wait_limit_ns;
 };
-int index_scores_columns(int T, int B, int H);
-cudaError_t launch_index_scores(IndexScoreArgs a, int columns, int num_sms, cudaStream_t s);
+cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s);
 
 struct SelectArgs {
   const float* scores;             // rows of C, stride elements apart

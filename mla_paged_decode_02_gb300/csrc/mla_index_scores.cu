@@ -4,23 +4,25 @@
 //   s_j = scale_j sum_h w_h max(0, q_h . k_j),   S_c = max over the seen keys j of block c of s_j,
 // -inf for a block without one; a NaN counts as -inf.
 //
-// Keys on M. A tile is 128 keys (A, 128 bytes each) against the heads of a group of neighbouring tokens
-// of one sequence (B, up to NB rows of 128 bytes): four E4M3 MMAs of K = 32, exact products, float32
-// sums in tensor memory, a key in each lane and a head in each column. So the sum over heads stays in a
-// thread, w_h is the same for all lanes, and only the maximum over a block's keys crosses lanes. A
-// token's heads start at a multiple of 16 columns; the columns between hold whatever follows in memory
-// and are never read.
+// Keys on M. A tile is 128 keys (A, 128 bytes each) against the heads of a few tokens of one sequence
+// (B, up to 128 rows of 128 bytes): four E4M3 MMAs of K = 32, exact products, float32 sums in tensor
+// memory, a key in each lane and a head in each column. So the sum over heads stays in a thread, w_h is the
+// same for all lanes, and only the maximum over a block's keys crosses lanes. A token's heads start
+// at a multiple of 16 columns; the columns between hold whatever follows in memory and are never read.
 //
-// Work is cut into units of one group x `unit_blocks` blocks; persistent CTAs, one per SM, take them in
-// turn, all groups of one stretch of the context before the next, so that groups of a sequence find
-// its keys in L2. A group's number says which sequence it belongs to: sequence b's groups start at
-// cu_q[b] / TG + b (TG tokens to a group), which leaves room enough for each, and a lane finds its
-// unit's by bisection.
+// Work is cut into units of one group of neighbouring tokens x `unit_blocks` blocks; persistent CTAs, one
+// per SM, take them in turn, all groups of one stretch of the context before the next, so that groups of
+// a sequence find its keys in L2. A group is up to four sub-groups of 128 columns, which share each key
+// tile in shared memory. A group's number says which sequence it belongs to: sequence b's groups start at
+// cu_q[b] / TG + b (TG tokens to a group), which leaves room enough for each, and a lane finds its unit's
+// by bisection. (With one token to a group that is token g itself.)
 //
-// Roles (320 threads): warp 0 resolves units, fills blocks that no token sees, and loads queries, weights,
-// keys (TMA boxes from the page table) and their scales; warp 1 issues the MMAs; warps 2-5 and 6-9 take
-// the tiles in turn, each with an accumulator of its own. The maxima of a unit's blocks gather in shared
-// memory. Every wait is bounded; a stall sets the error word, and the CTA drains and leaves.
+// Roles (608 threads): warp 0 resolves units, fills blocks that no token sees, and loads queries, weights,
+// keys (TMA boxes from the page table) and their scales; warps 1 and 2 issue the MMAs, each into a
+// pair of accumulators of 128 columns: two sub-groups of a tile, or two tiles of one; four warpgroups take
+// an accumulator each. The maxima of
+// a unit's blocks gather in shared memory. Every wait is bounded; a stall sets the error word, and the CTA
+// drains and leaves.
 #include "mla_index.h"
 #include "mla_ptx.cuh"
 #include "mla_ragged.cuh"
@@ -29,16 +31,26 @@
 namespace mla {
 namespace {
 
-constexpr int kISThreads = 320;
+constexpr int kISWarps = 16;                      // four warpgroups, two to a pair of accumulators
+constexpr int kISIssuers = 2;                     // issuing warps, one to a pair of accumulators
+constexpr int kISFirst = 1 + kISIssuers;          // first warp of the warpgroups
+constexpr int kISThreads = 32 * (kISFirst + kISWarps);
+constexpr int kISColumns = 128;                   // of an accumulator
+constexpr int kISTmem = 2 * kISIssuers * kISColumns;
 constexpr int kISKeys = 128;                      // keys of a tile
 constexpr int kISSlotBytes = kISKeys * kDIndex;   // 16 KB
-constexpr int kISSlots = 7;
-constexpr int kISBest = 2048;                     // (token, block) maxima of a unit
-constexpr int kISMaxTokens = 16;                  // 256 columns / 16
-
-template <int NB>
-constexpr int is_smem_bytes() {
-  return 1024 + 2 * NB * kDIndex + kISSlots * (kISSlotBytes + kISKeys * 4) + 2 * kISBest * 4 + 2 * NB * 4;
+constexpr int kISMaxSlots = 12;
+// Key scales have a ring of their own, read later than the keys. A slot of it is filled for tile t + 16
+// once the MMAs of tile t + 16 - 12 or a later one are done, which were issued after the product four
+// before them, of tile t or later, had been read.
+constexpr int kISScales = 16;
+constexpr uint32_t kISFirstWaitNs = 20000;        // a wait's first, sleeping look
+constexpr int kISBest = 1024;                     // (token, block) maxima of a unit
+constexpr int kISMaxTokens = 32;                  // of a group: 512 columns / 16
+constexpr int kISBases = 1024;                    // sequences whose first groups are kept in shared memory
+constexpr int kISSmem = 222 * 1024;               // dynamic
+constexpr int is_fixed_bytes(int q_rows) {
+  return 1024 + 2 * q_rows * kDIndex + kISScales * kISKeys * 4 + 2 * kISBest * 4 + 2 * q_rows * 4;
 }
 
 // an order-preserving code of a float, so that maxima can be taken as integers
@@ -52,14 +64,42 @@ constexpr int kLowest = (int)0x807FFFFFu;         // ordered(-inf)
 // max(0, x) that keeps a NaN
 __device__ __forceinline__ float positive(float x) {
   float y;
-  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+  asm volatile("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
   return y;
 }
-// (a, b) += (x, y) * (u, v)
-__device__ __forceinline__ void fma2(float& a, float& b, float x, float y, float u, float v) {
-  asm("{\n\t.reg .b64 p, q, r;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 r, {%0, %1};\n\t"
-      "fma.rn.f32x2 r, p, q, r;\n\tmov.b64 {%0, %1}, r;\n\t}"
-      : "+f"(a), "+f"(b) : "f"(x), "f"(y), "f"(u), "f"(v));
+// Two values to an instruction: acc = w max(0, (x, y)) + (first ? 0 : acc). Volatile, so that it stays
+// behind the wait for the tensor-memory load that brings x and y.
+template <bool kFirst>
+__device__ __forceinline__ void add_positive2(uint64_t& acc, float x, float y, uint64_t w) {
+  if (kFirst)
+    asm volatile("{\n\t.reg .f32 a, b;\n\t.reg .b64 p;\n\tmax.NaN.f32 a, %1, 0f00000000;\n\t"
+                 "max.NaN.f32 b, %2, 0f00000000;\n\tmov.b64 p, {a, b};\n\tmul.rn.f32x2 %0, p, %3;\n\t}"
+                 : "=l"(acc) : "f"(x), "f"(y), "l"(w));
+  else
+    asm volatile("{\n\t.reg .f32 a, b;\n\t.reg .b64 p;\n\tmax.NaN.f32 a, %1, 0f00000000;\n\t"
+                 "max.NaN.f32 b, %2, 0f00000000;\n\tmov.b64 p, {a, b};\n\tfma.rn.f32x2 %0, p, %3, %0;\n\t}"
+                 : "+l"(acc) : "f"(x), "f"(y), "l"(w));
+}
+// The same with x + |x| = 2 max(0, x) in its place, on the FMA pipe instead of the ALU.
+template <bool kFirst>
+__device__ __forceinline__ void add_positive2_twice(uint64_t& acc, float x, float y, uint64_t w) {
+  if (kFirst)
+    asm volatile("{\n\t.reg .f32 a, b;\n\t.reg .b64 p;\n\tabs.f32 a, %1;\n\tabs.f32 b, %2;\n\tadd.rn.f32 a, a, %1;\n\t"
+                 "add.rn.f32 b, b, %2;\n\tmov.b64 p, {a, b};\n\tmul.rn.f32x2 %0, p, %3;\n\t}"
+                 : "=l"(acc) : "f"(x), "f"(y), "l"(w));
+  else
+    asm volatile("{\n\t.reg .f32 a, b;\n\t.reg .b64 p;\n\tabs.f32 a, %1;\n\tabs.f32 b, %2;\n\tadd.rn.f32 a, a, %1;\n\t"
+                 "add.rn.f32 b, b, %2;\n\tmov.b64 p, {a, b};\n\tfma.rn.f32x2 %0, p, %3, %0;\n\t}"
+                 : "+l"(acc) : "f"(x), "f"(y), "l"(w));
+}
+// three pairs, and half of the fourth
+__device__ __forceinline__ float sum8(const uint64_t* s) {
+  float r;
+  asm("{\n\t.reg .b64 a, b;\n\t.reg .f32 x, y, u, v;\n\tadd.rn.f32x2 a, %1, %2;\n\tadd.rn.f32x2 a, a, %3;\n\t"
+      "mov.b64 {x, y}, a;\n\tmov.b64 {u, v}, %4;\n\tadd.rn.f32 x, x, y;\n\tadd.rn.f32 u, u, v;\n\t"
+      "fma.rn.f32 %0, u, 0f3F000000, x;\n\t}"
+      : "=f"(r) : "l"(s[0]), "l"(s[1]), "l"(s[2]), "l"(s[3]));
+  return r;
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -72,8 +112,53 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                :: "r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar) : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
-  tmem_ld16(taddr, v);
-  tmem_ld16(taddr + 16, v + 16);
+  uint32_t r[32];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                 "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                 "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+// the largest of the warp's values, NaN aside (NaN if all are)
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// CS heads of a token, its first ones or further ones, in four pairs of sums for short chains. max runs
+// on the ALU at half the rate of the FMA pipe: a quarter of the heads takes the other form.
+template <int CS, bool kFirst>
+__device__ __forceinline__ void add_heads(const float* v, const float* w, uint64_t* s) {
+#pragma unroll
+  for (int k = 0; k < CS; k += 8) {
+    const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(w + k), y = *reinterpret_cast<const ulonglong2*>(w + k + 4);
+    if (kFirst && k == 0) {
+      add_positive2<true>(s[0], v[k], v[k + 1], x.x);
+      add_positive2<true>(s[1], v[k + 2], v[k + 3], x.y);
+      add_positive2<true>(s[2], v[k + 4], v[k + 5], y.x);
+      add_positive2_twice<true>(s[3], v[k + 6], v[k + 7], y.y);
+    } else {
+      add_positive2<false>(s[0], v[k], v[k + 1], x.x);
+      add_positive2<false>(s[1], v[k + 2], v[k + 3], x.y);
+      add_positive2<false>(s[2], v[k + 4], v[k + 5], y.x);
+      add_positive2_twice<false>(s[3], v[k + 6], v[k + 7], y.y);
+    }
+  }
+}
+template <int CS>
+__device__ __forceinline__ void load_heads(uint32_t taddr, float* v) {
+  if (CS == 32) tmem_ld32(taddr, v);
+  else tmem_ld16(taddr, v);
+}
+
+// The rest of a wait that was not over at the first look, out of line.
+__device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, uint32_t abort_s, uint32_t* err, uint64_t limit_ns) {
+  volatile uint32_t* flag = reinterpret_cast<volatile uint32_t*>(__cvta_shared_to_generic(abort_s));
+  return mbar_wait(bar, parity, flag, err, MLA_DEVERR_TIMEOUT, limit_ns);
 }
 
 // A unit as the producer announces it.
@@ -84,63 +169,74 @@ struct UnitInfo {
   int seen[kISMaxTokens];
 };
 
+// The first group of sequence b, whose tokens start at row `start`.
+__device__ __forceinline__ int first_group(const IndexScoreArgs& a, int start, int b) {
+  return a.TG == 1 ? start : start / a.TG + b;
+}
+
 __device__ uint32_t g_unreported;                 // error bits of calls without an error word
 
 }  // namespace
 
-template <int NB>
+// CPT: 32-column chunks of a token, whose 32 CPT heads fill them; 0: any number of heads, 16 columns at a
+// time.
+template <int CPT>
 __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __grid_constant__ IndexScoreArgs a) {
+  constexpr int CS = CPT == 0 ? 16 : 32;
   extern __shared__ uint8_t dsmem_raw[];
-  __shared__ __align__(8) uint64_t bar_kfull[kISSlots], bar_kempty[kISSlots], bar_qfull[2], bar_qempty[2], bar_tfull[2],
-      bar_tempty[2], bar_unit, bar_drain, bar_never;
+  __shared__ __align__(8) uint64_t bar_kfull[kISMaxSlots], bar_kempty[kISMaxSlots], bar_qfull[2],
+      bar_qempty[2], bar_tfull[kISIssuers], bar_tempty[kISIssuers], bar_drain[kISIssuers], bar_unit, bar_never;
   __shared__ UnitInfo info_s[2];
+  __shared__ int base_s[kISBases];                  // a sequence's first group
   __shared__ uint32_t tmem_base_s, abort_s;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int S = a.key_slots, q_rows = a.q_rows;
   const uint32_t raw = smem_u32(dsmem_raw);
-  const uint32_t sQ = (raw + 1023u) & ~1023u, sK = sQ + 2 * NB * kDIndex;
-  uint8_t* gQ = dsmem_raw + (sQ - raw);
-  float* gS = reinterpret_cast<float*>(gQ + 2 * NB * kDIndex + kISSlots * kISSlotBytes);   // key scales
-  const uint32_t sS = sK + kISSlots * kISSlotBytes;
-  int* best = reinterpret_cast<int*>(gS + kISSlots * kISKeys);                             // [2][kISBest]
-  float* gW = reinterpret_cast<float*>(best + 2 * kISBest);                                // [2][NB]
+  const uint32_t sQ = (raw + 1023u) & ~1023u, sK = sQ + 2 * q_rows * kDIndex, sS = sK + S * kISSlotBytes;
+  float* gS = reinterpret_cast<float*>(dsmem_raw + (sS - raw));       // key scales
+  int* best = reinterpret_cast<int*>(gS + kISScales * kISKeys);       // [2][kISBest]
+  float* gW = reinterpret_cast<float*>(best + 2 * kISBest);           // [2][q_rows]
   const uint32_t b_kfull = smem_u32(bar_kfull), b_kempty = smem_u32(bar_kempty);
   const uint32_t b_qfull = smem_u32(bar_qfull), b_qempty = smem_u32(bar_qempty);
   const uint32_t b_tfull = smem_u32(bar_tfull), b_tempty = smem_u32(bar_tempty);
-  const uint32_t b_unit = smem_u32(&bar_unit), b_drain = smem_u32(&bar_drain), b_never = smem_u32(&bar_never);
-  volatile uint32_t* abort_flag = &abort_s;
+  const uint32_t b_unit = smem_u32(&bar_unit), b_drain = smem_u32(bar_drain), b_never = smem_u32(&bar_never);
   uint32_t* err = a.err != nullptr ? a.err : &g_unreported;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kISSlots; ++i) {
+    for (int i = 0; i < kISMaxSlots; ++i) {
       mbar_init(b_kfull + 8 * i, 1);
-      mbar_init(b_kempty + 8 * i, 1 + 4);     // the MMAs, and the warps that have read the scales
+      mbar_init(b_kempty + 8 * i, kISIssuers);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(b_qfull + 8 * i, 1);
-      mbar_init(b_qempty + 8 * i, 1 + 8);     // the MMAs, and the warps that are done with the unit
-      mbar_init(b_tfull + 8 * i, 1);
-      mbar_init(b_tempty + 8 * i, 4);
+      mbar_init(b_qempty + 8 * i, kISIssuers + kISWarps);   // the MMAs, and the warps that are done with the unit
     }
-    mbar_init(b_unit, 8);
-    mbar_init(b_drain, 1);
+    for (int i = 0; i < kISIssuers; ++i) {
+      mbar_init(b_tfull + 8 * i, 2);               // the MMAs, and the issuing thread, which saw the scales land
+      mbar_init(b_tempty + 8 * i, 8);
+      mbar_init(b_drain + 8 * i, 1);
+    }
+    mbar_init(b_unit, kISWarps);
     mbar_init(b_never, 1);
     abort_s = 0u;
     fence_mbarrier_init();
     tma_prefetch_desc(&a.tm_q);
     tma_prefetch_desc(&a.tm_k);
   }
-  if (warp == 1) tmem_alloc(smem_u32(&tmem_base_s), 2 * NB);
+  if (warp == 1) tmem_alloc(smem_u32(&tmem_base_s), kISTmem);
   for (int i = threadIdx.x; i < 2 * kISBest; i += kISThreads) best[i] = kLowest;
+  griddep_wait();
+  griddep_launch_dependents();
+  for (int b = threadIdx.x; b < min(a.B, kISBases); b += kISThreads) base_s[b] = first_group(a, a.cu_q[b], b);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_s;
-  griddep_wait();
-  griddep_launch_dependents();
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns));
+    return __all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, kISFirstWaitNs) ||
+                                       wait_longer(bar, parity, smem_u32(&abort_s), err, a.wait_limit_ns));
   };
-  const int TG = a.TG, Hp = a.Hp;
+  const int TG = a.TG, Hp = a.Hp, sub_tokens = a.sub_tokens;
 
   if (warp == 0) {
     // ---------------------------------------------------------------------- units, queries, keys
@@ -149,6 +245,7 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
     uint32_t slot = 0, ph = 1, nu = 0, filled = 0;
     bool ok = true;
     const int64_t total = (int64_t)a.slots * a.chunks;
+    const bool wide_weights = (reinterpret_cast<uintptr_t>(a.w) & 15) == 0;
     for (int64_t base = blockIdx.x; base < total && ok; base += 32 * (int64_t)gridDim.x) {
       // 32 units at a time, one to a lane
       const int64_t u = base + (int64_t)lane * gridDim.x;
@@ -158,14 +255,15 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
         int lo = 0, hi = a.B;                           // the last b with cu_q[b] / TG + b <= g
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
-          if (a.cu_q[mid] / TG + mid <= g) lo = mid;
+          if ((mid < kISBases ? base_s[mid] : first_group(a, a.cu_q[mid], mid)) <= g) lo = mid;
           else hi = mid;
         }
         b = lo;
         start = max(0, a.cu_q[b]);
         end = min(a.T, a.cu_q[b + 1]);
-        const int64_t first = (int64_t)start + (int64_t)(g - (start / TG + b)) * TG;
-        if (g >= start / TG + b && first < end) {
+        const int skip = g - first_group(a, start, b);
+        const int64_t first = (int64_t)start + (int64_t)skip * TG;
+        if (skip >= 0 && first < end) {
           t0 = (int)first;
           ntok = min(TG, end - t0);
           L = max(0, min(a.seq_lens[b], a.max_len));
@@ -189,6 +287,20 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
           continue;
         }
         const int tiles = (ulast - uk0 + kISKeys - 1) / kISKeys;
+        // the first rows of the unit's boxes, 32 at a time (one to a lane), 32 ahead
+        const int32_t* pages = a.block_table + (int64_t)ub * a.MB;
+        auto row_of = [&](int box) -> int {
+          const int tok = uk0 + box * a.box_rows;
+          if (tok >= ulast) return -1;
+          const int page = tok / a.P, in = tok - page * a.P;
+          int pg = __ldg(pages + page);
+          if (pg < 0 || pg >= a.num_pages) {
+            atomicOr(err, MLA_DEVERR_BLOCK_TABLE);
+            pg = 0;
+          }
+          return pg * a.P + in;
+        };
+        int rows = row_of(lane), ahead = row_of(lane + 32);
         const uint32_t qb = nu & 1;
         ok = wait(b_qempty + 8 * qb, ((nu >> 1) & 1) ^ 1);
         if (!ok) break;
@@ -202,35 +314,32 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
           I.blocks = blocks;
         }
         if (lane < un) I.seen[lane] = keys_seen(ut0 + lane, ustart, uend, uL, a.causal);
-        for (int i = lane; i < un * a.H; i += 32) gW[qb * NB + (i / a.H) * Hp + i % a.H] = a.w[(int64_t)ut0 * a.H + i];
+        // weights: one copy where a token's fill its columns, else by loads
+        const uint32_t wbytes = a.H == Hp && wide_weights ? (uint32_t)(un * Hp) * 4 : 0u;
+        if (wbytes == 0)
+          for (int i = lane; i < un * a.H; i += 32) gW[qb * q_rows + (i / a.H) * Hp + i % a.H] = a.w[(int64_t)ut0 * a.H + i];
         __syncwarp();
         const int qboxes = un * (Hp / 16);
-        if (el) mbar_arrive_expect_tx(b_qfull + 8 * qb, (uint32_t)qboxes * 16 * kDIndex);
+        if (el) {
+          mbar_arrive_expect_tx(b_qfull + 8 * qb, (uint32_t)qboxes * 16 * kDIndex + wbytes);
+          if (wbytes) bulk_load(smem_u32(gW + qb * q_rows), a.w + (int64_t)ut0 * a.H, wbytes, b_qfull + 8 * qb);
+        }
         __syncwarp();
         for (int i = lane; i < qboxes; i += 32)
-          tma_load_2d(sQ + qb * NB * kDIndex + i * 16 * kDIndex, &a.tm_q, b_qfull + 8 * qb, 0,
+          tma_load_2d(sQ + qb * q_rows * kDIndex + i * 16 * kDIndex, &a.tm_q, b_qfull + 8 * qb, 0,
                       (ut0 + i / (Hp / 16)) * a.H + (i % (Hp / 16)) * 16);
         ++nu;
-        // a lane's boxes of the unit: their pages one tile ahead
-        const int32_t* pages = a.block_table + (int64_t)ub * a.MB;
-        auto row_of = [&](int tile) -> int {
-          const int tok = uk0 + tile * kISKeys + lane * a.box_rows;
-          if (lane >= per || tok >= ulast) return -1;
-          const int page = tok / a.P, in = tok - page * a.P;
-          int pg = __ldg(pages + page);
-          if (pg < 0 || pg >= a.num_pages) {
-            atomicOr(err, MLA_DEVERR_BLOCK_TABLE);
-            pg = 0;
-          }
-          return pg * a.P + in;
-        };
-        int row = row_of(0);
         for (int tile = 0; tile < tiles; ++tile) {
-          const int next = tile + 1 < tiles ? row_of(tile + 1) : -1;
+          const int at = tile * per & 31;                 // per divides 32
+          if (tile > 0 && at == 0) {
+            rows = ahead;
+            ahead = row_of((tile * per & ~31) + 32 + lane);
+          }
+          const int row = __shfl_sync(0xffffffffu, rows, at + (lane & (per - 1)));
+          const int valid = __popc(__ballot_sync(0xffffffffu, lane < per && row >= 0));
           ok = wait(b_kempty + 8 * slot, ph);
           if (!ok) break;
-          const int valid = __popc(__ballot_sync(0xffffffffu, row >= 0));
-          const uint32_t bar = b_kfull + 8 * slot;
+          const uint32_t bar = b_kfull + 8 * slot, sc = filled % kISScales;
           if (el) mbar_arrive_expect_tx(bar, kISSlotBytes + (uint32_t)(valid * a.box_rows * 4));
           __syncwarp();
           if (lane < per) {
@@ -238,11 +347,10 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
             tma_load_2d(sK + slot * kISSlotBytes + lane * a.box_rows * kDIndex, &a.tm_k, bar, 0,
                         row >= 0 ? row : a.total_rows);
             if (row >= 0)
-              bulk_load(sS + (slot * kISKeys + lane * a.box_rows) * 4, a.scale + row, (uint32_t)a.box_rows * 4, bar);
+              bulk_load(sS + (sc * kISKeys + lane * a.box_rows) * 4, a.scale + row, (uint32_t)a.box_rows * 4, bar);
           }
-          row = next;
           ++filled;
-          if (++slot == kISSlots) { slot = 0; ph ^= 1; }
+          if (++slot == (uint32_t)S) { slot = 0; ph ^= 1; }
         }
       }
     }
@@ -259,65 +367,91 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
     if (!ok) {
       // copies in flight land before the CTA leaves: the last fill of each slot
       volatile uint32_t none = 0u;
+      auto land = [&](uint32_t bar, uint32_t fill, uint32_t of) {
+        mbar_wait(bar + 8 * (fill % of), (fill / of) & 1, &none, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns);
+      };
       if (lane == 0) {
-        for (uint32_t f = filled > kISSlots ? filled - kISSlots : 0; f < filled; ++f)
-          mbar_wait(b_kfull + 8 * (f % kISSlots), (f / kISSlots) & 1, &none, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns);
-        for (uint32_t k = nu >= 2 ? nu - 2 : 0; k < nu; ++k)
-          mbar_wait(b_qfull + 8 * (k & 1), (k >> 1) & 1, &none, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns);
+        for (uint32_t f = filled > (uint32_t)S ? filled - S : 0; f < filled; ++f) land(b_kfull, f, S);
+        for (uint32_t k = nu >= 2 ? nu - 2 : 0; k < nu; ++k) land(b_qfull, k, 2);
       }
       __syncwarp();
     }
-  } else if (warp == 1) {
+  } else if (warp < kISFirst) {
     // ---------------------------------------------------------------------------------- MMAs
     const bool el = elect_one();
-    uint32_t slot = 0, ph = 0, nt = 0;
+    const uint32_t me = (uint32_t)warp - 1;             // the pair of accumulators this warp fills
+    const uint32_t acc = tmem + me * 2 * kISColumns, b_full = b_tfull + 8 * me, b_free = b_tempty + 8 * me;
+    uint32_t slot = 0, ph = 0, n = 0, mine = 0;         // n: products so far, of both; mine: of this warp
     bool ok = true;
     for (uint32_t nu = 0; ok; ++nu) {
       const uint32_t qb = nu & 1;
       ok = wait(b_qfull + 8 * qb, (nu >> 1) & 1);
       if (!ok) break;
-      const int ntok = info_s[qb].ntok, tiles = info_s[qb].tiles;
+      // (the same in every lane, which the compiler can use for the descriptors)
+      const int ntok = __shfl_sync(0xffffffffu, info_s[qb].ntok, 0), tiles = __shfl_sync(0xffffffffu, info_s[qb].tiles, 0);
       if (ntok == 0) break;
-      const uint32_t idesc = make_idesc(128, (uint32_t)(ntok * Hp), 0, 0, 0);
-      const uint64_t qd = make_sdesc(sQ + qb * NB * kDIndex, 16, 1024, kSwizzle128);
-      for (int tile = 0; tile < tiles; ++tile, ++nt) {
-        const uint32_t st = nt & 1;
-        ok = wait(b_tempty + 8 * st, ((nt >> 1) & 1) ^ 1) && wait(b_kfull + 8 * slot, ph);
+      const uint64_t qd = make_sdesc(sQ + qb * q_rows * kDIndex, 16, 1024, kSwizzle128);
+      const bool one = ntok <= sub_tokens;              // one sub-group: a product is two tiles of it
+      const int pair = 2 * sub_tokens;
+      for (int tile = 0; tile < tiles && ok; tile += one ? 2 : 1) {
+        const bool two = one && tile + 1 < tiles;
+        const uint32_t slot1 = slot + 1 == (uint32_t)S ? 0 : slot + 1, ph1 = slot1 == 0 ? ph ^ 1 : ph;
+        ok = wait(b_kfull + 8 * slot, ph) && (!two || wait(b_kfull + 8 * slot1, ph1));
         if (!ok) break;
-        tc_fence_after();
-        if (el) {
-          const uint64_t kd = make_sdesc(sK + slot * kISSlotBytes, 16, 1024, kSwizzle128);
+        const uint64_t kd = make_sdesc(sK + slot * kISSlotBytes, 16, 1024, kSwizzle128);
+        for (int t = 0; t < ntok; t += pair, ++n) {
+          if ((n & 1) != me) continue;
+          ok = wait(b_free, (mine & 1) ^ 1);
+          if (!ok) break;
+          ++mine;
+          tc_fence_after();
+          if (el) {
+            const uint32_t idesc = make_idesc(128, (uint32_t)(min(pair, ntok - t) * Hp), 0, 0, 0);
+            const uint64_t qt = qd + (uint64_t)((uint32_t)(t * Hp * kDIndex) >> 4);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) umma_f8(tmem + st * NB, kd + 2 * k, qd + 2 * k, idesc, k > 0);
+            for (int k = 0; k < 4; ++k) umma_f8(acc, kd + 2 * k, qt + 2 * k, idesc, k > 0);
+            if (two) {
+              const uint64_t kd1 = make_sdesc(sK + slot1 * kISSlotBytes, 16, 1024, kSwizzle128);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) umma_f8(acc + kISColumns, kd1 + 2 * k, qt + 2 * k, idesc, k > 0);
+            }
+            umma_commit(b_full);
+            mbar_arrive(b_full);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        // both issuing warps see every tile land before they give its slot back
+        if (el) {
           umma_commit(b_kempty + 8 * slot);
-          umma_commit(b_tfull + 8 * st);
-          if (tile + 1 == tiles) umma_commit(b_qempty + 8 * qb);
+          if (two) umma_commit(b_kempty + 8 * slot1);
+          if (tile + (one ? 2 : 1) >= tiles) umma_commit(b_qempty + 8 * qb);
         }
         __syncwarp();
-        if (++slot == kISSlots) { slot = 0; ph ^= 1; }
+        if (two) { slot = slot1; ph = ph1; }
+        if (++slot == (uint32_t)S) { slot = 0; ph ^= 1; }
       }
     }
     if (!ok) {
       // the MMAs issued so far complete before tensor memory is freed
       volatile uint32_t none = 0u;
-      if (el) {
-        umma_commit(b_drain);
-        mbar_wait(b_drain, 0, &none, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns);
-      }
+      if (el) umma_commit(b_drain + 8 * me);
+      if (lane == 0) mbar_wait(b_drain + 8 * me, 0, &none, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns);
       __syncwarp();
     }
   } else {
     // --------------------------------------------------------- sums over heads, maxima over keys
-    const uint32_t wg = warp >= 6 ? 1u : 0u;
+    const uint32_t wg = (uint32_t)(warp - kISFirst) >> 2, set = wg >> 1, half = wg & 1;   // pair, and which of it
     const int quad = warp & 3;                          // tensor-memory lanes 32 quad ..
-    const int et = threadIdx.x - 64;                    // thread of the 256
-    const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16) + wg * NB;
+    const int et = threadIdx.x - 32 * kISFirst;
+    const uint32_t acc_set = tmem + ((uint32_t)(quad * 32) << 16) + set * 2 * kISColumns;
+    const uint32_t b_full = b_tfull + 8 * set, b_free = b_tempty + 8 * set;
     // errors that only the device can see
-    for (int b = blockIdx.x * 256 + et; b < a.B; b += gridDim.x * 256) {
+    for (int b = blockIdx.x * (32 * kISWarps) + et; b < a.B; b += gridDim.x * (32 * kISWarps)) {
       const uint32_t bad = ragged_errors(a.cu_q, a.seq_lens, b, a.T, a.max_len);
       if (bad) atomicOr(err, bad);
     }
-    uint32_t slot = 0, ph = 0, nt = 0;
+    uint32_t nt = 0, n = 0, taken = 0;                  // tiles and products so far, products of this pair
     bool ok = !(a.test_stall && !wait(b_never, 0));
     const bool whole = a.block % 32 == 0;               // a warp's keys lie in one block
     const int H = a.H;
@@ -329,66 +463,112 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
       const int ntok = I.ntok, tiles = I.tiles;
       if (ntok == 0) break;
       int* mine = best + qb * kISBest;
-      for (int tile = 0; tile < tiles; ++tile, ++nt) {
-        const uint32_t my_slot = slot, my_ph = ph;
-        if (++slot == kISSlots) { slot = 0; ph ^= 1; }
-        if ((nt & 1) != wg) continue;
-        ok = wait(b_tfull + 8 * wg, (nt >> 1) & 1) && wait(b_kfull + 8 * my_slot, my_ph);
+      const bool one = ntok <= sub_tokens;
+      const int turns = ntok > 2 * sub_tokens ? 2 : 1;  // products of a tile
+      const int products = one ? (tiles + 1) >> 1 : tiles * turns;
+      for (int m = (int)((n + set) & 1); m < products; m += 2, ++taken) {
+        const int tile = one ? 2 * m + (int)half : m >> (turns - 1);
+        const int t0 = one ? 0 : (2 * (m & (turns - 1)) + (int)half) * sub_tokens;
+        ok = wait(b_full, taken & 1);
         if (!ok) break;
+        // the accumulator has been read
+        auto release = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b_free);
+        };
+        if (tile >= tiles || t0 >= ntok) {              // the pair's second half is empty
+          release();
+          continue;
+        }
+        const uint32_t gt = nt + (uint32_t)tile;
+        const uint32_t acc = acc_set + half * (uint32_t)(one ? kISColumns : sub_tokens * Hp);
         tc_fence_after();
-        const float ks = gS[my_slot * kISKeys + quad * 32 + lane];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(b_kempty + 8 * my_slot);
+        const float ks = gS[(gt % kISScales) * kISKeys + quad * 32 + lane];
         const int in = tile * kISKeys + quad * 32 + lane;     // key within the unit
         const int key = I.k0 + in;
-        const int block = (whole ? in - lane : in) / a.block;
-        int keep = kLowest;
-        for (int i = 0; i < ntok; ++i) {
-          const float* w = gW + qb * NB + i * Hp;
-          float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-          int c = 0;
-          for (; c + 32 <= H; c += 32) {
-            float v[32];
-            tmem_ld32(lane_base + i * Hp + c, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float4 x = *reinterpret_cast<const float4*>(w + c + k);
-              fma2(s0, s1, positive(v[k]), positive(v[k + 1]), x.x, x.y);
-              fma2(s2, s3, positive(v[k + 2]), positive(v[k + 3]), x.z, x.w);
-            }
-          }
-          for (; c < H; c += 16) {
-            float v[16];
-            tmem_ld16(lane_base + i * Hp + c, v);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (c + k < H) s0 = fmaf(positive(v[k]), w[c + k], s0);
-          }
-          float s = ((s0 + s1) + (s2 + s3)) * ks;
-          s = key < I.seen[i] && s > -INFINITY ? s : -INFINITY;
+        const int toks = min(sub_tokens, ntok - t0);
+        const bool all_see = I.k0 + (tile + 1) * kISKeys <= I.seen[t0];
+        const float* w = gW + qb * q_rows + t0 * Hp;
+        int* to = mine + t0 * a.unit_blocks + (int)__umulhi((uint32_t)(whole ? in - lane : in), a.block_inv);
+        float keep = -INFINITY;
+        auto finish = [&](int i, float x) {             // the sum of token t0 + i
+          x *= ks;
+          if (!all_see && key >= I.seen[t0 + i]) x = -INFINITY;
           if (whole) {
-            const int m = __reduce_max_sync(0xffffffffu, ordered(s));
-            if (lane == i) keep = m;
+            x = warp_max(x);
+            if (lane == i) keep = x;
           } else {
 #pragma unroll
-            for (int o = 4; o > 0; o >>= 1) s = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, o));
-            if ((lane & 7) == 0) atomicMax(mine + i * a.unit_blocks + block, ordered(s));
+            for (int o = 4; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+            if ((lane & 7) == 0 && x > -INFINITY) atomicMax(to + i * a.unit_blocks, ordered(x));
+          }
+        };
+        uint64_t s[4];
+        if (CPT == 0) {
+          float v[CS];
+          for (int i = 0; i < toks; ++i) {
+            s[0] = s[1] = s[2] = s[3] = 0ull;
+            float rest = 0.f;
+            for (int c = 0; c < H; c += CS) {
+              load_heads<CS>(acc + i * Hp + c, v);
+              tmem_wait_ld();
+              if (c + CS <= H) {
+                add_heads<CS, false>(v, w + i * Hp + c, s);
+              } else {
+#pragma unroll
+                for (int k = 0; k < CS; ++k)
+                  if (c + k < H) rest = fmaf(positive(v[k]), w[i * Hp + c + k], rest);
+              }
+            }
+            finish(i, sum8(s) + rest);
+          }
+          release();
+        } else if (toks * CPT == 4) {
+          // two buffers: a chunk is on its way while the one before it is summed
+          float va[CS], vb[CS];
+          load_heads<CS>(acc, va);
+#pragma unroll
+          for (int c = 0; c < 4; c += 2) {
+            tmem_wait_ld();
+            load_heads<CS>(acc + (c + 1) * CS, vb);
+            if (CPT < 4 || c == 0) add_heads<CS, true>(va, w + c * CS, s);
+            else add_heads<CS, false>(va, w + c * CS, s);
+            if (CPT == 1) finish(c, sum8(s));
+            tmem_wait_ld();
+            if (c == 0) load_heads<CS>(acc + 2 * CS, va);
+            else release();
+            if (CPT == 1) add_heads<CS, true>(vb, w + (c + 1) * CS, s);
+            else add_heads<CS, false>(vb, w + (c + 1) * CS, s);
+            if (CPT == 1) finish(c + 1, sum8(s));
+            if (CPT == 2) finish(c >> 1, sum8(s));
+            if (CPT == 4 && c == 2) finish(0, sum8(s));
+          }
+        } else {
+          float v[CS];
+          for (int i = 0; i < toks; ++i) {
+#pragma unroll
+            for (int c = 0; c < CPT; ++c) {
+              load_heads<CS>(acc + (i * CPT + c) * CS, v);
+              tmem_wait_ld();
+              if (c == 0) add_heads<CS, true>(v, w + (i * CPT + c) * CS, s);
+              else add_heads<CS, false>(v, w + (i * CPT + c) * CS, s);
+            }
+            if (i + 1 == toks) release();
+            finish(i, sum8(s));
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(b_tempty + 8 * wg);
-        if (whole && lane < ntok) atomicMax(mine + lane * a.unit_blocks + block, keep);
+        if (whole && lane < toks && keep > -INFINITY) atomicMax(to + lane * a.unit_blocks, ordered(keep));
       }
       if (!ok) break;
+      n += (uint32_t)products;
+      nt += (uint32_t)tiles;
       __syncwarp();
-      if (lane == 0) mbar_arrive(b_unit);               // all eight warps' maxima are in
+      if (lane == 0) mbar_arrive(b_unit);               // all warps' maxima are in
       ok = wait(b_unit, nu & 1);
       if (!ok) break;
-      const int n = ntok * a.unit_blocks;
-      for (int x = et; x < n; x += 256) {
+      const int all = ntok * a.unit_blocks;
+      for (int x = et; x < all; x += 32 * kISWarps) {
         const int i = x / a.unit_blocks, c = x - i * a.unit_blocks;
         if (c < I.blocks) a.out[(int64_t)(I.t0 + i) * a.C + I.c0 + c] = from_ordered(mine[x]);
         mine[x] = kLowest;
@@ -400,50 +580,52 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, 2 * NB);
+  if (warp == 1) tmem_dealloc(tmem, kISTmem);
 }
 
-// Columns of the accumulators: a decode step's groups are one token, whose heads take 64 or 128; with
-// two tokens or more to a sequence on average, up to 256 columns of them share each key tile.
-int index_scores_columns(int T, int B, int H) { return T >= 2 * (int64_t)B ? 256 : H <= 64 ? 64 : 128; }
-
-cudaError_t launch_index_scores(IndexScoreArgs a, int columns, int num_sms, cudaStream_t s) {
+cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s) {
   a.Hp = (a.H + 15) / 16 * 16;
-  a.TG = columns / a.Hp;
-  if (columns < 256) a.TG = 1;
-  if (a.TG > kISMaxTokens) a.TG = kISMaxTokens;
-  a.slots = a.T / a.TG + a.B;
+  a.sub_tokens = kISColumns / a.Hp;
+  // a decode step's groups are one token; with two tokens or more to a sequence on average, up to four
+  // sub-groups share each key tile
+  const bool many = a.T >= 2 * (int64_t)a.B;
+  a.TG = many ? 2 * kISIssuers * a.sub_tokens : 1;
+  a.q_rows = a.TG * a.Hp;
+  a.slots = a.TG == 1 ? a.T : a.T / a.TG + a.B;
+  a.key_slots = (kISSmem - is_fixed_bytes(a.q_rows)) / kISSlotBytes;
+  if (a.key_slots > kISMaxSlots) a.key_slots = kISMaxSlots;
+  const int smem = is_fixed_bytes(a.q_rows) + a.key_slots * kISSlotBytes;
   // a unit: whole blocks and whole tiles, about eight units to a CTA, 512 to 8192 keys
   int lcm = a.block;
   while (lcm % kISKeys != 0) lcm += a.block;
   const int64_t groups = (a.T + a.TG - 1) / a.TG;
-  int64_t keys = groups * a.max_len / (8 * (int64_t)num_sms);
-  keys = keys < 512 ? 512 : keys > (columns < 256 ? 1024 : 8192) ? (columns < 256 ? 1024 : 8192) : keys;
+  const int64_t top = many ? 8192 : 1024;
+  int64_t keys = groups * a.max_len / ((many ? 24 : 8) * (int64_t)num_sms);
+  keys = keys < 512 ? 512 : keys > top ? top : keys;
   int64_t m = keys / lcm;
   const int64_t most = kISBest / ((int64_t)a.TG * (lcm / a.block));
   m = m > most ? most : m;
   if (m < 1) m = 1;
   a.unit_blocks = (int)(m * (lcm / a.block));
   a.chunks = (a.C + a.unit_blocks - 1) / a.unit_blocks;
+  a.block_inv = (uint32_t)((((uint64_t)1 << 32) + a.block - 1) / a.block);   // keys of a unit x block < 2^32
   const int64_t total = (int64_t)a.slots * a.chunks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(total < num_sms ? total : num_sms));
   cfg.blockDim = dim3(kISThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto go = [&](auto* kernel, int smem) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    cfg.dynamicSmemBytes = smem;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+  auto go = [&](auto* kernel) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kISSmem);
+    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kernel, a);
   };
-  if (columns == 64) return go(index_scores_kernel<64>, is_smem_bytes<64>());
-  if (columns == 128) return go(index_scores_kernel<128>, is_smem_bytes<128>());
-  return go(index_scores_kernel<256>, is_smem_bytes<256>());
+  return a.H == 32 ? go(index_scores_kernel<1>) : a.H == 64 ? go(index_scores_kernel<2>)
+         : a.H == 128 ? go(index_scores_kernel<4>) : go(index_scores_kernel<0>);
 }
 
 }  // namespace mla
