@@ -295,9 +295,9 @@ mla_status mla_merge_states(const void* out_a, const float* lse_a, const void* o
 
 /* Cache write of new tokens' index keys, and their index queries, with the position rotation on
  * the way. Of a row x of 128 (a key, or one head of a query) the last 64 values are turned as in
- * mla_rope_cache_write; then scale = max(max|x| / 448, 2^-126) and code = e4m3(x / scale), IEEE
- * float32 quotients, rounded to nearest even. A row with a value that is not finite gets a NaN scale
- * (and never a score above -infinity).
+ * mla_rope_cache_write; then, with m = max(max|x|, 448 x 2^-126), scale = m / 448 and code =
+ * e4m3(x (448 / m)): IEEE float32 operations, the code rounded to nearest even. A row with a value
+ * that is not finite gets a NaN scale (and never a score above -infinity).
  *   keys          rows of 128 bf16, key_stride elements apart (a multiple of 8), 16-byte aligned
  *   positions, cos_sin, max_pos, interleaved, slot_mapping   as mla_rope_cache_write; slots >= 0
  *                 are distinct

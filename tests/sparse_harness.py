@@ -105,10 +105,10 @@ class SparseCase(ChunkCase):
 
 def quantised(x):
     """E4M3 codes (uint8) of the rows of x and their float32 scales, as index_cache_write() makes them."""
-    x = x.float()
-    scale = torch.clamp(x.abs().amax(dim=-1) / torch.tensor(448.0), min=2.0 ** -126)
-    code = (x / scale[..., None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
-    return code.view(torch.uint8), scale
+    x, top = x.float(), torch.tensor(448.0)
+    m = torch.clamp(x.abs().amax(dim=-1), min=448 * 2.0 ** -126)
+    code = (x * (top / m)[..., None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
+    return code.view(torch.uint8), m / top
 
 
 class ScoreCase:

@@ -32,8 +32,9 @@ def rotated(x, cs, interleaved):
 
 
 def quantise(x):
-    scale = torch.clamp(x.abs().amax(dim=-1) / torch.tensor(448.0), min=2.0 ** -126)
-    return (x / scale[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8), scale
+    top = torch.tensor(448.0)
+    m = torch.clamp(x.abs().amax(dim=-1), min=448 * 2.0 ** -126)
+    return (x * (top / m)[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8), m / top
 
 
 def table(n, seed=0):
