@@ -926,14 +926,12 @@ MLA_EXPORT mla_status mla_sparse_attention(const mla_sparse_params* p, const voi
   const int per_page = p->page_size / p->block_size;
   SparsePlanArgs pa{};
   pa.sched = chunk_sched_args(ws, w.chunk, p->num_heads, p->num_tokens, pairs, fp8);
-  pa.sched.B = p->num_tokens;
   pa.selected = selected;
   pa.block_table = block_table;
   pa.seq_lens = seq_lens;
   pa.cu_q = cu_q_lens;
   pa.table = reinterpret_cast<int32_t*>(ws + w.table_off);
   pa.lens = reinterpret_cast<int32_t*>(ws + w.lens_off);
-  pa.flags = reinterpret_cast<uint32_t*>(ws + w.flags_off);
   pa.B = p->batch;
   pa.T = p->num_tokens;
   pa.K = p->top_k;

@@ -62,14 +62,13 @@ cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t s);
 // The plan of a sparse attention: each token becomes a sequence of its own whose pages are its
 // selected blocks, ascending, for the chunk attention's kernels.
 struct SparsePlanArgs {
-  ChunkSchedArgs sched;            // hdr, gbase, cta_first, split_list, units, H, workers, setup, tokens
+  ChunkSchedArgs sched;            // hdr, cta_first, split_list, units, H, workers, setup
   const int32_t* selected;         // [T, K]
   const int32_t* block_table;      // [B, MB]
   const int32_t* seq_lens;
   const int32_t* cu_q;             // [B + 1]
   int32_t* table;                  // [T, width]: selected blocks in units of `block` rows of the pool
-  int32_t* lens;                   // [T]: keys of those blocks that the token sees
-  uint32_t* flags;                 // [kPlanCtas]: error bits found by each CTA
+  int32_t* lens;                   // [T]: keys of those blocks that the token sees (for many tokens)
   int32_t B, T, K, width, block, P, MB, num_pages, max_len, causal;
   int32_t words;                   // 32-bit words of a token's set of blocks
 };
@@ -78,13 +77,12 @@ cudaError_t launch_sparse_plan(const SparsePlanArgs& a, cudaStream_t s);
 
 struct SparseWs {
   ChunkWs chunk;
-  size_t flags_off, lens_off, table_off, total;
+  size_t lens_off, table_off, total;
 };
 inline SparseWs sparse_ws_layout(int64_t tokens, int H, int width, int workers) {
   SparseWs w{};
   w.chunk = chunk_ws_layout((int)tokens, tokens, H, workers);
   size_t off = w.chunk.total;
-  w.flags_off = off;  off = align_up(off + sizeof(uint32_t) * kPlanCtas, 256);
   w.lens_off = off;   off = align_up(off + sizeof(int32_t) * (size_t)tokens, 256);
   w.table_off = off;  off = align_up(off + sizeof(int32_t) * (size_t)tokens * (size_t)width, 256);
   w.total = off;

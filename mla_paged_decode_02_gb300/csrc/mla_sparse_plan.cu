@@ -4,111 +4,222 @@
 // kernels that is a sequence of its own, with one new token, pages of `block` rows and a page table
 // that names the chosen blocks in ascending order: only its last page can hold keys that the token
 // does not see, so a length says which keys count. The plan makes that table and those lengths,
-// whatever the order of the caller's list: the chosen blocks are marked in a bit set, so that an index
-// given twice counts once, and those without a key that the token sees (negative ones among them) are
-// left out.
+// whatever the order of the caller's list: blocks without a key that the token sees (negative ones among
+// them) are left out, and a list that does not ascend goes through a bit set, so that an index
+// given twice counts once.
 //
-// One cluster of eight CTAs: a warp takes a token at a time, then the first CTA partitions the tokens'
-// keys over the attention's workers, as the chunk attention's scheduler does.
-#include "mla_chunk_schedule.cuh"
+// Then the tokens' keys are shared out. A token's H rows are ceil(H / 128) blocks of up to 128 rows with
+// equally many tiles of 256 keys; laid end to end, X set-up positions and the tiles for each, worker c
+// (a CTA pair) takes positions [c q, (c + 1) q), q = ceil(all / workers). A block that a boundary cuts
+// becomes one unit per worker. (The partition of the chunk scheduler, without its search for the
+// sequence of a block: here a block's number says which token it belongs to.)
+//
+// One cluster of eight CTAs: a warp takes a token at a time and sends its length to the first CTA's shared
+// memory, where the partition is made. Bound by latency: the list, lengths and offsets are read at once,
+// then the page numbers; after a cluster barrier two scans.
 #include "mla_index.h"
 #include "mla_ptx.cuh"
 #include "mla_ragged.cuh"
+#include "mla_scan.cuh"
 
 namespace mla {
 namespace {
 
-// Token t as a sequence of its own; rows [first, last) belong to sequences.
-struct TokenSeqs {
-  static constexpr bool kMayFlagTable = true;
-  const int32_t* lens;
-  int first, last;
-  __device__ __forceinline__ int start(int t) const { return t; }
-  __device__ __forceinline__ int count(int t) const { return t >= first && t < last ? 1 : 0; }
-  __device__ __forceinline__ int len(int t) const { return lens[t]; }
-  __device__ __forceinline__ uint32_t errors(int) const { return 0u; }
-};
+constexpr int kPlanLens = 8192;            // tokens whose lengths fit the first CTA's shared memory
+
+__device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kChunkTile - 1) / kChunkTile : 1; }
 
 }  // namespace
 
 __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePlanArgs a, int warps) {
-  extern __shared__ uint32_t sets[];                     // [warps][words]
+  extern __shared__ int32_t plan_smem[];   // [T <= kPlanLens] lengths, then [warps][words] sets
   __shared__ int64_t scan_tmp[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ uint32_t flags_s[kPlanCtas];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
   const uint32_t rank = cluster_ctarank();
+  const bool near = a.T <= kPlanLens;
+  // (the first CTA has to run before its shared memory is written)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   griddep_wait();                          // the inputs and the workspace may be the work before's
   griddep_launch_dependents();
   uint32_t bad = 0;
-  for (int b = rank * kSchedThreads + threadIdx.x; b < a.B; b += kPlanCtas * kSchedThreads)
+  for (int b = rank * kSchedThreads + tid; b < a.B; b += kPlanCtas * kSchedThreads)
     bad |= ragged_errors(a.cu_q, a.seq_lens, b, a.T, a.max_len);
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  const uint32_t lens_of_first = map_to_rank(smem_u32(plan_smem), 0);
   if (warp < warps) {
-    uint32_t* set = sets + (size_t)warp * a.words;
+    uint32_t* set = reinterpret_cast<uint32_t*>(plan_smem) + (near ? a.T : 0) + (size_t)warp * a.words;
     const int per_page = a.P / a.block;
-    for (int t = rank * warps + warp; t < a.T; t += kPlanCtas * warps) {
-      const int b = sequence_of(a.cu_q, a.B, t, lane);
-      int seen = 0;
-      if (b >= 0) {
-        const int L = max(0, min(a.seq_lens[b], a.max_len));
-        seen = keys_seen(t, a.cu_q[b], a.cu_q[b + 1], L, a.causal);
-      }
-      const int nb = (seen + a.block - 1) / a.block, nw = (nb + 31) >> 5;
-      for (int w = lane; w < nw; w += 32) set[w] = 0u;
-      __syncwarp();
+    for (int t = rank + kPlanCtas * warp; t < a.T; t += kPlanCtas * warps) {
+      // at once: the list, and what is needed if sequence t is the token's
       const int32_t* chosen = a.selected + (int64_t)t * a.K;
-      for (int k = lane; k < a.K && nb > 0; k += 32) {
-        const int c = chosen[k];
-        if (c >= 0 && c < nb) atomicOr(set + (c >> 5), 1u << (c & 31));
+      const int first32 = lane < a.K ? chosen[lane] : -1;
+      const bool guess = t < a.B;
+      int start = guess ? a.cu_q[t] : 0, end = guess ? a.cu_q[t + 1] : 0, L = guess ? a.seq_lens[t] : 0;
+      int b = t;
+      if (!(guess && start == t && end == t + 1)) {
+        b = sequence_of(a.cu_q, a.B, t, lane);
+        if (b >= 0) {
+          start = a.cu_q[b];
+          end = a.cu_q[b + 1];
+          L = a.seq_lens[b];
+        }
       }
-      __syncwarp();
+      const int seen = b < 0 ? 0 : keys_seen(t, start, end, max(0, min(L, a.max_len)), a.causal);
+      const int nb = (seen + a.block - 1) / a.block;
       int32_t* row = a.table + (int64_t)t * a.width;
       const int32_t* pages = a.block_table + (int64_t)(b < 0 ? 0 : b) * a.MB;
-      int total = 0;
-      for (int w0 = 0; w0 < nw; w0 += 32) {
-        uint32_t word = w0 + lane < nw ? set[w0 + lane] : 0u;
-        const int n = __popc(word);
-        int at = n;
+      auto put = [&](int at, int c) {
+        const int page = per_page == 1 ? c : c / per_page;
+        int pg = pages[page];
+        if (pg < 0 || pg >= a.num_pages) {               // reads page 0, as elsewhere
+          bad |= MLA_DEVERR_BLOCK_TABLE;
+          pg = 0;
+        }
+        row[at] = pg * per_page + (c - page * per_page);
+      };
+      int total = 0, top = -1;                           // blocks so far, the largest of them
+      bool ascends = true;
+      for (int k0 = 0; k0 < a.K && nb > 0; k0 += 32) {
+        const int c = k0 == 0 ? first32 : k0 + lane < a.K ? chosen[k0 + lane] : -1;
+        const bool valid = c >= 0 && c < nb;
+        const uint32_t all = __ballot_sync(0xffffffffu, valid), lower = all & ((1u << lane) - 1u);
+        const int other = __shfl_sync(0xffffffffu, c, lower != 0 ? 31 - __clz(lower) : 0);
+        ascends = __all_sync(0xffffffffu, !valid || c > (lower != 0 ? other : top));
+        if (!ascends) break;
+        if (valid) put(total + __popc(lower), c);
+        if (all != 0) top = __shfl_sync(0xffffffffu, c, 31 - __clz(all));
+        total += __popc(all);
+      }
+      if (!ascends) {
+        const int nw = (nb + 31) >> 5;
+        for (int w = lane; w < nw; w += 32) set[w] = 0u;
+        __syncwarp();
+        for (int k = lane; k < a.K; k += 32) {
+          const int c = chosen[k];
+          if (c >= 0 && c < nb) atomicOr(set + (c >> 5), 1u << (c & 31));
+        }
+        __syncwarp();
+        total = 0;
+        for (int w0 = 0; w0 < nw; w0 += 32) {
+          uint32_t word = w0 + lane < nw ? set[w0 + lane] : 0u;
+          const int n = __popc(word);
+          int at = n;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, at, o);
-          if (lane >= o) at += y;
-        }
-        const int all = __shfl_sync(0xffffffffu, at, 31);
-        at += total - n;
-        total += all;
-        while (word) {
-          const int c = (w0 + lane) * 32 + __ffs(word) - 1;
-          word &= word - 1;
-          int pg = pages[c / per_page];
-          if (pg < 0 || pg >= a.num_pages) {             // reads page 0, as elsewhere
-            bad |= MLA_DEVERR_BLOCK_TABLE;
-            pg = 0;
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, at, o);
+            if (lane >= o) at += y;
           }
-          row[at++] = pg * per_page + c % per_page;
+          const int all = __shfl_sync(0xffffffffu, at, 31);
+          at += total - n;
+          total += all;
+          for (; word != 0; word &= word - 1) put(at++, (w0 + lane) * 32 + __ffs(word) - 1);
         }
+        top = (set[(nb - 1) >> 5] >> ((nb - 1) & 31) & 1u) != 0u ? nb - 1 : -1;
+        __syncwarp();
       }
       if (lane == 0) {
-        const bool partial = nb > 0 && (set[(nb - 1) >> 5] >> ((nb - 1) & 31) & 1u) != 0u;
-        a.lens[t] = total * a.block - (partial ? nb * a.block - seen : 0);
+        const int len = total * a.block - (nb > 0 && top == nb - 1 ? nb * a.block - seen : 0);
+        if (near) st_cluster_u32(lens_of_first + 4 * t, (uint32_t)len);
+        else a.lens[t] = len;
       }
-      __syncwarp();
     }
   }
   bad = (__syncthreads_or((bad & MLA_DEVERR_CU_Q) != 0) ? MLA_DEVERR_CU_Q : 0u) |
         (__syncthreads_or((bad & MLA_DEVERR_SEQ_LEN) != 0) ? MLA_DEVERR_SEQ_LEN : 0u) |
         (__syncthreads_or((bad & MLA_DEVERR_BLOCK_TABLE) != 0) ? MLA_DEVERR_BLOCK_TABLE : 0u);
-  if (threadIdx.x == 0) a.flags[rank] = bad;
+  if (tid == 0) st_cluster_u32(map_to_rank(smem_u32(flags_s + rank), 0), bad);
+  const int first = a.cu_q[0], last = a.cu_q[a.B];
   cluster_sync();                          // tables, lengths and flags of all CTAs
   if (rank != 0) return;
-  bad = threadIdx.x < kPlanCtas ? a.flags[threadIdx.x] : 0u;
-  chunk_schedule(a.sched, TokenSeqs{a.lens, a.cu_q[0], a.cu_q[a.B]}, bad, scan_tmp);
+
+  const ChunkSchedArgs& s = a.sched;
+  bad = 0;
+#pragma unroll
+  for (int i = 0; i < kPlanCtas; ++i) bad |= flags_s[i];
+  if (tid == 0) s.hdr[0] = bad;
+  // offsets that do not ascend within the rows of q: nothing is computed
+  if ((bad & MLA_DEVERR_CU_Q) != 0 || last <= first) {
+    for (int c = tid; c <= s.workers; c += kSchedThreads) s.cta_first[c] = 0;
+    if (tid == 0) s.hdr[1] = s.hdr[2] = s.hdr[3] = s.hdr[4] = 0;
+    return;
+  }
+  const int G = (s.H + kChunkRows - 1) / kChunkRows;     // blocks of a token
+  auto len_of = [&](int t) { return near ? plan_smem[t] : a.lens[t]; };
+  // a thread takes neighbouring tokens
+  const int tokens = last - first, chunk = (tokens + kSchedThreads - 1) / kSchedThreads;
+  const int t0 = first + min(tokens, tid * chunk), t1 = min(last, t0 + chunk);
+  int64_t mine = 0;
+  for (int t = t0; t < t1; ++t) mine += tiles_of(len_of(t));
+  int64_t all;
+  const int64_t before = block_exclusive_scan(mine, scan_tmp, &all) * G;
+  const int64_t W = all * G, S = (int64_t)tokens * G;
+  // X is dropped when a worker's share would be too small for it (q <= 2 X): then every worker's range
+  // holds at least one tile
+  int X = s.setup;
+  int64_t q = (W + S * X + s.workers - 1) / s.workers;
+  if (X > 0 && q <= 2 * (int64_t)X) {
+    X = 0;
+    q = (W + s.workers - 1) / s.workers;
+  }
+  const bool small = W + S * X + q < (int64_t)1 << 31;   // (64-bit divisions are several times as long)
+  auto worker_of = [&](int64_t p) -> int64_t { return small ? (int64_t)((uint32_t)p / (uint32_t)q) : p / q; };
+  const int64_t pos0 = before + (int64_t)(t0 - first) * G * X;
+  int64_t pos = pos0, mine3 = 0;           // units << 32 | cut blocks << 16 | partial slots (as the chunk scheduler)
+  for (int t = t0; t < t1; ++t) {
+    const int n = tiles_of(len_of(t));
+    for (int g = 0; g < G; ++g) {
+      const int64_t ts = pos + X, ns = worker_of(ts + n - 1) - worker_of(ts) + 1;
+      mine3 += (ns << 32) + (ns >= 2 ? (1 << 16) + ns : 0);
+      pos = ts + n;
+    }
+  }
+  int64_t all3;
+  const int64_t before3 = block_exclusive_scan(mine3, scan_tmp, &all3);
+  const int64_t n_units = all3 >> 32, n_split = (all3 >> 16) & 0xFFFF;
+  int64_t unit = before3 >> 32, split = (before3 >> 16) & 0xFFFF, slot = before3 & 0xFFFF;
+  for (int c = tid; c <= s.workers; c += kSchedThreads) s.cta_first[c] = (int32_t)n_units;
+  __syncthreads();
+  pos = pos0;
+  for (int t = t0; t < t1; ++t) {
+    const int len = len_of(t), n = tiles_of(len);
+    for (int g = 0; g < G; ++g) {
+      const int64_t pre = pos, ts = pos + X, c0 = worker_of(ts);
+      const int ns = (int)(worker_of(ts + n - 1) - c0 + 1);
+      const int r0 = g * kChunkRows, rows = min(kChunkRows, s.H - r0);
+      const int32_t row0 = (int32_t)((int64_t)t * s.H + r0);
+      if (ns >= 2) s.split_list[split++] = make_int4(row0, rows, ns, (int)slot);
+      for (int k = 0; k < ns; ++k) {
+        const int64_t c = c0 + k;
+        const int64_t p0 = ts > c * q ? ts : c * q;
+        const int64_t p1 = ts + n < (c + 1) * q ? ts + n : (c + 1) * q;
+        const int tb = (int)(p0 - ts), te = len > 0 ? (int)(p1 - ts) : 0;
+        int4* u = reinterpret_cast<int4*>(s.units + unit);
+        u[0] = make_int4(t, row0, r0, tb | (te << 16));
+        u[1] = make_int4(ns >= 2 ? (int)slot + k : -1, len, len, rows);
+        // the worker's first unit: its range starts at this piece, or inside this block's set-up
+        if (p0 == c * q || (k == 0 && pre <= c * q)) s.cta_first[c] = (int32_t)unit;
+        ++unit;
+      }
+      if (ns >= 2) slot += ns;
+      pos = ts + n;
+    }
+  }
+  if (tid == 0) {
+    s.hdr[1] = (uint32_t)n_units;
+    s.hdr[2] = (uint32_t)n_split;
+    s.hdr[3] = (uint32_t)(q < 0xFFFFFFFFll ? q : 0xFFFFFFFFll);
+    s.hdr[4] = (uint32_t)X;
+  }
 }
 
 cudaError_t launch_sparse_plan(const SparsePlanArgs& a, cudaStream_t s) {
-  // as many warps as have room for their sets: 32 up to 48 K blocks
-  constexpr int kRoom = 200 * 1024;
-  int warps = kRoom / (a.words * 4);
+  // as many warps as have room for their sets: 32 for contexts up to 48 K blocks
+  constexpr int kRoom = 220 * 1024;
+  const int lens = a.T <= kPlanLens ? a.T : 0;
+  int warps = (kRoom - lens * 4) / (a.words * 4);
   warps = warps > 32 ? 32 : warps;
-  const size_t smem = (size_t)warps * a.words * 4;
+  const size_t smem = (size_t)lens * 4 + (size_t)warps * a.words * 4;
   cudaError_t e = cudaFuncSetAttribute(sparse_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
