@@ -38,8 +38,9 @@ struct IndexScoreArgs {
   uint32_t* err;
   int32_t B, T, H, P, MB, num_pages, max_len, block, C, causal;
   int32_t box_rows, total_rows;
-  int32_t Hp, TG, sub_tokens;      // columns of a token, tokens of a group and of a sub-group
-  int32_t q_rows, key_slots;       // rows of a query buffer, tiles of keys in shared memory
+  int32_t Hp, TG, sub_tokens;      // columns of a token, tokens of a group (a power of two) and of a sub-group
+  int32_t tg_log2;
+  int32_t q_rows, units, key_slots;   // rows of a query buffer, query buffers, tiles of keys in shared memory
   int32_t slots, chunks;           // group numbers, stretches of unit_blocks blocks
   int32_t unit_blocks;
   uint32_t block_inv;              // 2^32 / block, rounded up

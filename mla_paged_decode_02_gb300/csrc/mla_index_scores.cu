@@ -17,8 +17,8 @@
 // cu_q[b] / TG + b (TG tokens to a group), which leaves room enough for each, and a lane finds its unit's
 // by bisection. (With one token to a group that is token g itself.)
 //
-// Roles (608 threads): warp 0 resolves units, fills blocks that no token sees, and loads queries, weights,
-// keys (TMA boxes from the page table) and their scales; warps 1 and 2 issue the MMAs, each into a
+// Roles (640 threads): warp 0 resolves units, loads their queries and weights, and writes their scores;
+// warp 3 loads keys (TMA boxes from the page table) and their scales; warps 1 and 2 issue the MMAs, each into a
 // pair of accumulators of 128 columns: two sub-groups of a tile, or two tiles of one; four warpgroups take
 // an accumulator each. The maxima of
 // a unit's blocks gather in shared memory. Every wait is bounded; a stall sets the error word, and the CTA
@@ -33,7 +33,7 @@ namespace {
 
 constexpr int kISWarps = 16;                      // four warpgroups, two to a pair of accumulators
 constexpr int kISIssuers = 2;                     // issuing warps, one to a pair of accumulators
-constexpr int kISFirst = 1 + kISIssuers;          // first warp of the warpgroups
+constexpr int kISFirst = 2 + kISIssuers;          // first warp of the warpgroups
 constexpr int kISThreads = 32 * (kISFirst + kISWarps);
 constexpr int kISColumns = 128;                   // of an accumulator
 constexpr int kISTmem = 2 * kISIssuers * kISColumns;
@@ -45,12 +45,14 @@ constexpr int kISMaxSlots = 12;
 // before them, of tile t or later, had been read.
 constexpr int kISScales = 16;
 constexpr uint32_t kISFirstWaitNs = 20000;        // a wait's first, sleeping look
-constexpr int kISBest = 1024;                     // (token, block) maxima of a unit
+constexpr int kISBest = 1024;                     // (token, block) maxima of a unit, at most
+constexpr int kISMaxUnits = 4;                    // units whose queries are in shared memory
 constexpr int kISMaxTokens = 32;                  // of a group: 512 columns / 16
-constexpr int kISBases = 1024;                    // sequences whose first groups are kept in shared memory
-constexpr int kISSmem = 222 * 1024;               // dynamic
-constexpr int is_fixed_bytes(int q_rows) {
-  return 1024 + 2 * q_rows * kDIndex + kISScales * kISKeys * 4 + 2 * kISBest * 4 + 2 * q_rows * 4;
+constexpr int kISSeqs = 512;                      // sequences whose offsets and lengths are kept in shared memory
+constexpr int kISSmem = 221 * 1024;               // dynamic
+// all but the key tiles: queries, scales, maxima, weights
+constexpr int is_fixed_bytes(int units, int q_rows, int maxima) {
+  return 1024 + kISScales * kISKeys * 4 + units * (q_rows * kDIndex + maxima * 4 + q_rows * 4);
 }
 
 // an order-preserving code of a float, so that maxima can be taken as integers
@@ -163,15 +165,15 @@ __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, uint32_t
 
 // A unit as the producer announces it.
 struct UnitInfo {
-  int t0, ntok;          // its tokens; ntok = 0: no more units
-  int k0, tiles;         // first key, tiles of 128 keys
+  int t0, ntok, seq;     // its tokens and their sequence; ntok = 0: no more units
+  int k0, last, tiles;   // first key, end of the keys that a token sees, tiles of 128 keys
   int c0, blocks;        // first column of the scores, columns to be written
   int seen[kISMaxTokens];
 };
 
-// The first group of sequence b, whose tokens start at row `start`.
+// The first group of sequence b, whose tokens start at row `start` (groups are a power of two).
 __device__ __forceinline__ int first_group(const IndexScoreArgs& a, int start, int b) {
-  return a.TG == 1 ? start : start / a.TG + b;
+  return a.TG == 1 ? start : (start >> a.tg_log2) + b;
 }
 
 __device__ uint32_t g_unreported;                 // error bits of calls without an error word
@@ -184,22 +186,22 @@ template <int CPT>
 __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __grid_constant__ IndexScoreArgs a) {
   constexpr int CS = CPT == 0 ? 16 : 32;
   extern __shared__ uint8_t dsmem_raw[];
-  __shared__ __align__(8) uint64_t bar_kfull[kISMaxSlots], bar_kempty[kISMaxSlots], bar_qfull[2],
-      bar_qempty[2], bar_tfull[kISIssuers], bar_tempty[kISIssuers], bar_drain[kISIssuers], bar_unit, bar_never;
-  __shared__ UnitInfo info_s[2];
-  __shared__ int base_s[kISBases];                  // a sequence's first group
+  __shared__ __align__(8) uint64_t bar_kfull[kISMaxSlots], bar_kempty[kISMaxSlots], bar_info[kISMaxUnits],
+      bar_qfull[kISMaxUnits], bar_qempty[kISMaxUnits], bar_tfull[kISIssuers], bar_tempty[kISIssuers], bar_drain[kISIssuers], bar_never;
+  __shared__ UnitInfo info_s[kISMaxUnits];
+  __shared__ int cu_s[kISSeqs + 1], len_s[kISSeqs];
   __shared__ uint32_t tmem_base_s, abort_s;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
-  const int S = a.key_slots, q_rows = a.q_rows;
+  const int S = a.key_slots, q_rows = a.q_rows, units = a.units, maxima = a.TG * a.unit_blocks;
   const uint32_t raw = smem_u32(dsmem_raw);
-  const uint32_t sQ = (raw + 1023u) & ~1023u, sK = sQ + 2 * q_rows * kDIndex, sS = sK + S * kISSlotBytes;
+  const uint32_t sQ = (raw + 1023u) & ~1023u, sK = sQ + units * q_rows * kDIndex, sS = sK + S * kISSlotBytes;
   float* gS = reinterpret_cast<float*>(dsmem_raw + (sS - raw));       // key scales
-  int* best = reinterpret_cast<int*>(gS + kISScales * kISKeys);       // [2][kISBest]
-  float* gW = reinterpret_cast<float*>(best + 2 * kISBest);           // [2][q_rows]
+  float* gW = gS + kISScales * kISKeys;                               // [units][q_rows]
+  int* best = reinterpret_cast<int*>(gW + units * q_rows);            // [units][maxima]
   const uint32_t b_kfull = smem_u32(bar_kfull), b_kempty = smem_u32(bar_kempty);
-  const uint32_t b_qfull = smem_u32(bar_qfull), b_qempty = smem_u32(bar_qempty);
+  const uint32_t b_info = smem_u32(bar_info), b_qfull = smem_u32(bar_qfull), b_qempty = smem_u32(bar_qempty);
   const uint32_t b_tfull = smem_u32(bar_tfull), b_tempty = smem_u32(bar_tempty);
-  const uint32_t b_unit = smem_u32(&bar_unit), b_drain = smem_u32(bar_drain), b_never = smem_u32(&bar_never);
+  const uint32_t b_drain = smem_u32(bar_drain), b_never = smem_u32(&bar_never);
   uint32_t* err = a.err != nullptr ? a.err : &g_unreported;
 
   if (threadIdx.x == 0) {
@@ -207,7 +209,8 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
       mbar_init(b_kfull + 8 * i, 1);
       mbar_init(b_kempty + 8 * i, kISIssuers);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kISMaxUnits; ++i) {
+      mbar_init(b_info + 8 * i, 1);
       mbar_init(b_qfull + 8 * i, 1);
       mbar_init(b_qempty + 8 * i, kISIssuers + kISWarps);   // the MMAs, and the warps that are done with the unit
     }
@@ -216,7 +219,6 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
       mbar_init(b_tempty + 8 * i, 8);
       mbar_init(b_drain + 8 * i, 1);
     }
-    mbar_init(b_unit, kISWarps);
     mbar_init(b_never, 1);
     abort_s = 0u;
     fence_mbarrier_init();
@@ -224,10 +226,13 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
     tma_prefetch_desc(&a.tm_k);
   }
   if (warp == 1) tmem_alloc(smem_u32(&tmem_base_s), kISTmem);
-  for (int i = threadIdx.x; i < 2 * kISBest; i += kISThreads) best[i] = kLowest;
+  for (int i = threadIdx.x; i < units * maxima; i += kISThreads) best[i] = kLowest;
   griddep_wait();
   griddep_launch_dependents();
-  for (int b = threadIdx.x; b < min(a.B, kISBases); b += kISThreads) base_s[b] = first_group(a, a.cu_q[b], b);
+  for (int b = threadIdx.x; b <= min(a.B, kISSeqs); b += kISThreads) {
+    cu_s[b] = a.cu_q[b];
+    if (b < min(a.B, kISSeqs)) len_s[b] = a.seq_lens[b];
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -239,143 +244,176 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
   const int TG = a.TG, Hp = a.Hp, sub_tokens = a.sub_tokens;
 
   if (warp == 0) {
-    // ---------------------------------------------------------------------- units, queries, keys
+    // ---------------------------------------------------------------------- units and their queries
     const bool el = elect_one();
-    const int per = kISKeys / a.box_rows;               // boxes of a tile: lane i issues box i
-    uint32_t slot = 0, ph = 1, nu = 0, filled = 0;
+    uint32_t ub = 0, uph = 1, nu = 0;                   // the unit's buffer and the parity of its barriers, units so far
     bool ok = true;
     const int64_t total = (int64_t)a.slots * a.chunks;
     const bool wide_weights = (reinterpret_cast<uintptr_t>(a.w) & 15) == 0;
+    // waits until a buffer's last unit is done, and writes its scores
+    auto finish_unit = [&](uint32_t buffer, uint32_t parity, bool used) -> bool {
+      if (!wait(b_qempty + 8 * buffer, parity)) return false;
+      if (!used) return true;
+      const UnitInfo& I = info_s[buffer];
+      int* from = best + buffer * maxima;
+      for (int i = 0; i < I.ntok; ++i)
+        for (int c = lane; c < a.unit_blocks; c += 32) {
+          if (c < I.blocks) a.out[(int64_t)(I.t0 + i) * a.C + I.c0 + c] = from_ordered(from[i * a.unit_blocks + c]);
+          from[i * a.unit_blocks + c] = kLowest;
+        }
+      __syncwarp();
+      return true;
+    };
+    auto cu = [&](int b) { return b <= kISSeqs ? cu_s[b] : a.cu_q[b]; };
     for (int64_t base = blockIdx.x; base < total && ok; base += 32 * (int64_t)gridDim.x) {
       // 32 units at a time, one to a lane
       const int64_t u = base + (int64_t)lane * gridDim.x;
-      int b = 0, t0 = 0, ntok = 0, k0 = 0, c0 = 0, last = 0, start = 0, end = 0, L = 0;
+      int b = 0, t0 = 0, ntok = 0, k0 = 0, last = 0, start = 0, end = 0, L = 0;
       if (u < total) {
         const int chunk = (int)(u / a.slots), g = (int)(u - (int64_t)chunk * a.slots);
-        int lo = 0, hi = a.B;                           // the last b with cu_q[b] / TG + b <= g
+        int lo = 0, hi = a.B;                           // the last b whose first group is at most g
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
-          if ((mid < kISBases ? base_s[mid] : first_group(a, a.cu_q[mid], mid)) <= g) lo = mid;
+          if (first_group(a, cu(mid), mid) <= g) lo = mid;
           else hi = mid;
         }
         b = lo;
-        start = max(0, a.cu_q[b]);
-        end = min(a.T, a.cu_q[b + 1]);
+        start = max(0, cu(b));
+        end = min(a.T, cu(b + 1));
         const int skip = g - first_group(a, start, b);
         const int64_t first = (int64_t)start + (int64_t)skip * TG;
         if (skip >= 0 && first < end) {
           t0 = (int)first;
           ntok = min(TG, end - t0);
-          L = max(0, min(a.seq_lens[b], a.max_len));
-          c0 = chunk * a.unit_blocks;
-          k0 = c0 * a.block;
+          L = max(0, min(b < kISSeqs ? len_s[b] : a.seq_lens[b], a.max_len));
+          k0 = chunk * a.unit_blocks * a.block;
           last = min(keys_seen(t0 + ntok - 1, start, end, L, a.causal), k0 + a.unit_blocks * a.block);
         }
       }
-      const uint32_t any = __ballot_sync(0xffffffffu, ntok > 0);
-      for (uint32_t m = any; m != 0 && ok; m &= m - 1) {
+      for (uint32_t m = __ballot_sync(0xffffffffu, ntok > 0); m != 0 && ok; m &= m - 1) {
         const int src = __ffs(m) - 1;
-        const int ub = __shfl_sync(0xffffffffu, b, src), ut0 = __shfl_sync(0xffffffffu, t0, src);
+        const int us = __shfl_sync(0xffffffffu, b, src), ut0 = __shfl_sync(0xffffffffu, t0, src);
         const int un = __shfl_sync(0xffffffffu, ntok, src), uk0 = __shfl_sync(0xffffffffu, k0, src);
-        const int uc0 = __shfl_sync(0xffffffffu, c0, src), ulast = __shfl_sync(0xffffffffu, last, src);
-        const int ustart = __shfl_sync(0xffffffffu, start, src), uend = __shfl_sync(0xffffffffu, end, src);
-        const int uL = __shfl_sync(0xffffffffu, L, src);
-        const int blocks = min(a.unit_blocks, a.C - uc0);
+        const int ulast = __shfl_sync(0xffffffffu, last, src);
+        const int c0 = (int)((base + (int64_t)src * gridDim.x) / a.slots) * a.unit_blocks, blocks = min(a.unit_blocks, a.C - c0);
         if (ulast <= uk0) {                             // no token sees these blocks
           for (int i = 0; i < un; ++i)
-            for (int c = lane; c < blocks; c += 32) a.out[(int64_t)(ut0 + i) * a.C + uc0 + c] = -INFINITY;
+            for (int c = lane; c < blocks; c += 32) a.out[(int64_t)(ut0 + i) * a.C + c0 + c] = -INFINITY;
           continue;
         }
-        const int tiles = (ulast - uk0 + kISKeys - 1) / kISKeys;
-        // the first rows of the unit's boxes, 32 at a time (one to a lane), 32 ahead
-        const int32_t* pages = a.block_table + (int64_t)ub * a.MB;
-        auto row_of = [&](int box) -> int {
-          const int tok = uk0 + box * a.box_rows;
-          if (tok >= ulast) return -1;
-          const int page = tok / a.P, in = tok - page * a.P;
-          int pg = __ldg(pages + page);
-          if (pg < 0 || pg >= a.num_pages) {
-            atomicOr(err, MLA_DEVERR_BLOCK_TABLE);
-            pg = 0;
-          }
-          return pg * a.P + in;
-        };
-        int rows = row_of(lane), ahead = row_of(lane + 32);
-        const uint32_t qb = nu & 1;
-        ok = wait(b_qempty + 8 * qb, ((nu >> 1) & 1) ^ 1);
+        const int ustart = __shfl_sync(0xffffffffu, start, src), uend = __shfl_sync(0xffffffffu, end, src);
+        const int uL = __shfl_sync(0xffffffffu, L, src);
+        ok = finish_unit(ub, uph, nu >= (uint32_t)units);
         if (!ok) break;
-        UnitInfo& I = info_s[qb];
+        UnitInfo& I = info_s[ub];
         if (lane == 0) {
           I.t0 = ut0;
           I.ntok = un;
           I.k0 = uk0;
-          I.tiles = tiles;
-          I.c0 = uc0;
+          I.last = ulast;
+          I.tiles = (ulast - uk0 + kISKeys - 1) / kISKeys;
+          I.c0 = c0;
           I.blocks = blocks;
+          I.seq = us;
         }
         if (lane < un) I.seen[lane] = keys_seen(ut0 + lane, ustart, uend, uL, a.causal);
         // weights: one copy where a token's fill its columns, else by loads
         const uint32_t wbytes = a.H == Hp && wide_weights ? (uint32_t)(un * Hp) * 4 : 0u;
         if (wbytes == 0)
-          for (int i = lane; i < un * a.H; i += 32) gW[qb * q_rows + (i / a.H) * Hp + i % a.H] = a.w[(int64_t)ut0 * a.H + i];
+          for (int i = lane; i < un * a.H; i += 32) gW[ub * q_rows + (i / a.H) * Hp + i % a.H] = a.w[(int64_t)ut0 * a.H + i];
         __syncwarp();
         const int qboxes = un * (Hp / 16);
         if (el) {
-          mbar_arrive_expect_tx(b_qfull + 8 * qb, (uint32_t)qboxes * 16 * kDIndex + wbytes);
-          if (wbytes) bulk_load(smem_u32(gW + qb * q_rows), a.w + (int64_t)ut0 * a.H, wbytes, b_qfull + 8 * qb);
+          mbar_arrive(b_info + 8 * ub);
+          mbar_arrive_expect_tx(b_qfull + 8 * ub, (uint32_t)qboxes * 16 * kDIndex + wbytes);
+          if (wbytes) bulk_load(smem_u32(gW + ub * q_rows), a.w + (int64_t)ut0 * a.H, wbytes, b_qfull + 8 * ub);
         }
         __syncwarp();
         for (int i = lane; i < qboxes; i += 32)
-          tma_load_2d(sQ + qb * q_rows * kDIndex + i * 16 * kDIndex, &a.tm_q, b_qfull + 8 * qb, 0,
+          tma_load_2d(sQ + ub * q_rows * kDIndex + i * 16 * kDIndex, &a.tm_q, b_qfull + 8 * ub, 0,
                       (ut0 + i / (Hp / 16)) * a.H + (i % (Hp / 16)) * 16);
         ++nu;
-        for (int tile = 0; tile < tiles; ++tile) {
-          const int at = tile * per & 31;                 // per divides 32
-          if (tile > 0 && at == 0) {
-            rows = ahead;
-            ahead = row_of((tile * per & ~31) + 32 + lane);
-          }
-          const int row = __shfl_sync(0xffffffffu, rows, at + (lane & (per - 1)));
-          const int valid = __popc(__ballot_sync(0xffffffffu, lane < per && row >= 0));
-          ok = wait(b_kempty + 8 * slot, ph);
-          if (!ok) break;
-          const uint32_t bar = b_kfull + 8 * slot, sc = filled % kISScales;
-          if (el) mbar_arrive_expect_tx(bar, kISSlotBytes + (uint32_t)(valid * a.box_rows * 4));
-          __syncwarp();
-          if (lane < per) {
-            // a box past the keys starts at the end of the pool and reads zeros
-            tma_load_2d(sK + slot * kISSlotBytes + lane * a.box_rows * kDIndex, &a.tm_k, bar, 0,
-                        row >= 0 ? row : a.total_rows);
-            if (row >= 0)
-              bulk_load(sS + (sc * kISKeys + lane * a.box_rows) * 4, a.scale + row, (uint32_t)a.box_rows * 4, bar);
-          }
-          ++filled;
-          if (++slot == (uint32_t)S) { slot = 0; ph ^= 1; }
-        }
+        if (++ub == (uint32_t)units) { ub = 0; uph ^= 1; }
       }
     }
-    // the end of the units
+    // the end of the units: the others leave, and the last units' scores are written
+    ok = ok && finish_unit(ub, uph, nu >= (uint32_t)units);
     if (ok) {
-      const uint32_t qb = nu & 1;
-      ok = wait(b_qempty + 8 * qb, ((nu >> 1) & 1) ^ 1);
-      if (ok) {
-        if (lane == 0) info_s[qb].ntok = 0;
-        __syncwarp();
-        if (el) mbar_arrive(b_qfull + 8 * qb);
-      }
-    }
-    if (!ok) {
-      // copies in flight land before the CTA leaves: the last fill of each slot
-      volatile uint32_t none = 0u;
-      auto land = [&](uint32_t bar, uint32_t fill, uint32_t of) {
-        mbar_wait(bar + 8 * (fill % of), (fill / of) & 1, &none, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns);
-      };
-      if (lane == 0) {
-        for (uint32_t f = filled > (uint32_t)S ? filled - S : 0; f < filled; ++f) land(b_kfull, f, S);
-        for (uint32_t k = nu >= 2 ? nu - 2 : 0; k < nu; ++k) land(b_qfull, k, 2);
-      }
+      if (lane == 0) info_s[ub].ntok = 0;
       __syncwarp();
+      if (el) {
+        mbar_arrive(b_info + 8 * ub);
+        mbar_arrive(b_qfull + 8 * ub);
+      }
+      for (int i = 1; i < units && ok; ++i) {
+        if (++ub == (uint32_t)units) { ub = 0; uph ^= 1; }
+        ok = finish_unit(ub, uph, nu + i >= (uint32_t)units);
+      }
     }
+    if (!ok && lane == 0) {
+      // copies in flight land before the CTA leaves: the last fill of each buffer
+      volatile uint32_t none = 0u;
+      for (uint32_t k = nu > (uint32_t)units ? nu - units : 0; k < nu; ++k)
+        mbar_wait(b_qfull + 8 * (k % units), (k / units) & 1, &none, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ---------------------------------------------------------------------------- keys and scales
+    const bool el = elect_one();
+    const int per = kISKeys / a.box_rows;               // boxes of a tile: lane i issues box i
+    uint32_t ub = 0, uph = 0, slot = 0, ph = 1, filled = 0;
+    bool ok = true;
+    while (ok) {
+      ok = wait(b_info + 8 * ub, uph);
+      if (!ok) break;
+      const UnitInfo& I = info_s[ub];
+      const int ntok = I.ntok, tiles = I.tiles, k0 = I.k0, last = I.last;
+      if (ntok == 0) break;
+      // the first rows of the unit's boxes, 32 at a time (one to a lane), 32 ahead
+      const int32_t* pages = a.block_table + (int64_t)I.seq * a.MB;
+      auto row_of = [&](int box) -> int {
+        const int tok = k0 + box * a.box_rows;
+        if (tok >= last) return -1;
+        const int page = tok / a.P, in = tok - page * a.P;
+        int pg = __ldg(pages + page);
+        if (pg < 0 || pg >= a.num_pages) {
+          atomicOr(err, MLA_DEVERR_BLOCK_TABLE);
+          pg = 0;
+        }
+        return pg * a.P + in;
+      };
+      int rows = row_of(lane), ahead = tiles * per > 32 ? row_of(lane + 32) : -1;
+      for (int tile = 0; tile < tiles; ++tile) {
+        const int at = tile * per & 31;                 // per divides 32
+        if (tile > 0 && at == 0) {
+          rows = ahead;
+          ahead = row_of((tile * per & ~31) + 32 + lane);
+        }
+        const int row = __shfl_sync(0xffffffffu, rows, at + (lane & (per - 1)));
+        const int valid = __popc(__ballot_sync(0xffffffffu, lane < per && row >= 0));
+        ok = wait(b_kempty + 8 * slot, ph);
+        if (!ok) break;
+        const uint32_t bar = b_kfull + 8 * slot, sc = filled % kISScales;
+        if (el) mbar_arrive_expect_tx(bar, kISSlotBytes + (uint32_t)(valid * a.box_rows * 4));
+        __syncwarp();
+        if (lane < per) {
+          // a box past the keys starts at the end of the pool and reads zeros
+          tma_load_2d(sK + slot * kISSlotBytes + lane * a.box_rows * kDIndex, &a.tm_k, bar, 0,
+                      row >= 0 ? row : a.total_rows);
+          if (row >= 0)
+            bulk_load(sS + (sc * kISKeys + lane * a.box_rows) * 4, a.scale + row, (uint32_t)a.box_rows * 4, bar);
+        }
+        ++filled;
+        if (++slot == (uint32_t)S) { slot = 0; ph ^= 1; }
+      }
+      if (++ub == (uint32_t)units) { ub = 0; uph ^= 1; }
+    }
+    if (!ok && lane == 0) {
+      volatile uint32_t none = 0u;
+      for (uint32_t f = filled > (uint32_t)S ? filled - S : 0; f < filled; ++f)
+        mbar_wait(b_kfull + 8 * (f % S), (f / S) & 1, &none, err, MLA_DEVERR_TIMEOUT, a.wait_limit_ns);
+    }
+    __syncwarp();
   } else if (warp < kISFirst) {
     // ---------------------------------------------------------------------------------- MMAs
     const bool el = elect_one();
@@ -383,9 +421,8 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
     const uint32_t acc = tmem + me * 2 * kISColumns, b_full = b_tfull + 8 * me, b_free = b_tempty + 8 * me;
     uint32_t slot = 0, ph = 0, n = 0, mine = 0;         // n: products so far, of both; mine: of this warp
     bool ok = true;
-    for (uint32_t nu = 0; ok; ++nu) {
-      const uint32_t qb = nu & 1;
-      ok = wait(b_qfull + 8 * qb, (nu >> 1) & 1);
+    for (uint32_t qb = 0, qph = 0; ok; qb + 1 == (uint32_t)units ? (qb = 0, qph ^= 1) : ++qb) {
+      ok = wait(b_qfull + 8 * qb, qph);
       if (!ok) break;
       // (the same in every lane, which the compiler can use for the descriptors)
       const int ntok = __shfl_sync(0xffffffffu, info_s[qb].ntok, 0), tiles = __shfl_sync(0xffffffffu, info_s[qb].tiles, 0);
@@ -455,14 +492,13 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
     bool ok = !(a.test_stall && !wait(b_never, 0));
     const bool whole = a.block % 32 == 0;               // a warp's keys lie in one block
     const int H = a.H;
-    for (uint32_t nu = 0; ok; ++nu) {
-      const uint32_t qb = nu & 1;
-      ok = wait(b_qfull + 8 * qb, (nu >> 1) & 1);
+    for (uint32_t qb = 0, qph = 0; ok; qb + 1 == (uint32_t)units ? (qb = 0, qph ^= 1) : ++qb) {
+      ok = wait(b_qfull + 8 * qb, qph);
       if (!ok) break;
       const UnitInfo& I = info_s[qb];
       const int ntok = I.ntok, tiles = I.tiles;
       if (ntok == 0) break;
-      int* mine = best + qb * kISBest;
+      int* mine = best + qb * maxima;
       const bool one = ntok <= sub_tokens;
       const int turns = ntok > 2 * sub_tokens ? 2 : 1;  // products of a tile
       const int products = one ? (tiles + 1) >> 1 : tiles * turns;
@@ -564,16 +600,6 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
       n += (uint32_t)products;
       nt += (uint32_t)tiles;
       __syncwarp();
-      if (lane == 0) mbar_arrive(b_unit);               // all warps' maxima are in
-      ok = wait(b_unit, nu & 1);
-      if (!ok) break;
-      const int all = ntok * a.unit_blocks;
-      for (int x = et; x < all; x += 32 * kISWarps) {
-        const int i = x / a.unit_blocks, c = x - i * a.unit_blocks;
-        if (c < I.blocks) a.out[(int64_t)(I.t0 + i) * a.C + I.c0 + c] = from_ordered(mine[x]);
-        mine[x] = kLowest;
-      }
-      __syncwarp();
       if (lane == 0) mbar_arrive(b_qempty + 8 * qb);
     }
   }
@@ -590,12 +616,10 @@ cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s) {
   // sub-groups share each key tile
   const bool many = a.T >= 2 * (int64_t)a.B;
   a.TG = many ? 2 * kISIssuers * a.sub_tokens : 1;
+  a.tg_log2 = 31 - __builtin_clz((unsigned)a.TG);      // 128 / Hp rounded down is a power of two
   a.q_rows = a.TG * a.Hp;
   a.slots = a.TG == 1 ? a.T : a.T / a.TG + a.B;
-  a.key_slots = (kISSmem - is_fixed_bytes(a.q_rows)) / kISSlotBytes;
-  if (a.key_slots > kISMaxSlots) a.key_slots = kISMaxSlots;
-  const int smem = is_fixed_bytes(a.q_rows) + a.key_slots * kISSlotBytes;
-  // a unit: whole blocks and whole tiles, about eight units to a CTA, 512 to 8192 keys
+  // a unit: whole blocks and whole tiles, 512 to 8192 keys, about 24 units to a CTA (8 of a decode step)
   int lcm = a.block;
   while (lcm % kISKeys != 0) lcm += a.block;
   const int64_t groups = (a.T + a.TG - 1) / a.TG;
@@ -609,6 +633,11 @@ cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s) {
   a.unit_blocks = (int)(m * (lcm / a.block));
   a.chunks = (a.C + a.unit_blocks - 1) / a.unit_blocks;
   a.block_inv = (uint32_t)((((uint64_t)1 << 32) + a.block - 1) / a.block);   // keys of a unit x block < 2^32
+  a.units = many ? 2 : kISMaxUnits;
+  const int fixed = is_fixed_bytes(a.units, a.q_rows, a.TG * a.unit_blocks);
+  a.key_slots = (kISSmem - fixed) / kISSlotBytes;
+  if (a.key_slots > kISMaxSlots) a.key_slots = kISMaxSlots;
+  const int smem = fixed + a.key_slots * kISSlotBytes;
   const int64_t total = (int64_t)a.slots * a.chunks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(total < num_sms ? total : num_sms));
