@@ -560,38 +560,26 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
             finish(i, sum8(s) + rest);
           }
           release();
-        } else if (toks * CPT == 4) {
-          // two buffers: a chunk is on its way while the one before it is summed
-          float va[CS], vb[CS];
-          load_heads<CS>(acc, va);
-#pragma unroll
-          for (int c = 0; c < 4; c += 2) {
-            tmem_wait_ld();
-            load_heads<CS>(acc + (c + 1) * CS, vb);
-            if (CPT < 4 || c == 0) add_heads<CS, true>(va, w + c * CS, s);
-            else add_heads<CS, false>(va, w + c * CS, s);
-            if (CPT == 1) finish(c, sum8(s));
-            tmem_wait_ld();
-            if (c == 0) load_heads<CS>(acc + 2 * CS, va);
-            else release();
-            if (CPT == 1) add_heads<CS, true>(vb, w + (c + 1) * CS, s);
-            else add_heads<CS, false>(vb, w + (c + 1) * CS, s);
-            if (CPT == 1) finish(c + 1, sum8(s));
-            if (CPT == 2) finish(c >> 1, sum8(s));
-            if (CPT == 4 && c == 2) finish(0, sum8(s));
-          }
         } else {
-          float v[CS];
-          for (int i = 0; i < toks; ++i) {
+          // (the warps of a scheduler cover each other's loads: a second buffer changes nothing)
+          auto token = [&](int i) {
+            float v[CS];
 #pragma unroll
             for (int c = 0; c < CPT; ++c) {
-              load_heads<CS>(acc + (i * CPT + c) * CS, v);
+              const int at = (i * CPT + c) * CS;
+              load_heads<CS>(acc + at, v);
               tmem_wait_ld();
-              if (c == 0) add_heads<CS, true>(v, w + (i * CPT + c) * CS, s);
-              else add_heads<CS, false>(v, w + (i * CPT + c) * CS, s);
+              if (c + 1 == CPT && i + 1 == toks) release();
+              if (c == 0) add_heads<CS, true>(v, w + at, s);
+              else add_heads<CS, false>(v, w + at, s);
             }
-            if (i + 1 == toks) release();
             finish(i, sum8(s));
+          };
+          if (toks * CPT == 4) {
+#pragma unroll
+            for (int i = 0; i < 4 / (CPT > 0 ? CPT : 1); ++i) token(i);
+          } else {
+            for (int i = 0; i < toks; ++i) token(i);
           }
         }
         if (whole && lane < toks && keep > -INFINITY) atomicMax(to + lane * a.unit_blocks, ordered(keep));
