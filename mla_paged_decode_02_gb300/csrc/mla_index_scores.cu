@@ -113,6 +113,14 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
                :: "r"(dst), "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar) : "memory");
 }
+// 16 bytes from global to this CTA's shared memory, asynchronously; and this thread's arrival on `bar` once
+// its copies so far have landed (counted as pending from the start)
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared::cta.global [%0], [%1], 16;" :: "r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
+}
+__device__ __forceinline__ void arrive_after_copies(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
+}
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   uint32_t r[32];
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
@@ -194,7 +202,8 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int S = a.key_slots, q_rows = a.q_rows, units = a.units, maxima = a.TG * a.unit_blocks;
   const uint32_t raw = smem_u32(dsmem_raw);
-  const uint32_t sQ = (raw + 1023u) & ~1023u, sK = sQ + units * q_rows * kDIndex, sS = sK + S * kISSlotBytes;
+  const uint32_t sQ = (raw + 1023u) & ~1023u, sK = sQ + units * q_rows * kDIndex;
+  const uint32_t sS = sK + S * kISSlotBytes;
   float* gS = reinterpret_cast<float*>(dsmem_raw + (sS - raw));       // key scales
   float* gW = gS + kISScales * kISKeys;                               // [units][q_rows]
   int* best = reinterpret_cast<int*>(gW + units * q_rows);            // [units][maxima]
@@ -206,7 +215,7 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kISMaxSlots; ++i) {
-      mbar_init(b_kfull + 8 * i, 1);
+      mbar_init(b_kfull + 8 * i, 1 + 32);           // the keys, and the loading warp's scales
       mbar_init(b_kempty + 8 * i, kISIssuers);
     }
     for (int i = 0; i < kISMaxUnits; ++i) {
@@ -383,6 +392,8 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
         return pg * a.P + in;
       };
       int rows = row_of(lane), ahead = tiles * per > 32 ? row_of(lane + 32) : -1;
+      // a lane brings four scales of each tile
+      const int my_box = lane * 4 / a.box_rows, my_row = lane * 4 - my_box * a.box_rows;
       for (int tile = 0; tile < tiles; ++tile) {
         const int at = tile * per & 31;                 // per divides 32
         if (tile > 0 && at == 0) {
@@ -390,19 +401,17 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
           ahead = row_of((tile * per & ~31) + 32 + lane);
         }
         const int row = __shfl_sync(0xffffffffu, rows, at + (lane & (per - 1)));
-        const int valid = __popc(__ballot_sync(0xffffffffu, lane < per && row >= 0));
+        const int srow = __shfl_sync(0xffffffffu, rows, at + my_box);
         ok = wait(b_kempty + 8 * slot, ph);
         if (!ok) break;
-        const uint32_t bar = b_kfull + 8 * slot, sc = filled % kISScales;
-        if (el) mbar_arrive_expect_tx(bar, kISSlotBytes + (uint32_t)(valid * a.box_rows * 4));
+        const uint32_t bar = b_kfull + 8 * slot;
+        if (el) mbar_arrive_expect_tx(bar, kISSlotBytes);
         __syncwarp();
-        if (lane < per) {
-          // a box past the keys starts at the end of the pool and reads zeros
-          tma_load_2d(sK + slot * kISSlotBytes + lane * a.box_rows * kDIndex, &a.tm_k, bar, 0,
-                      row >= 0 ? row : a.total_rows);
-          if (row >= 0)
-            bulk_load(sS + (sc * kISKeys + lane * a.box_rows) * 4, a.scale + row, (uint32_t)a.box_rows * 4, bar);
-        }
+        // a box past the keys starts at the end of the pool and reads zeros
+        if (lane < per)
+          tma_load_2d(sK + slot * kISSlotBytes + lane * a.box_rows * kDIndex, &a.tm_k, bar, 0, row >= 0 ? row : a.total_rows);
+        if (srow >= 0) copy16(sS + ((filled % kISScales) * kISKeys + lane * 4) * 4, a.scale + srow + my_row);
+        arrive_after_copies(bar);
         ++filled;
         if (++slot == (uint32_t)S) { slot = 0; ph ^= 1; }
       }
