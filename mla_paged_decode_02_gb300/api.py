@@ -323,12 +323,16 @@ def _addresses(stream, *tensors):
     dereferences these there, so all of them have to live on it. (The checks of the calls below
     cost as much as a small kernel: they look at each property once.)"""
     dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
+    at = []
     for t in tensors:
-        if t is not None and t.get_device() != dev:            # -1: not on a GPU
+        if t is None:
+            at.append(None)
+            continue
+        if t.get_device() != dev:            # -1: not on a GPU
             raise ValueError("every tensor must be on the current device" if t.is_cuda else
                              "every tensor must be on the GPU")
-    handle = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    return handle, [None if t is None else t.data_ptr() for t in tensors]
+        at.append(t.data_ptr())
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream, at
 
 
 def _allocated(stream, shape, dtype, device) -> torch.Tensor:
@@ -508,44 +512,37 @@ def merge_states(out_a: torch.Tensor, lse_a: torch.Tensor, out_b: torch.Tensor, 
     return out, lse
 
 
-_I32_MAX = 0x7FFFFFFF
+_I32_MAX = 0x7FFFFFFF        # a structure's or an argument's 32-bit field would keep the low bits of a larger number
 _CODES = (torch.float8_e4m3fn, torch.uint8)
-
-
-def _int32_max(**sizes) -> None:
-    """A structure's or an argument's 32-bit field would keep the low bits of a larger number."""
-    for name, value in sizes.items():
-        if not -_I32_MAX <= value <= _I32_MAX:
-            raise ValueError(f"{name} is out of range")
 
 
 def _ragged(seq_lens, cu_q_lens, block_table=None) -> int:
     """Checks the offsets, lengths and block table of a ragged batch; its number of sequences."""
-    for name, t in (("seq_lens", seq_lens), ("cu_q_lens", cu_q_lens), ("block_table", block_table)):
-        if t is not None and (t.dtype is not torch.int32 or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous int32 tensor")
-    B = seq_lens.numel()
-    if seq_lens.dim() != 1 or cu_q_lens.shape != (B + 1,):
+    i32, shape = torch.int32, seq_lens.shape
+    if len(shape) != 1 or cu_q_lens.shape != (shape[0] + 1,):
         raise ValueError("seq_lens must be [B] and cu_q_lens [B + 1]")
-    if block_table is not None and (block_table.dim() != 2 or block_table.shape[0] != B):
-        raise ValueError("block_table must be [B, MB]")
-    return B
+    if seq_lens.dtype is not i32 or cu_q_lens.dtype is not i32 or not seq_lens.is_contiguous() or not cu_q_lens.is_contiguous():
+        raise ValueError("seq_lens and cu_q_lens must be contiguous int32 tensors")
+    if block_table is not None:
+        table = block_table.shape
+        if len(table) != 2 or table[0] != shape[0] or block_table.dtype is not i32 or not block_table.is_contiguous():
+            raise ValueError("block_table must be a contiguous int32 [B, MB] tensor")
+    return shape[0]
 
 
 def _error_word(device_error) -> None:
-    if device_error is not None and (device_error.dtype not in (torch.int32, torch.uint32) or device_error.numel() < 1):
+    if device_error.dtype not in (torch.int32, torch.uint32) or device_error.numel() < 1:
         raise ValueError("device_error must be a 32-bit integer tensor")
 
 
 def _index_pool(index_cache, index_scale):
     """(pages, rows of a page) of an index cache and its scales."""
-    if index_cache.dtype not in _CODES or index_cache.dim() != 3 or index_cache.shape[2] != D_INDEX or \
-            not index_cache.is_contiguous():
+    shape = index_cache.shape
+    if len(shape) != 3 or shape[2] != D_INDEX or index_cache.dtype not in _CODES or not index_cache.is_contiguous():
         raise ValueError("index_cache must be a contiguous uint8 or float8_e4m3fn [Np, P, 128] tensor")
-    Np, P, _ = index_cache.shape
-    if index_scale.dtype is not torch.float32 or index_scale.shape != (Np, P) or not index_scale.is_contiguous():
+    if index_scale.dtype is not torch.float32 or index_scale.shape != shape[:2] or not index_scale.is_contiguous():
         raise ValueError("index_scale must be a contiguous float32 [Np, P] tensor")
-    return Np, P
+    return shape[0], shape[1]
 
 
 def index_cache_write(keys: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor, slot_mapping: torch.Tensor,
@@ -561,21 +558,22 @@ def index_cache_write(keys: torch.Tensor, positions: torch.Tensor, cos_sin: torc
     strided views of projections. Negative positions mark padding tokens."""
     n = keys.shape[0]
     stride = _rows_of(keys, n, D_INDEX, "keys")
-    i64 = torch.int64
-    if positions.dtype is not i64 or positions.shape != (n,) or not positions.is_contiguous() or \
-            slot_mapping.dtype is not i64 or slot_mapping.shape != (n,) or not slot_mapping.is_contiguous():
+    i64, f32, rows = torch.int64, torch.float32, (n,)
+    if positions.dtype is not i64 or positions.shape != rows or not positions.is_contiguous() or \
+            slot_mapping.dtype is not i64 or slot_mapping.shape != rows or not slot_mapping.is_contiguous():
         raise ValueError("positions and slot_mapping must be contiguous int64 [N] tensors")
-    if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or cos_sin.shape[1] != 64 or not cos_sin.is_contiguous():
+    table = cos_sin.shape
+    if len(table) != 2 or table[1] != 64 or cos_sin.dtype is not f32 or not cos_sin.is_contiguous():
         raise ValueError("cos_sin must be a contiguous float32 [max_pos, 64] tensor")
     Np, P = _index_pool(index_cache, index_scale)
-    given = [t is not None for t in (queries, weights, q_index, q_weights)]
-    if any(given) != all(given):
-        raise ValueError("queries, weights, q_index and q_weights are given together or not at all")
     H, qt, qh = 0, 0, 0
     if queries is not None:
-        if queries.dtype is not torch.bfloat16 or queries.dim() != 3 or queries.shape[0] != n or queries.shape[2] != D_INDEX:
+        if weights is None or q_index is None or q_weights is None:
+            raise ValueError("queries, weights, q_index and q_weights are given together or not at all")
+        shape = queries.shape
+        if len(shape) != 3 or shape[0] != n or shape[2] != D_INDEX or queries.dtype is not torch.bfloat16:
             raise ValueError("queries must be a bf16 [N, H, 128] tensor with contiguous last dimension")
-        H = queries.shape[1]
+        H = shape[1]
         qt, qh, inner = queries.stride()
         if H < 1 or (inner != 1 and n > 0):
             raise ValueError("queries must be a bf16 [N, H, 128] tensor with contiguous last dimension")
@@ -585,17 +583,21 @@ def index_cache_write(keys: torch.Tensor, positions: torch.Tensor, cos_sin: torc
             qh = 0
         if qt % 8 != 0 or qh % 8 != 0:
             raise ValueError("the tokens and heads of queries must be apart by a multiple of 8 elements")
-        if q_index.dtype not in _CODES or q_index.shape != (n, H, D_INDEX) or not q_index.is_contiguous():
+        if q_index.dtype not in _CODES or q_index.shape != shape or not q_index.is_contiguous():
             raise ValueError("q_index must be a contiguous uint8 or float8_e4m3fn [N, H, 128] tensor")
-        for t in (weights, q_weights):
-            if t.dtype is not torch.float32 or t.shape != (n, H) or not t.is_contiguous():
-                raise ValueError("weights and q_weights must be contiguous float32 [N, H] tensors")
-    _error_word(device_error)
+        heads = shape[:2]
+        if weights.dtype is not f32 or weights.shape != heads or not weights.is_contiguous() or \
+                q_weights.dtype is not f32 or q_weights.shape != heads or not q_weights.is_contiguous():
+            raise ValueError("weights and q_weights must be contiguous float32 [N, H] tensors")
+    elif weights is not None or q_index is not None or q_weights is not None:
+        raise ValueError("queries, weights, q_index and q_weights are given together or not at all")
+    if device_error is not None:
+        _error_word(device_error)
     if n == 0:
-        queries = weights = q_index = q_weights = None
-    handle, at = _addresses(stream, keys if n > 0 else None, positions, cos_sin, slot_mapping, index_cache, index_scale,
-                            queries, weights, q_index, q_weights, device_error)
-    st = lib().mla_index_cache_write(at[0], stride, at[1], at[2], cos_sin.shape[0], 1 if interleaved else 0, at[3], n,
+        keys = queries = weights = q_index = q_weights = None
+    handle, at = _addresses(stream, keys, positions, cos_sin, slot_mapping, index_cache, index_scale, queries, weights,
+                            q_index, q_weights, device_error)
+    st = lib().mla_index_cache_write(at[0], stride, at[1], at[2], table[0], 1 if interleaved else 0, at[3], n,
                                      at[4], at[5], Np, P, at[6], qt, qh, at[7], H, at[8], at[9], at[10], handle)
     if st != MLA_OK:
         raise MLAError(st, "mla_index_cache_write")
@@ -611,17 +613,18 @@ def index_scores(q_index: torch.Tensor, q_weights: torch.Tensor, index_cache: to
     q_index [T, H, 128] and q_weights [T, H] as index_cache_write() leaves them; the ragged batch as
     chunk_attention(). Rows that belong to no sequence are left as they are in out (uninitialised when
     it is allocated here)."""
-    if q_index.dtype not in _CODES or q_index.dim() != 3 or q_index.shape[2] != D_INDEX or not q_index.is_contiguous():
+    shape = q_index.shape
+    if len(shape) != 3 or shape[2] != D_INDEX or q_index.dtype not in _CODES or not q_index.is_contiguous():
         raise ValueError("q_index must be a contiguous uint8 or float8_e4m3fn [T, H, 128] tensor")
-    T, H, _ = q_index.shape
-    if q_weights.dtype is not torch.float32 or q_weights.shape != (T, H) or not q_weights.is_contiguous():
+    T, H, _ = shape
+    if q_weights.dtype is not torch.float32 or q_weights.shape != shape[:2] or not q_weights.is_contiguous():
         raise ValueError("q_weights must be a contiguous float32 [T, H] tensor")
     Np, P = _index_pool(index_cache, index_scale)
     B = _ragged(seq_lens, cu_q_lens, block_table)
-    _error_word(device_error)
-    if max_seq_len < 1 or block_size < 1:
-        raise ValueError("max_seq_len and block_size must be positive")
-    _int32_max(max_seq_len=max_seq_len, block_size=block_size)
+    if device_error is not None:
+        _error_word(device_error)
+    if not 0 < max_seq_len <= _I32_MAX or not 0 < block_size <= _I32_MAX:
+        raise ValueError("max_seq_len and block_size must be positive and fit 32 bits")
     shape = (T, (max_seq_len + block_size - 1) // block_size)
     if out is not None and (out.dtype is not torch.float32 or out.shape != shape or not out.is_contiguous()):
         raise ValueError("out must be a contiguous float32 [T, ceil(max_seq_len / block_size)] tensor")
@@ -644,21 +647,24 @@ def select_blocks(scores: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens: torch
     blocks, then those with the largest scores (ties to the lower index), ascending, -1 behind them.
     scores [T, blocks] float32 as index_scores() returns them (rows may be apart). Rows that belong to no
     sequence are left as they are in out (uninitialised when it is allocated here)."""
-    if scores.dtype is not torch.float32 or scores.dim() != 2:
+    shape = scores.shape
+    if len(shape) != 2 or scores.dtype is not torch.float32:
         raise ValueError("scores must be a float32 [T, blocks] tensor with contiguous rows")
-    T, C = scores.shape
+    T, C = shape
     stride, inner = scores.stride()
-    if T > 0 and C > 1 and inner != 1:
+    if inner != 1 and T > 0 and C > 1:
         raise ValueError("scores must be a float32 [T, blocks] tensor with contiguous rows")
     if T <= 1:
         stride = max(stride, C)
     if stride < C:
         raise ValueError("the rows of scores must not overlap")
     B = _ragged(seq_lens, cu_q_lens)
-    _error_word(device_error)
-    if top_k < 1 or keep_first < 0 or keep_last < 0 or keep_first + keep_last > top_k:
+    if device_error is not None:
+        _error_word(device_error)
+    if keep_first < 0 or keep_last < 0 or not 0 < top_k <= _I32_MAX or keep_first + keep_last > top_k:
         raise ValueError("top_k must be positive and hold keep_first + keep_last blocks")
-    _int32_max(top_k=top_k, block_size=block_size)
+    if not 0 < block_size <= _I32_MAX:
+        raise ValueError("block_size must be positive and fit 32 bits")
     if out is not None and (out.dtype is not torch.int32 or out.shape != (T, top_k) or not out.is_contiguous()):
         raise ValueError("out must be a contiguous int32 [T, top_k] tensor")
     handle, at = _addresses(stream, scores, seq_lens, cu_q_lens, out, device_error)
@@ -674,7 +680,9 @@ def select_blocks(scores: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens: torch
 
 def make_sparse_params(batch, num_tokens, num_heads, page_size, num_pages, max_blocks_per_seq, max_seq_len, block_size,
                        top_k, kv_dtype, causal=True) -> SparseParams:
-    _int32_max(max_seq_len=max_seq_len, block_size=block_size, top_k=top_k)
+    for name, value in (("max_seq_len", max_seq_len), ("block_size", block_size), ("top_k", top_k)):
+        if value > _I32_MAX:
+            raise ValueError(f"{name} must fit 32 bits")
     return SparseParams(int(batch), int(num_tokens), int(num_heads), int(page_size), int(num_pages),
                         int(max_blocks_per_seq), int(max_seq_len), int(block_size), int(top_k), int(kv_dtype),
                         int(bool(causal)))
@@ -700,14 +708,17 @@ def sparse_attention(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch
     block_size tokens. selected [T, K] int32, as select_blocks() returns it, is a set for each token:
     order and repetitions do not matter, entries that name no block with a visible key (-1 among them)
     are left out. A token without any key gets out 0 and lse -inf. Returns (out, lse)."""
-    if q.dim() != 3 or q.shape[2] != D_QK or q.dtype != torch.bfloat16 or not q.is_contiguous():
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != D_QK or q.dtype is not torch.bfloat16 or not q.is_contiguous():
         raise ValueError("q must be a contiguous bf16 [T, H, 576] tensor")
-    T, H, _ = q.shape
-    if kv_cache.dim() != 3 or kv_cache.shape[2] != D_QK or not kv_cache.is_contiguous():
+    T, H, _ = shape
+    shape = kv_cache.shape
+    if len(shape) != 3 or shape[2] != D_QK or not kv_cache.is_contiguous():
         raise ValueError("kv_cache must be a contiguous [Np, P, 576] tensor")
-    Np, P, _ = kv_cache.shape
+    Np, P, _ = shape
     B = _ragged(seq_lens, cu_q_lens, block_table)
-    if selected.dtype is not torch.int32 or selected.dim() != 2 or selected.shape[0] != T or not selected.is_contiguous():
+    shape = selected.shape
+    if len(shape) != 2 or shape[0] != T or selected.dtype is not torch.int32 or not selected.is_contiguous():
         raise ValueError("selected must be a contiguous int32 [T, K] tensor")
     kvd = _kv_dtype_of(kv_cache)
     if kvd == KV_FP8_E4M3 and (kv_scale is None or kv_scale.dtype != torch.float32 or kv_scale.numel() < 1):
@@ -719,7 +730,7 @@ def sparse_attention(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch
     if workspace is not None and not workspace.is_contiguous():     # its size is taken from its elements
         raise ValueError("workspace must be contiguous")
     scale = kv_scale if kvd == KV_FP8_E4M3 else None
-    params = make_sparse_params(B, T, H, P, Np, block_table.shape[1], max_seq_len, block_size, selected.shape[1], kvd, causal)
+    params = make_sparse_params(B, T, H, P, Np, block_table.shape[1], max_seq_len, block_size, shape[1], kvd, causal)
     handle, at = _addresses(stream, q, kv_cache, block_table, seq_lens, cu_q_lens, selected, scale, out, lse, workspace)
     if out is None:
         out = _allocated(stream, (T, H, D_V), torch.bfloat16, q.device)

@@ -762,6 +762,16 @@ mla_status check_blocks(const mla_index_params* p) {
   if ((int64_t)p->num_pages * p->page_size >= (int64_t)1 << 31) return MLA_ERR_UNSUPPORTED;
   return MLA_OK;
 }
+std::atomic<uint32_t> g_index_prepared[kMaxDevices];   // bit 0: index scores, 1: sparse plan
+
+// per-device attributes, once
+template <class Prepare>
+bool prepare_once(int dev, uint32_t bit, Prepare&& prepare) {
+  if (g_index_prepared[dev].load() & bit) return true;
+  if (prepare() != cudaSuccess) return false;
+  g_index_prepared[dev].fetch_or(bit);
+  return true;
+}
 int blocks_of(int len, int block) { return (len + block - 1) / block; }
 // rows of 128 bytes
 bool encode_index_map(CUtensorMap* m, const void* base, int64_t rows, uint32_t box_rows) {
@@ -791,7 +801,7 @@ MLA_EXPORT mla_status mla_index_scores(const mla_index_params* p, const void* q_
   int dev;
   if (current_device(&dev) != cudaSuccess) return MLA_ERR_CUDA;
   const int nsm = sm_count(dev);
-  if (nsm <= 0 || !get_encoder()) return MLA_ERR_CUDA;
+  if (nsm <= 0 || !get_encoder() || !prepare_once(dev, 1u, index_scores_prepare)) return MLA_ERR_CUDA;
   IndexScoreArgs a;
   std::memset(&a, 0, sizeof(a));
   const int64_t rows = (int64_t)p->num_pages * p->page_size;
@@ -919,7 +929,7 @@ MLA_EXPORT mla_status mla_sparse_attention(const mla_sparse_params* p, const voi
   const SparseWs w = sparse_ws_layout(p->num_tokens, p->num_heads, width, pairs);
   if (workspace_bytes < w.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
   if (!get_encoder()) return MLA_ERR_CUDA;
-  if (prepare_chunk(dev, fp8) != cudaSuccess) return MLA_ERR_CUDA;
+  if (prepare_chunk(dev, fp8) != cudaSuccess || !prepare_once(dev, 2u, sparse_plan_prepare)) return MLA_ERR_CUDA;
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -47,6 +47,7 @@ struct IndexScoreArgs {
   int32_t test_stall;
   uint64_t wait_limit_ns;
 };
+cudaError_t index_scores_prepare();   // per-device kernel attributes
 cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s);
 
 struct SelectArgs {
@@ -74,6 +75,7 @@ struct SparsePlanArgs {
   int32_t words;                   // 32-bit words of a token's set of blocks
 };
 constexpr int kPlanCtas = 8;       // one cluster
+cudaError_t sparse_plan_prepare();    // per-device kernel attributes
 cudaError_t launch_sparse_plan(const SparsePlanArgs& a, cudaStream_t s);
 
 struct SparseWs {

@@ -606,6 +606,14 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
   if (warp == 1) tmem_dealloc(tmem, kISTmem);
 }
 
+cudaError_t index_scores_prepare() {
+  for (auto* kernel : {index_scores_kernel<0>, index_scores_kernel<1>, index_scores_kernel<2>, index_scores_kernel<4>}) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kISSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
 cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s) {
   a.Hp = (a.H + 15) / 16 * 16;
   a.sub_tokens = kISColumns / a.Hp;
@@ -646,12 +654,10 @@ cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto go = [&](auto* kernel) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kISSmem);
-    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kernel, a);
-  };
-  return a.H == 32 ? go(index_scores_kernel<1>) : a.H == 64 ? go(index_scores_kernel<2>)
-         : a.H == 128 ? go(index_scores_kernel<4>) : go(index_scores_kernel<0>);
+  return a.H == 32    ? cudaLaunchKernelEx(&cfg, index_scores_kernel<1>, a)
+         : a.H == 64  ? cudaLaunchKernelEx(&cfg, index_scores_kernel<2>, a)
+         : a.H == 128 ? cudaLaunchKernelEx(&cfg, index_scores_kernel<4>, a)
+                      : cudaLaunchKernelEx(&cfg, index_scores_kernel<0>, a);
 }
 
 }  // namespace mla

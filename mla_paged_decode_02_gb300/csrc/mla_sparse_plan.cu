@@ -25,6 +25,7 @@
 namespace mla {
 namespace {
 
+constexpr int kRoom = 220 * 1024;          // shared memory for lengths and sets
 constexpr int kPlanLens = 8192;            // tokens whose lengths fit the first CTA's shared memory
 
 __device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kChunkTile - 1) / kChunkTile : 1; }
@@ -213,15 +214,16 @@ __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePla
   }
 }
 
+cudaError_t sparse_plan_prepare() {
+  return cudaFuncSetAttribute(sparse_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
+}
+
 cudaError_t launch_sparse_plan(const SparsePlanArgs& a, cudaStream_t s) {
   // as many warps as have room for their sets: 32 for contexts up to 48 K blocks
-  constexpr int kRoom = 220 * 1024;
   const int lens = a.T <= kPlanLens ? a.T : 0;
   int warps = (kRoom - lens * 4) / (a.words * 4);
   warps = warps > 32 ? 32 : warps;
   const size_t smem = (size_t)lens * 4 + (size_t)warps * a.words * 4;
-  cudaError_t e = cudaFuncSetAttribute(sparse_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kPlanCtas);
   cfg.blockDim = dim3(kSchedThreads);
