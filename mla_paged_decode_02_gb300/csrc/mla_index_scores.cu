@@ -20,9 +20,8 @@
 // Roles (640 threads): warp 0 resolves units, loads their queries and weights, and writes their scores;
 // warp 3 loads keys (TMA boxes from the page table) and their scales; warps 1 and 2 issue the MMAs, each into a
 // pair of accumulators of 128 columns: two sub-groups of a tile, or two tiles of one; four warpgroups take
-// an accumulator each. The maxima of
-// a unit's blocks gather in shared memory. Every wait is bounded; a stall sets the error word, and the CTA
-// drains and leaves.
+// an accumulator each. The maxima of a unit's blocks gather in shared memory. Every wait is bounded; a stall
+// sets the error word, and the CTA drains and leaves.
 #include "mla_index.h"
 #include "mla_ptx.cuh"
 #include "mla_ragged.cuh"
@@ -41,8 +40,9 @@ constexpr int kISKeys = 128;                      // keys of a tile
 constexpr int kISSlotBytes = kISKeys * kDIndex;   // 16 KB
 constexpr int kISMaxSlots = 12;
 // Key scales have a ring of their own, read later than the keys. A slot of it is filled for tile t + 16
-// once the MMAs of tile t + 16 - 12 or a later one are done, which were issued after the product four
-// before them, of tile t or later, had been read.
+// once the keys of tile t + 4 or a later one have been given back by both issuing warps. A product covers
+// two tiles at most and the two pairs of accumulators alternate, so by then the warp that issued tile t's
+// product has issued its next one, which waited until tile t's had been read.
 constexpr int kISScales = 16;
 constexpr uint32_t kISFirstWaitNs = 20000;        // a wait's first, sleeping look
 constexpr int kISBest = 1024;                     // (token, block) maxima of a unit, at most

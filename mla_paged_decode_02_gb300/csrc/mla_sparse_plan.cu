@@ -12,7 +12,10 @@
 // equally many tiles of 256 keys; laid end to end, X set-up positions and the tiles for each, worker c
 // (a CTA pair) takes positions [c q, (c + 1) q), q = ceil(all / workers). A block that a boundary cuts
 // becomes one unit per worker. (The partition of the chunk scheduler, without its search for the
-// sequence of a block: here a block's number says which token it belongs to.)
+// sequence of a block: here a block's number says which token it belongs to.) Where a share holds six
+// blocks or more, blocks stay whole and go to the worker in whose share their middle lies: a worker then
+// has up to half a block more, and nothing is merged (512 tokens x 128 heads x 2048 keys, bf16: 192 us so,
+// 194 with cut blocks, whose merge takes 12).
 //
 // One cluster of eight CTAs: a warp takes a token at a time and sends its length to the first CTA's shared
 // memory, where the partition is made. Bound by latency: the list, lengths and offsets are read at once,
@@ -166,6 +169,35 @@ __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePla
   const bool small = W + S * X + q < (int64_t)1 << 31;   // (64-bit divisions are several times as long)
   auto worker_of = [&](int64_t p) -> int64_t { return small ? (int64_t)((uint32_t)p / (uint32_t)q) : p / q; };
   const int64_t pos0 = before + (int64_t)(t0 - first) * G * X;
+  if (q >= 6 * (int64_t)(tiles_of(a.width * a.block) + X)) {
+    for (int c = tid; c <= s.workers; c += kSchedThreads) s.cta_first[c] = (int32_t)S;
+    if (tid == 0) {
+      s.hdr[1] = (uint32_t)S;
+      s.hdr[2] = 0;
+      s.hdr[3] = (uint32_t)(q < 0xFFFFFFFFll ? q : 0xFFFFFFFFll);
+      s.hdr[4] = (uint32_t)X;
+    }
+    __syncthreads();
+    int64_t pos = pos0, last_worker = -1;
+    if (t0 > first && t0 < t1) {
+      const int n = tiles_of(len_of(t0 - 1));
+      last_worker = worker_of(pos0 - (X + n) + (X + n) / 2);
+    }
+    for (int t = t0; t < t1; ++t) {
+      const int len = len_of(t), n = tiles_of(len);
+      for (int g = 0; g < G; ++g) {
+        const int64_t c = worker_of(pos + (X + n) / 2), unit = (int64_t)(t - first) * G + g;
+        const int r0 = g * kChunkRows, rows = min(kChunkRows, s.H - r0);
+        int4* u = reinterpret_cast<int4*>(s.units + unit);
+        u[0] = make_int4(t, (int32_t)((int64_t)t * s.H + r0), r0, (len > 0 ? n : 0) << 16);
+        u[1] = make_int4(-1, len, len, rows);
+        if (c != last_worker) s.cta_first[c] = (int32_t)unit;
+        last_worker = c;
+        pos += X + n;
+      }
+    }
+    return;
+  }
   int64_t pos = pos0, mine3 = 0;           // units << 32 | cut blocks << 16 | partial slots (as the chunk scheduler)
   for (int t = t0; t < t1; ++t) {
     const int n = tiles_of(len_of(t));

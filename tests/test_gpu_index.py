@@ -181,6 +181,31 @@ def test_scores_of_many_sequences_with_idle_ones_and_long_contexts():
     c.check(list(range(0, 1100, 41)) + [1100])
 
 
+def test_scores_of_short_contexts_under_a_long_limit():
+    c = ScoreCase([(1, 40), (0, 9), (2, 300), (1, 1)], 64, 16, 8, seed=7, max_seq_len=1 << 20)
+    c.run()
+    c.check()
+
+
+def test_scores_of_calls_at_once():
+    cases = [ScoreCase([(60, 900), (1, 2000)], 64, 64, 64, seed=20 + i) for i in range(3)]
+    for c in cases:
+        c.run()
+    want = [c.out.clone() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for c, s in zip(cases, streams):
+            c.out.fill_(7.5)
+        torch.cuda.synchronize()
+        for c, s in zip(cases, streams):
+            api.index_scores(*c.dev, max_seq_len=c.max_seq_len, block_size=64, out=c.out, device_error=c.error, stream=s)
+        torch.cuda.synchronize()
+        for c, w in zip(cases, want):
+            assert torch.equal(c.out, w)
+    cases[0].check()
+
+
 def test_scores_of_keys_and_queries_that_are_not_finite():
     c = ScoreCase([(3, 200)], 16, 64, 64, seed=2)
     j = c.slots[0]

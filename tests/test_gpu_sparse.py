@@ -100,6 +100,54 @@ def test_many_tokens_and_sequences():
     c.check(list(range(0, 700, 23)))
 
 
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_whole_blocks_of_many_tokens(kv):
+    """Shares of six row blocks or more are not cut; lists of all lengths, rows that see nothing among them."""
+    rng = np.random.default_rng(3)
+    lens = [(400, 900), (0, 30), (300, 250), (37, 37), (200, 2000)]
+    c = SparseCase(lens, 130, 64, 32, 3, kv, seed=12, pad=5, lead=3)
+    c.selected[::7] = -1
+    c.selected[5] = torch.tensor([2, 1, 0])
+    c.run()
+    torch.cuda.synchronize()
+    assert api.decode_check(c.workspace) == (0, 0)
+    for b, (n, _) in enumerate(lens):
+        for i in sorted(set(rng.integers(0, n, 12).tolist()) | {0, n - 1}) if n else ():
+            t = c.starts[b] + i
+            keys = c.keys_of(b, i)
+            out, lse = c.out[t].double().cpu(), c.lse[t].double().cpu()
+            if not keys:
+                assert (out == 0).all() and (lse == -INF).all()
+                continue
+            k = c.keys[b][keys]
+            s = c.q[t].double() @ k.T * SCALE
+            w = torch.softmax(s, dim=1)
+            A, r = w @ k[:, :512].abs(), w @ k[:, :512]
+            bound = 2.0 ** -8 * (A + r.abs())
+            if kv == F8:
+                bound = bound + 2.0 ** -11 * A + 2.0 ** -13 * k[:, :512].abs().sum(dim=0) * w.amax(dim=1, keepdim=True) + \
+                    2.0 ** -16 * c.q[t].double().abs().amax() * SCALE * k.abs().sum(dim=1).max() * A
+            assert ((out - r).abs() <= 1.05 * bound + 1e-6).all()
+            assert (lse - torch.logsumexp(s, dim=1)).abs().max() <= LSE_ABS[kv]
+    assert (c.out[:3] == 7.0).all() and (c.out[-5:] == 7.0).all() and (c.lse[-5:] == -3.5).all()
+
+
+def test_more_tokens_than_lengths_fit_shared_memory():
+    lens = [(4000, 4000), (5000, 5100), (1, 70)]
+    c = SparseCase(lens, 1, 16, 16, 2, BF, seed=13)
+    c.run()
+    torch.cuda.synchronize()
+    assert api.decode_check(c.workspace) == (0, 0)
+    for b, i in ((0, 0), (0, 1), (0, 3999), (1, 0), (1, 2500), (1, 4999), (2, 0)):
+        t = c.starts[b] + i
+        k = c.keys[b][c.keys_of(b, i)]
+        s = c.q[t].double() @ k.T * SCALE
+        w = torch.softmax(s, dim=1)
+        A, r = w @ k[:, :512].abs(), w @ k[:, :512]
+        assert ((c.out[t].double().cpu() - r).abs() <= 1.05 * 2.0 ** -8 * (A + r.abs()) + 1e-6).all()
+        assert (c.lse[t].double().cpu() - torch.logsumexp(s, dim=1)).abs().max() <= LSE_ABS[BF]
+
+
 def test_a_long_context():
     L = (1 << 20) - 3
     pages = L // 64 + 1
