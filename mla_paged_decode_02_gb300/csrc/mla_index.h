@@ -41,8 +41,7 @@ struct IndexScoreArgs {
   int32_t Hp, TG, sub_tokens;      // columns of a token, tokens of a group (a power of two) and of a sub-group
   int32_t tg_log2;
   int32_t q_rows, units, key_slots;   // rows of a query buffer, query buffers, tiles of keys in shared memory
-  int32_t slots, chunks;           // group numbers, stretches of unit_blocks blocks
-  int32_t unit_blocks;
+  int32_t unit_blocks;             // blocks of a unit
   uint32_t block_inv;              // 2^32 / block, rounded up
   int32_t test_stall;
   uint64_t wait_limit_ns;

@@ -10,14 +10,14 @@
 // same for all lanes, and only the maximum over a block's keys crosses lanes. A token's heads start
 // at a multiple of 16 columns; the columns between hold whatever follows in memory and are never read.
 //
-// Work is cut into units of one group of neighbouring tokens x `unit_blocks` blocks; persistent CTAs, one
-// per SM, take them in turn, all groups of one stretch of the context before the next, so that groups of
-// a sequence find its keys in L2. A group is up to four sub-groups of 128 columns, which share each key
-// tile in shared memory. A group's number says which sequence it belongs to: sequence b's groups start at
-// cu_q[b] / TG + b (TG tokens to a group), which leaves room enough for each, and a lane finds its unit's
-// by bisection. (With one token to a group that is token g itself.)
+// Work is cut into units of one group of up to TG neighbouring tokens x `unit_blocks` blocks, as far as the
+// context goes; persistent CTAs, one per SM, take them in turn. Units are numbered by sequence and, within
+// one, all groups of a stretch of the context before the next, so that groups of a sequence find its keys
+// in L2. Each CTA counts them itself, 512 sequences at a time, and a lane finds its unit's sequence by
+// bisection: 32 units at once. A group is up to four sub-groups of 128 columns, which share each key tile
+// in shared memory.
 //
-// Roles (640 threads): warp 0 resolves units, loads their queries and weights, and writes their scores;
+// Roles (640 threads): warp 0 counts units, loads their queries and weights, and writes their scores;
 // warp 3 loads keys (TMA boxes from the page table) and their scales; warps 1 and 2 issue the MMAs, each into a
 // pair of accumulators of 128 columns: two sub-groups of a tile, or two tiles of one; four warpgroups take
 // an accumulator each. The maxima of a unit's blocks gather in shared memory. Every wait is bounded; a stall
@@ -48,8 +48,8 @@ constexpr uint32_t kISFirstWaitNs = 20000;        // a wait's first, sleeping lo
 constexpr int kISBest = 1024;                     // (token, block) maxima of a unit, at most
 constexpr int kISMaxUnits = 4;                    // units whose queries are in shared memory
 constexpr int kISMaxTokens = 32;                  // of a group: 512 columns / 16
-constexpr int kISSeqs = 512;                      // sequences whose offsets and lengths are kept in shared memory
-constexpr int kISSmem = 221 * 1024;               // dynamic
+constexpr int kISSeqs = 512;                      // sequences whose units are counted at a time
+constexpr int kISSmem = 216 * 1024;               // dynamic
 // all but the key tiles: queries, scales, maxima, weights
 constexpr int is_fixed_bytes(int units, int q_rows, int maxima) {
   return 1024 + kISScales * kISKeys * 4 + units * (q_rows * kDIndex + maxima * 4 + q_rows * 4);
@@ -175,14 +175,9 @@ __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, uint32_t
 struct UnitInfo {
   int t0, ntok, seq;     // its tokens and their sequence; ntok = 0: no more units
   int k0, last, tiles;   // first key, end of the keys that a token sees, tiles of 128 keys
-  int c0, blocks;        // first column of the scores, columns to be written
+  int c0, blocks, rest;  // first column of the scores, columns with maxima and those of -inf behind them
   int seen[kISMaxTokens];
 };
-
-// The first group of sequence b, whose tokens start at row `start` (groups are a power of two).
-__device__ __forceinline__ int first_group(const IndexScoreArgs& a, int start, int b) {
-  return a.TG == 1 ? start : (start >> a.tg_log2) + b;
-}
 
 __device__ uint32_t g_unreported;                 // error bits of calls without an error word
 
@@ -198,6 +193,7 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
       bar_qfull[kISMaxUnits], bar_qempty[kISMaxUnits], bar_tfull[kISIssuers], bar_tempty[kISIssuers], bar_drain[kISIssuers], bar_never;
   __shared__ UnitInfo info_s[kISMaxUnits];
   __shared__ int cu_s[kISSeqs + 1], len_s[kISSeqs];
+  __shared__ uint32_t first_s[kISSeqs + 1];         // a sequence's first unit
   __shared__ uint32_t tmem_base_s, abort_s;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int S = a.key_slots, q_rows = a.q_rows, units = a.units, maxima = a.TG * a.unit_blocks;
@@ -238,10 +234,6 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
   for (int i = threadIdx.x; i < units * maxima; i += kISThreads) best[i] = kLowest;
   griddep_wait();
   griddep_launch_dependents();
-  for (int b = threadIdx.x; b <= min(a.B, kISSeqs); b += kISThreads) {
-    cu_s[b] = a.cu_q[b];
-    if (b < min(a.B, kISSeqs)) len_s[b] = a.seq_lens[b];
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -257,7 +249,7 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
     const bool el = elect_one();
     uint32_t ub = 0, uph = 1, nu = 0;                   // the unit's buffer and the parity of its barriers, units so far
     bool ok = true;
-    const int64_t total = (int64_t)a.slots * a.chunks;
+    const int unit_keys = a.unit_blocks * a.block;
     const bool wide_weights = (reinterpret_cast<uintptr_t>(a.w) & 15) == 0;
     // waits until a buffer's last unit is done, and writes its scores
     auto finish_unit = [&](uint32_t buffer, uint32_t parity, bool used) -> bool {
@@ -265,85 +257,120 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
       if (!used) return true;
       const UnitInfo& I = info_s[buffer];
       int* from = best + buffer * maxima;
-      for (int i = 0; i < I.ntok; ++i)
+      for (int i = 0; i < I.ntok; ++i) {
+        float* to = a.out + (int64_t)(I.t0 + i) * a.C + I.c0;
         for (int c = lane; c < a.unit_blocks; c += 32) {
-          if (c < I.blocks) a.out[(int64_t)(I.t0 + i) * a.C + I.c0 + c] = from_ordered(from[i * a.unit_blocks + c]);
+          if (c < I.blocks) to[c] = from_ordered(from[i * a.unit_blocks + c]);
           from[i * a.unit_blocks + c] = kLowest;
         }
+        for (int c = lane; c < I.rest; c += 32) to[I.blocks + c] = -INFINITY;
+      }
       __syncwarp();
       return true;
     };
-    auto cu = [&](int b) { return b <= kISSeqs ? cu_s[b] : a.cu_q[b]; };
-    for (int64_t base = blockIdx.x; base < total && ok; base += 32 * (int64_t)gridDim.x) {
-      // 32 units at a time, one to a lane
-      const int64_t u = base + (int64_t)lane * gridDim.x;
-      int b = 0, t0 = 0, ntok = 0, k0 = 0, last = 0, start = 0, end = 0, L = 0;
-      if (u < total) {
-        const int chunk = (int)(u / a.slots), g = (int)(u - (int64_t)chunk * a.slots);
-        int lo = 0, hi = a.B;                           // the last b whose first group is at most g
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (first_group(a, cu(mid), mid) <= g) lo = mid;
-          else hi = mid;
+    int64_t next = blockIdx.x, counted = 0;             // this CTA's next unit; units of the sequences before
+    for (int b0 = 0; b0 < a.B && ok; b0 += kISSeqs) {
+      // units of up to 512 sequences
+      const int nb = min(a.B - b0, kISSeqs);
+      for (int i = lane; i <= nb; i += 32) cu_s[i] = a.cu_q[b0 + i];
+      for (int i = lane; i < nb; i += 32) len_s[i] = max(0, min(a.seq_lens[b0 + i], a.max_len));
+      __syncwarp();
+      uint32_t units_before = 0;
+      bool bad = false;
+      for (int i0 = 0; i0 < nb; i0 += 32) {
+        uint32_t mine = 0;
+        if (i0 + lane < nb) {
+          const int n = cu_s[i0 + lane + 1] - cu_s[i0 + lane];
+          bad |= cu_s[i0 + lane] < 0 || n < 0 || cu_s[i0 + lane + 1] > a.T;
+          // (a sequence without keys has a unit that sees none)
+          if (n > 0) mine = (uint32_t)((n + TG - 1) >> a.tg_log2) * (uint32_t)max(1, (len_s[i0 + lane] + unit_keys - 1) / unit_keys);
         }
-        b = lo;
-        start = max(0, cu(b));
-        end = min(a.T, cu(b + 1));
-        const int skip = g - first_group(a, start, b);
-        const int64_t first = (int64_t)start + (int64_t)skip * TG;
-        if (skip >= 0 && first < end) {
-          t0 = (int)first;
+        uint32_t x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        if (i0 + lane < nb) first_s[i0 + lane] = units_before + x - mine;
+        units_before += __shfl_sync(0xffffffffu, x, 31);
+      }
+      __syncwarp();
+      if (__any_sync(0xffffffffu, bad)) break;          // offsets that do not ascend: no scores from here on
+      const int64_t end_units = counted + units_before;
+      for (; next < end_units && ok; next += 32 * (int64_t)gridDim.x) {
+        // 32 units at a time, one to a lane
+        const int64_t u = next + (int64_t)lane * gridDim.x;
+        int b = 0, t0 = 0, ntok = 0, chunk = 0, start = 0, end = 0, L = 0;
+        if (u < end_units) {
+          const uint32_t r = (uint32_t)(u - counted);
+          int hi = nb;                                  // the last sequence whose first unit is at most r
+          while (hi - b > 1) {
+            const int mid = (b + hi) >> 1;
+            if (first_s[mid] <= r) b = mid;
+            else hi = mid;
+          }
+          start = cu_s[b];
+          end = cu_s[b + 1];
+          L = len_s[b];
+          const uint32_t groups = (uint32_t)((end - start + TG - 1) >> a.tg_log2), in = r - first_s[b];
+          chunk = (int)(in / groups);
+          t0 = start + ((int)(in - (uint32_t)chunk * groups) << a.tg_log2);
           ntok = min(TG, end - t0);
-          L = max(0, min(b < kISSeqs ? len_s[b] : a.seq_lens[b], a.max_len));
-          k0 = chunk * a.unit_blocks * a.block;
-          last = min(keys_seen(t0 + ntok - 1, start, end, L, a.causal), k0 + a.unit_blocks * a.block);
+        }
+        const int taken = __popc(__ballot_sync(0xffffffffu, u < end_units));
+        for (int src = 0; src < taken && ok; ++src) {
+          const int us = b0 + __shfl_sync(0xffffffffu, b, src), ut0 = __shfl_sync(0xffffffffu, t0, src);
+          const int un = __shfl_sync(0xffffffffu, ntok, src), uchunk = __shfl_sync(0xffffffffu, chunk, src);
+          const int ustart = __shfl_sync(0xffffffffu, start, src), uend = __shfl_sync(0xffffffffu, end, src);
+          const int uL = __shfl_sync(0xffffffffu, L, src);
+          const int c0 = uchunk * a.unit_blocks, uk0 = uchunk * unit_keys;
+          const int ulast = min(keys_seen(ut0 + un - 1, ustart, uend, uL, a.causal), uk0 + unit_keys);
+          // the blocks behind the sequence's last unit hold no key
+          const int blocks = min(a.unit_blocks, a.C - c0), rest = uk0 + unit_keys >= uL ? a.C - c0 - blocks : 0;
+          if (ulast <= uk0) {                             // no token sees these blocks
+            for (int i = 0; i < un; ++i)
+              for (int c = lane; c < blocks + rest; c += 32) a.out[(int64_t)(ut0 + i) * a.C + c0 + c] = -INFINITY;
+            continue;
+          }
+          ok = finish_unit(ub, uph, nu >= (uint32_t)units);
+          if (!ok) break;
+          UnitInfo& I = info_s[ub];
+          if (lane == 0) {
+            I.t0 = ut0;
+            I.ntok = un;
+            I.k0 = uk0;
+            I.last = ulast;
+            I.tiles = (ulast - uk0 + kISKeys - 1) / kISKeys;
+            I.c0 = c0;
+            I.blocks = blocks;
+            I.rest = rest;
+            I.seq = us;
+          }
+          if (lane < un) I.seen[lane] = keys_seen(ut0 + lane, ustart, uend, uL, a.causal);
+          // weights: one copy where a token's fill its columns, else by loads
+          const uint32_t wbytes = a.H == Hp && wide_weights ? (uint32_t)(un * Hp) * 4 : 0u;
+          if (wbytes == 0)
+            for (int i = lane; i < un * a.H; i += 32) gW[ub * q_rows + (i / a.H) * Hp + i % a.H] = a.w[(int64_t)ut0 * a.H + i];
+          __syncwarp();
+          const int qboxes = un * (Hp / 16);
+          if (el) {
+            mbar_arrive(b_info + 8 * ub);
+            mbar_arrive_expect_tx(b_qfull + 8 * ub, (uint32_t)qboxes * 16 * kDIndex + wbytes);
+            if (wbytes) bulk_load(smem_u32(gW + ub * q_rows), a.w + (int64_t)ut0 * a.H, wbytes, b_qfull + 8 * ub);
+          }
+          __syncwarp();
+          for (int i = lane; i < qboxes; i += 32)
+            tma_load_2d(sQ + ub * q_rows * kDIndex + i * 16 * kDIndex, &a.tm_q, b_qfull + 8 * ub, 0,
+                        (ut0 + i / (Hp / 16)) * a.H + (i % (Hp / 16)) * 16);
+          ++nu;
+          if (++ub == (uint32_t)units) { ub = 0; uph ^= 1; }
+        }
+        if (taken < 32) {                               // the rest are units of sequences to come
+          next += (int64_t)taken * gridDim.x;
+          break;
         }
       }
-      for (uint32_t m = __ballot_sync(0xffffffffu, ntok > 0); m != 0 && ok; m &= m - 1) {
-        const int src = __ffs(m) - 1;
-        const int us = __shfl_sync(0xffffffffu, b, src), ut0 = __shfl_sync(0xffffffffu, t0, src);
-        const int un = __shfl_sync(0xffffffffu, ntok, src), uk0 = __shfl_sync(0xffffffffu, k0, src);
-        const int ulast = __shfl_sync(0xffffffffu, last, src);
-        const int c0 = (int)((base + (int64_t)src * gridDim.x) / a.slots) * a.unit_blocks, blocks = min(a.unit_blocks, a.C - c0);
-        if (ulast <= uk0) {                             // no token sees these blocks
-          for (int i = 0; i < un; ++i)
-            for (int c = lane; c < blocks; c += 32) a.out[(int64_t)(ut0 + i) * a.C + c0 + c] = -INFINITY;
-          continue;
-        }
-        const int ustart = __shfl_sync(0xffffffffu, start, src), uend = __shfl_sync(0xffffffffu, end, src);
-        const int uL = __shfl_sync(0xffffffffu, L, src);
-        ok = finish_unit(ub, uph, nu >= (uint32_t)units);
-        if (!ok) break;
-        UnitInfo& I = info_s[ub];
-        if (lane == 0) {
-          I.t0 = ut0;
-          I.ntok = un;
-          I.k0 = uk0;
-          I.last = ulast;
-          I.tiles = (ulast - uk0 + kISKeys - 1) / kISKeys;
-          I.c0 = c0;
-          I.blocks = blocks;
-          I.seq = us;
-        }
-        if (lane < un) I.seen[lane] = keys_seen(ut0 + lane, ustart, uend, uL, a.causal);
-        // weights: one copy where a token's fill its columns, else by loads
-        const uint32_t wbytes = a.H == Hp && wide_weights ? (uint32_t)(un * Hp) * 4 : 0u;
-        if (wbytes == 0)
-          for (int i = lane; i < un * a.H; i += 32) gW[ub * q_rows + (i / a.H) * Hp + i % a.H] = a.w[(int64_t)ut0 * a.H + i];
-        __syncwarp();
-        const int qboxes = un * (Hp / 16);
-        if (el) {
-          mbar_arrive(b_info + 8 * ub);
-          mbar_arrive_expect_tx(b_qfull + 8 * ub, (uint32_t)qboxes * 16 * kDIndex + wbytes);
-          if (wbytes) bulk_load(smem_u32(gW + ub * q_rows), a.w + (int64_t)ut0 * a.H, wbytes, b_qfull + 8 * ub);
-        }
-        __syncwarp();
-        for (int i = lane; i < qboxes; i += 32)
-          tma_load_2d(sQ + ub * q_rows * kDIndex + i * 16 * kDIndex, &a.tm_q, b_qfull + 8 * ub, 0,
-                      (ut0 + i / (Hp / 16)) * a.H + (i % (Hp / 16)) * 16);
-        ++nu;
-        if (++ub == (uint32_t)units) { ub = 0; uph ^= 1; }
-      }
+      counted = end_units;
     }
     // the end of the units: the others leave, and the last units' scores are written
     ok = ok && finish_unit(ub, uph, nu >= (uint32_t)units);
@@ -617,33 +644,32 @@ cudaError_t index_scores_prepare() {
 cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s) {
   a.Hp = (a.H + 15) / 16 * 16;
   a.sub_tokens = kISColumns / a.Hp;
-  // a decode step's groups are one token; with two tokens or more to a sequence on average, up to four
-  // sub-groups share each key tile
-  const bool many = a.T >= 2 * (int64_t)a.B;
-  a.TG = many ? 2 * kISIssuers * a.sub_tokens : 1;
-  a.tg_log2 = 31 - __builtin_clz((unsigned)a.TG);      // 128 / Hp rounded down is a power of two
+  // tokens to a group: as many as sequences have on average (a power of two), up to four sub-groups
+  const int most_tokens = 2 * kISIssuers * a.sub_tokens;
+  a.tg_log2 = 0;
+  while ((1 << a.tg_log2) < a.T / a.B && (1 << a.tg_log2) < most_tokens) ++a.tg_log2;
+  a.TG = 1 << a.tg_log2;
+  const bool many = a.TG > a.sub_tokens;
   a.q_rows = a.TG * a.Hp;
-  a.slots = a.TG == 1 ? a.T : a.T / a.TG + a.B;
-  // a unit: whole blocks and whole tiles, 512 to 8192 keys, about 24 units to a CTA (8 of a decode step)
+  // a unit: whole blocks and whole tiles, 512 to 8192 keys, about 24 units to a CTA (6 of a decode step)
   int lcm = a.block;
   while (lcm % kISKeys != 0) lcm += a.block;
   const int64_t groups = (a.T + a.TG - 1) / a.TG;
   const int64_t top = many ? 8192 : 1024;
-  int64_t keys = groups * a.max_len / ((many ? 24 : 8) * (int64_t)num_sms);
+  int64_t keys = groups * a.max_len / ((many ? 24 : 6) * (int64_t)num_sms);
   keys = keys < 512 ? 512 : keys > top ? top : keys;
   int64_t m = keys / lcm;
   const int64_t most = kISBest / ((int64_t)a.TG * (lcm / a.block));
   m = m > most ? most : m;
   if (m < 1) m = 1;
   a.unit_blocks = (int)(m * (lcm / a.block));
-  a.chunks = (a.C + a.unit_blocks - 1) / a.unit_blocks;
   a.block_inv = (uint32_t)((((uint64_t)1 << 32) + a.block - 1) / a.block);   // keys of a unit x block < 2^32
-  a.units = many ? 2 : kISMaxUnits;
+  a.units = a.q_rows <= 256 ? kISMaxUnits : 2;
   const int fixed = is_fixed_bytes(a.units, a.q_rows, a.TG * a.unit_blocks);
   a.key_slots = (kISSmem - fixed) / kISSlotBytes;
   if (a.key_slots > kISMaxSlots) a.key_slots = kISMaxSlots;
   const int smem = fixed + a.key_slots * kISSlotBytes;
-  const int64_t total = (int64_t)a.slots * a.chunks;
+  const int64_t total = ((int64_t)a.T / a.TG + a.B) * ((a.C + a.unit_blocks - 1) / a.unit_blocks);   // units at most
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(total < num_sms ? total : num_sms));
   cfg.blockDim = dim3(kISThreads);
