@@ -883,6 +883,67 @@ mla_status check_sparse_params(const mla_sparse_params* p) {
   if ((int64_t)p->num_tokens * p->num_heads > kMaxChunkRows) return MLA_ERR_UNSUPPORTED;
   return MLA_OK;
 }
+cudaError_t prepare_decode16(int dev) {
+  const uint32_t bit = 1u << variant_bit(16, true);
+  if (g_prepared[dev].load() & bit) return cudaSuccess;
+  const cudaError_t e = decode_prepare(16, true);
+  if (e == cudaSuccess) g_prepared[dev].fetch_or(bit);
+  return e;
+}
+
+// the plan, the decode kernel over the tokens' selected blocks, and the merge of cut ones (E4M3, up to 16 rows)
+mla_status sparse_few(const mla_sparse_params* p, const SparsePlanArgs& pa, const void* q, const void* kv_cache,
+                      float softmax_scale, const float* kv_scale, void* out, float* lse, uint8_t* ws, const SparseWs& w,
+                      int nsm, cudaStream_t s) {
+  const int rc = 16, H = p->num_heads, per_page = p->page_size / p->block_size;
+  const int64_t rows = (int64_t)p->num_pages * p->page_size;
+  DecodeArgs da;
+  std::memset(&da, 0, sizeof(da));
+  da.box_rows = 64;
+  if (p->num_tokens > 0 &&
+      (!encode_q_map(&da.tm_q, q, p->num_tokens, H, rc) ||
+       !encode_kv_map(&da.tm_k, kv_cache, rows, (uint32_t)decode_key_chunks_per_slot(rc, true), 64, true, true) ||
+       !encode_kv_map(&da.tm_v, kv_cache, rows, (uint32_t)decode_value_chunks_per_box(rc, true), 64, true, true)))
+    return MLA_ERR_INVALID_ARG;
+  if (launch_sparse_plan(pa, s) != cudaSuccess) return MLA_ERR_CUDA;
+  if (p->num_tokens == 0) return MLA_OK;
+  da.kv_cache = kv_cache;
+  da.block_table = pa.table;
+  da.batch_info = pa.batch_info;
+  da.units = reinterpret_cast<const int4*>(pa.sched.units);
+  da.cta_first = pa.sched.cta_first;
+  da.hdr = pa.sched.hdr;
+  da.out = static_cast<__nv_bfloat16*>(out);
+  da.lse = lse;
+  da.part_o = reinterpret_cast<float*>(ws + w.decode.po_off);
+  da.part_lse = reinterpret_cast<float*>(ws + w.decode.plse_off);
+  da.err = pa.sched.hdr;
+  da.kv_scale = kv_scale;
+  da.s_q = 1;
+  da.H = H;
+  da.R = H;
+  da.P = p->block_size;                    // to the decode kernel a block is a page
+  da.MB = pa.width;
+  da.num_pages = p->num_pages * per_page;
+  da.causal = 0;
+  da.softmax_scale = softmax_scale;
+  da.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  da.test_stall = g_test_stall.load(std::memory_order_relaxed);
+  if (launch_decode(da, rc, true, nsm, s) != cudaSuccess) return MLA_ERR_CUDA;
+  CombineArgs ca{};                        // B = 0: the plan has checked the pages
+  ca.hdr = pa.sched.hdr;
+  ca.err = pa.sched.hdr;
+  ca.split_list = pa.sched.split_list;
+  ca.part_o = da.part_o;
+  ca.part_lse = da.part_lse;
+  ca.out = da.out;
+  ca.lse = lse;
+  ca.R = H;
+  ca.RC = rc;
+  if (launch_combine(ca, 8 * nsm, s) != cudaSuccess) return MLA_ERR_CUDA;
+  return MLA_OK;
+}
+
 // columns of the table of selected blocks
 int sparse_width(const mla_sparse_params* p) { return std::min(p->top_k, blocks_of(p->max_seq_len, p->block_size)); }
 
@@ -898,7 +959,9 @@ MLA_EXPORT size_t mla_sparse_workspace_size(const mla_sparse_params* p, int32_t 
     if (num_sms <= 0) return 0;
   }
   if (num_sms < 2) return 0;
-  return sparse_ws_layout(p->num_tokens, p->num_heads, sparse_width(p), num_sms / 2).total;
+  return sparse_ws_layout(p->num_tokens, p->num_heads, p->kv_dtype == MLA_KV_FP8_E4M3, p->block_size, sparse_width(p),
+                          num_sms)
+      .total;
 }
 
 MLA_EXPORT mla_status mla_sparse_attention(const mla_sparse_params* p, const void* q, const void* kv_cache,
@@ -926,16 +989,31 @@ MLA_EXPORT mla_status mla_sparse_attention(const mla_sparse_params* p, const voi
   const int pairs = nsm / 2;
   if (pairs < 1) return MLA_ERR_UNSUPPORTED;
   const int width = sparse_width(p);
-  const SparseWs w = sparse_ws_layout(p->num_tokens, p->num_heads, width, pairs);
+  const SparseWs w = sparse_ws_layout(p->num_tokens, p->num_heads, fp8, p->block_size, width, nsm);
   if (workspace_bytes < w.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
   if (!get_encoder()) return MLA_ERR_CUDA;
-  if (prepare_chunk(dev, fp8) != cudaSuccess || !prepare_once(dev, 2u, sparse_plan_prepare)) return MLA_ERR_CUDA;
+  if (!prepare_once(dev, 2u, sparse_plan_prepare)) return MLA_ERR_CUDA;
+  if (w.few ? prepare_decode16(dev) != cudaSuccess : prepare_chunk(dev, fp8) != cudaSuccess) return MLA_ERR_CUDA;
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int per_page = p->page_size / p->block_size;
   SparsePlanArgs pa{};
-  pa.sched = chunk_sched_args(ws, w.chunk, p->num_heads, p->num_tokens, pairs, fp8);
+  if (w.few) {
+    pa.few = 1;
+    pa.sched.hdr = reinterpret_cast<uint32_t*>(ws);
+    pa.sched.cta_first = reinterpret_cast<int32_t*>(ws + w.decode.cta_off);
+    pa.sched.split_list = reinterpret_cast<int4*>(ws + w.decode.split_off);
+    pa.sched.units = reinterpret_cast<ChunkUnit*>(ws + w.decode.units_off);
+    pa.sched.H = p->num_heads;
+    pa.sched.workers = nsm;
+    pa.sched.setup = 4;                    // as the decode scheduler's
+    pa.batch_info = reinterpret_cast<int4*>(ws + w.decode.batch_off);
+    pa.out = static_cast<__nv_bfloat16*>(out);
+    pa.lse = lse;
+  } else {
+    pa.sched = chunk_sched_args(ws, w.chunk, p->num_heads, p->num_tokens, pairs, fp8);
+  }
   pa.selected = selected;
   pa.block_table = block_table;
   pa.seq_lens = seq_lens;
@@ -953,6 +1031,7 @@ MLA_EXPORT mla_status mla_sparse_attention(const mla_sparse_params* p, const voi
   pa.max_len = (int)std::min<int64_t>((int64_t)p->max_blocks_per_seq * p->page_size, p->max_seq_len);
   pa.causal = p->causal;
   pa.words = (blocks_of(pa.max_len, p->block_size) + 31) / 32;
+  if (w.few) return sparse_few(p, pa, q, kv_cache, softmax_scale, kv_scale, out, lse, ws, w, nsm, s);
   ChunkArgs ca;
   std::memset(&ca, 0, sizeof(ca));
   // to the attention kernel a block is a page, and a token a sequence whose pages are its selected blocks

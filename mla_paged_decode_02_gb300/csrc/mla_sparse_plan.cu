@@ -9,8 +9,9 @@
 // given twice counts once.
 //
 // Then the tokens' keys are shared out. A token's H rows are ceil(H / 128) blocks of up to 128 rows with
-// equally many tiles of 256 keys; laid end to end, X set-up positions and the tiles for each, worker c
-// (a CTA pair) takes positions [c q, (c + 1) q), q = ceil(all / workers). A block that a boundary cuts
+// equally many tiles of 256 keys (for the decode kernel one block, and tiles of 128); laid end to end, X
+// set-up positions and the tiles for each, worker c (a CTA pair; an SM) takes positions [c q, (c + 1) q),
+// q = ceil(all / workers). A block that a boundary cuts
 // becomes one unit per worker. (The partition of the chunk scheduler, without its search for the
 // sequence of a block: here a block's number says which token it belongs to.) Where a share holds six
 // blocks or more, blocks stay whole and go to the worker in whose share their middle lies: a worker then
@@ -31,10 +32,18 @@ namespace {
 constexpr int kRoom = 220 * 1024;          // shared memory for lengths and sets
 constexpr int kPlanLens = 8192;            // tokens whose lengths fit the first CTA's shared memory
 
-__device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kChunkTile - 1) / kChunkTile : 1; }
+// tiles of 256 keys (a block that sees no key has one, in which its zeros are written), or of 128 for the
+// decode kernel, which has no part in a token without keys
+template <bool kFew>
+__device__ __forceinline__ int tiles_of(int len) {
+  if (kFew) return (len + kTileTokens - 1) / kTileTokens;
+  return len > 0 ? (len + kChunkTile - 1) / kChunkTile : 1;
+}
 
 }  // namespace
 
+// kFew: for the decode kernel (up to 16 rows), else for the chunk attention's.
+template <bool kFew>
 __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePlanArgs a, int warps) {
   extern __shared__ int32_t plan_smem[];   // [T <= kPlanLens] lengths, then [warps][words] sets
   __shared__ int64_t scan_tmp[32];
@@ -50,6 +59,7 @@ __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePla
   for (int b = rank * kSchedThreads + tid; b < a.B; b += kPlanCtas * kSchedThreads)
     bad |= ragged_errors(a.cu_q, a.seq_lens, b, a.T, a.max_len);
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  bool none = false;                       // a token of this warp's has no key
   const uint32_t lens_of_first = map_to_rank(smem_u32(plan_smem), 0);
   if (warp < warps) {
     uint32_t* set = reinterpret_cast<uint32_t*>(plan_smem) + (near ? a.T : 0) + (size_t)warp * a.words;
@@ -126,21 +136,31 @@ __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePla
         const int len = total * a.block - (nb > 0 && top == nb - 1 ? nb * a.block - seen : 0);
         if (near) st_cluster_u32(lens_of_first + 4 * t, (uint32_t)len);
         else a.lens[t] = len;
+        if (kFew) a.batch_info[t] = make_int4(0, 0, len, 0);
       }
+      none |= total == 0;
     }
   }
   bad = (__syncthreads_or((bad & MLA_DEVERR_CU_Q) != 0) ? MLA_DEVERR_CU_Q : 0u) |
         (__syncthreads_or((bad & MLA_DEVERR_SEQ_LEN) != 0) ? MLA_DEVERR_SEQ_LEN : 0u) |
         (__syncthreads_or((bad & MLA_DEVERR_BLOCK_TABLE) != 0) ? MLA_DEVERR_BLOCK_TABLE : 0u);
-  if (tid == 0) st_cluster_u32(map_to_rank(smem_u32(flags_s + rank), 0), bad);
+  if (tid < kPlanCtas) st_cluster_u32(map_to_rank(smem_u32(flags_s + rank), tid), bad);
   const int first = a.cu_q[0], last = a.cu_q[a.B];
   cluster_sync();                          // tables, lengths and flags of all CTAs
-  if (rank != 0) return;
-
   const ChunkSchedArgs& s = a.sched;
   bad = 0;
 #pragma unroll
   for (int i = 0; i < kPlanCtas; ++i) bad |= flags_s[i];
+  if (kFew && none && (bad & MLA_DEVERR_CU_Q) == 0) {
+    // tokens without keys get their results here
+    for (int t = rank + kPlanCtas * warp; t < a.T; t += kPlanCtas * warps) {
+      if (t < first || t >= last || a.batch_info[t].z != 0) continue;
+      uint4* out = reinterpret_cast<uint4*>(a.out + (int64_t)t * s.H * kDV);
+      for (int i = lane; i < s.H * (kDV / 8); i += 32) out[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (int i = lane; i < s.H; i += 32) a.lse[(int64_t)t * s.H + i] = -INFINITY;
+    }
+  }
+  if (rank != 0) return;
   if (tid == 0) s.hdr[0] = bad;
   // offsets that do not ascend within the rows of q: nothing is computed
   if ((bad & MLA_DEVERR_CU_Q) != 0 || last <= first) {
@@ -148,16 +168,19 @@ __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePla
     if (tid == 0) s.hdr[1] = s.hdr[2] = s.hdr[3] = s.hdr[4] = 0;
     return;
   }
-  const int G = (s.H + kChunkRows - 1) / kChunkRows;     // blocks of a token
+  const int G = kFew ? 1 : (s.H + kChunkRows - 1) / kChunkRows;   // blocks of a token
   auto len_of = [&](int t) { return near ? plan_smem[t] : a.lens[t]; };
   // a thread takes neighbouring tokens
   const int tokens = last - first, chunk = (tokens + kSchedThreads - 1) / kSchedThreads;
   const int t0 = first + min(tokens, tid * chunk), t1 = min(last, t0 + chunk);
-  int64_t mine = 0;
-  for (int t = t0; t < t1; ++t) mine += tiles_of(len_of(t));
+  int64_t mine = 0;                        // tokens with tiles << 40 | tiles
+  for (int t = t0; t < t1; ++t) {
+    const int n = tiles_of<kFew>(len_of(t));
+    mine += n > 0 ? ((int64_t)1 << 40) + n : 0;
+  }
   int64_t all;
-  const int64_t before = block_exclusive_scan(mine, scan_tmp, &all) * G;
-  const int64_t W = all * G, S = (int64_t)tokens * G;
+  const int64_t before = block_exclusive_scan(mine, scan_tmp, &all), kTiles = ((int64_t)1 << 40) - 1;
+  const int64_t W = (all & kTiles) * G, S = (all >> 40) * G;
   // X is dropped when a worker's share would be too small for it (q <= 2 X): then every worker's range
   // holds at least one tile
   int X = s.setup;
@@ -166,10 +189,22 @@ __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePla
     X = 0;
     q = (W + s.workers - 1) / s.workers;
   }
+  if (q == 0) q = 1;                       // (no keys at all)
   const bool small = W + S * X + q < (int64_t)1 << 31;   // (64-bit divisions are several times as long)
   auto worker_of = [&](int64_t p) -> int64_t { return small ? (int64_t)((uint32_t)p / (uint32_t)q) : p / q; };
-  const int64_t pos0 = before + (int64_t)(t0 - first) * G * X;
-  if (q >= 6 * (int64_t)(tiles_of(a.width * a.block) + X)) {
+  const int64_t pos0 = (before & kTiles) * G + (before >> 40) * G * X;
+  // a unit: tiles [tb, te) of block g of token t, for the attention kernels
+  auto put_unit = [&](int64_t unit, int t, int g, int len, int tb, int te, int slot) {
+    if (kFew) {
+      reinterpret_cast<int4*>(s.units)[unit] = make_int4(t, 0, tb | (te << 16), slot);
+    } else {
+      const int r0 = g * kChunkRows;
+      int4* u = reinterpret_cast<int4*>(s.units + unit);
+      u[0] = make_int4(t, (int32_t)((int64_t)t * s.H + r0), r0, len > 0 ? tb | (te << 16) : 0);
+      u[1] = make_int4(slot, len, len, min(kChunkRows, s.H - r0));
+    }
+  };
+  if (q >= 6 * (int64_t)(tiles_of<kFew>(a.width * a.block) + X)) {
     for (int c = tid; c <= s.workers; c += kSchedThreads) s.cta_first[c] = (int32_t)S;
     if (tid == 0) {
       s.hdr[1] = (uint32_t)S;
@@ -178,19 +213,19 @@ __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePla
       s.hdr[4] = (uint32_t)X;
     }
     __syncthreads();
-    int64_t pos = pos0, last_worker = -1;
-    if (t0 > first && t0 < t1) {
-      const int n = tiles_of(len_of(t0 - 1));
+    int64_t pos = pos0, unit = (before >> 40) * G, last_worker = -1;
+    // the worker of the block before (of the last token before that has tiles)
+    for (int t = t0 - 1; t >= first && t0 < t1; --t) {
+      const int n = tiles_of<kFew>(len_of(t));
+      if (n == 0) continue;
       last_worker = worker_of(pos0 - (X + n) + (X + n) / 2);
+      break;
     }
     for (int t = t0; t < t1; ++t) {
-      const int len = len_of(t), n = tiles_of(len);
-      for (int g = 0; g < G; ++g) {
-        const int64_t c = worker_of(pos + (X + n) / 2), unit = (int64_t)(t - first) * G + g;
-        const int r0 = g * kChunkRows, rows = min(kChunkRows, s.H - r0);
-        int4* u = reinterpret_cast<int4*>(s.units + unit);
-        u[0] = make_int4(t, (int32_t)((int64_t)t * s.H + r0), r0, (len > 0 ? n : 0) << 16);
-        u[1] = make_int4(-1, len, len, rows);
+      const int len = len_of(t), n = tiles_of<kFew>(len);
+      for (int g = 0; g < G && n > 0; ++g, ++unit) {
+        const int64_t c = worker_of(pos + (X + n) / 2);
+        put_unit(unit, t, g, len, 0, n, -1);
         if (c != last_worker) s.cta_first[c] = (int32_t)unit;
         last_worker = c;
         pos += X + n;
@@ -200,8 +235,8 @@ __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePla
   }
   int64_t pos = pos0, mine3 = 0;           // units << 32 | cut blocks << 16 | partial slots (as the chunk scheduler)
   for (int t = t0; t < t1; ++t) {
-    const int n = tiles_of(len_of(t));
-    for (int g = 0; g < G; ++g) {
+    const int n = tiles_of<kFew>(len_of(t));
+    for (int g = 0; g < G && n > 0; ++g) {
       const int64_t ts = pos + X, ns = worker_of(ts + n - 1) - worker_of(ts) + 1;
       mine3 += (ns << 32) + (ns >= 2 ? (1 << 16) + ns : 0);
       pos = ts + n;
@@ -215,21 +250,20 @@ __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePla
   __syncthreads();
   pos = pos0;
   for (int t = t0; t < t1; ++t) {
-    const int len = len_of(t), n = tiles_of(len);
-    for (int g = 0; g < G; ++g) {
+    const int len = len_of(t), n = tiles_of<kFew>(len);
+    for (int g = 0; g < G && n > 0; ++g) {
       const int64_t pre = pos, ts = pos + X, c0 = worker_of(ts);
       const int ns = (int)(worker_of(ts + n - 1) - c0 + 1);
-      const int r0 = g * kChunkRows, rows = min(kChunkRows, s.H - r0);
-      const int32_t row0 = (int32_t)((int64_t)t * s.H + r0);
-      if (ns >= 2) s.split_list[split++] = make_int4(row0, rows, ns, (int)slot);
+      if (ns >= 2) {
+        const int r0 = g * kChunkRows;
+        s.split_list[split++] = kFew ? make_int4(t, 0, ns, (int)slot)
+                                     : make_int4((int32_t)((int64_t)t * s.H + r0), min(kChunkRows, s.H - r0), ns, (int)slot);
+      }
       for (int k = 0; k < ns; ++k) {
         const int64_t c = c0 + k;
         const int64_t p0 = ts > c * q ? ts : c * q;
         const int64_t p1 = ts + n < (c + 1) * q ? ts + n : (c + 1) * q;
-        const int tb = (int)(p0 - ts), te = len > 0 ? (int)(p1 - ts) : 0;
-        int4* u = reinterpret_cast<int4*>(s.units + unit);
-        u[0] = make_int4(t, row0, r0, tb | (te << 16));
-        u[1] = make_int4(ns >= 2 ? (int)slot + k : -1, len, len, rows);
+        put_unit(unit, t, g, len, (int)(p0 - ts), (int)(p1 - ts), ns >= 2 ? (int)slot + k : -1);
         // the worker's first unit: its range starts at this piece, or inside this block's set-up
         if (p0 == c * q || (k == 0 && pre <= c * q)) s.cta_first[c] = (int32_t)unit;
         ++unit;
@@ -247,7 +281,8 @@ __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePla
 }
 
 cudaError_t sparse_plan_prepare() {
-  return cudaFuncSetAttribute(sparse_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
+  const cudaError_t e = cudaFuncSetAttribute(sparse_plan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(sparse_plan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
 }
 
 cudaError_t launch_sparse_plan(const SparsePlanArgs& a, cudaStream_t s) {
@@ -270,7 +305,8 @@ cudaError_t launch_sparse_plan(const SparsePlanArgs& a, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, sparse_plan_kernel, a, warps);
+  return a.few ? cudaLaunchKernelEx(&cfg, sparse_plan_kernel<true>, a, warps)
+               : cudaLaunchKernelEx(&cfg, sparse_plan_kernel<false>, a, warps);
 }
 
 }  // namespace mla

@@ -33,6 +33,9 @@ CASES = [
     ([(2, 600)], 300, 64, 64, 4, True, 0, 0),
     ([(20, 333)], 3, 48, 48, 20, True, 0, 0),               # lists longer than the context
     ([(7, 500)], 33, 200, 40, 6, True, 1, 0),
+    ([(5, 3), (2, 200), (0, 9), (3, 700)], 16, 64, 64, 3, True, 2, 1),
+    ([(300, 400)], 7, 128, 64, 2, True, 1, 0),
+    ([(1, 5000), (2, 3000)], 9, 128, 128, 20, True, 0, 0),
 ]
 
 
@@ -44,21 +47,22 @@ def test_sparse_matches_float64(lens, H, P, block, K, causal, pad, lead, kv):
     c.check()
 
 
+@pytest.mark.parametrize("P", [16, 64])
 @pytest.mark.parametrize("kv", [BF, F8])
-def test_lists_are_sets(kv):
+def test_lists_are_sets(kv, P):
     """Any order, repetitions, negative numbers, blocks past the context, empty lists, and lists whose
     blocks a token does not see yet."""
-    lens = [(4, 300), (3, 130)]
+    lens = [(4, 300 * P // 16), (3, 8 * P + 2)]
     big = 1 << 30
     lists = [[3, 0, 7, 3, 3, 0], [18, 1, -5, big, -big - 1, 2], [-1] * 6, [big] * 6, [8, 8, 8, 8, 8, 8], [0, 8, 9, 10, -1, 4],
              [8, 7, 6, 5, 4, 3]]
-    c = SparseCase(lens, 16, 16, 16, 6, kv, seed=5, selected=lists)
+    c = SparseCase(lens, 16, P, P, 6, kv, seed=5, selected=lists)
     c.run()
     c.check()
     assert math.isinf(c.lse[2, 0].item()) and math.isinf(c.lse[3, 0].item())
-    # sequence 1 sees 128, 129 and 130 keys: its first token does not see block 8
+    # sequence 1 sees 8 P, 8 P + 1 and 8 P + 2 keys: its first token does not see block 8
     assert math.isinf(c.lse[4, 0].item()) and not math.isinf(c.lse[5, 0].item())
-    again = SparseCase(lens, 16, 16, 16, 6, kv, seed=5, selected=[sorted(r, reverse=True) for r in lists])
+    again = SparseCase(lens, 16, P, P, 6, kv, seed=5, selected=[sorted(r, reverse=True) for r in lists])
     again.run()
     torch.cuda.synchronize()
     assert torch.equal(again.out, c.out) and torch.equal(again.lse, c.lse)
@@ -100,12 +104,12 @@ def test_many_tokens_and_sequences():
     c.check(list(range(0, 700, 23)))
 
 
-@pytest.mark.parametrize("kv", [BF, F8])
-def test_whole_blocks_of_many_tokens(kv):
+@pytest.mark.parametrize("kv,H", [(BF, 130), (F8, 130), (F8, 16)])
+def test_whole_blocks_of_many_tokens(kv, H):
     """Shares of six row blocks or more are not cut; lists of all lengths, rows that see nothing among them."""
     rng = np.random.default_rng(3)
-    lens = [(400, 900), (0, 30), (300, 250), (37, 37), (200, 2000)]
-    c = SparseCase(lens, 130, 64, 32, 3, kv, seed=12, pad=5, lead=3)
+    lens = [(400, 900), (0, 30), (300, 250), (37, 37), (1500 if H == 16 else 200, 2000)]
+    c = SparseCase(lens, H, 64, 64 if H == 16 else 32, 3, kv, seed=12, pad=5, lead=3)
     c.selected[::7] = -1
     c.selected[5] = torch.tensor([2, 1, 0])
     c.run()
@@ -173,9 +177,10 @@ def test_a_long_context():
         assert (lse[i].double() - torch.logsumexp(s, dim=1)).abs().max() <= 1e-4
 
 
-def test_device_errors():
+@pytest.mark.parametrize("kv,P", [(BF, 16), (F8, 64)])
+def test_device_errors(kv, P):
     def run(**change):
-        c = SparseCase([(2, 100), (1, 64)], 8, 16, 16, 7, seed=4, pad=2)
+        c = SparseCase([(2, 100 * P // 16), (1, 64)], 8, P, P, 7, kv, seed=4, pad=2)
         for k, v in change.items():
             if k == "page":
                 c.table[0, 3] = v
@@ -200,12 +205,13 @@ def test_device_errors():
     c.check()
 
 
-def test_default_buffers_streams_and_two_graphs():
-    c = SparseCase([(5, 300), (1, 90), (2, 700)], 48, 64, 32, 4, F8, seed=9)
+@pytest.mark.parametrize("H,block", [(48, 32), (16, 64)])
+def test_default_buffers_streams_and_two_graphs(H, block):
+    c = SparseCase([(5, 300), (1, 90), (2, 700)], H, 64, block, 4, F8, seed=9)
     c.run()
     torch.cuda.synchronize()
     out, lse = c.out.clone(), c.lse.clone()
-    kw = dict(max_seq_len=c.max_seq_len, block_size=32)
+    kw = dict(max_seq_len=c.max_seq_len, block_size=block)
     o, l = api.sparse_attention(*c.dev, SCALE, c.dscale, **kw)
     assert torch.equal(o, out) and torch.equal(l, lse)
     s = torch.cuda.Stream()
@@ -239,8 +245,9 @@ def test_default_buffers_streams_and_two_graphs():
     assert torch.equal(graphs[0][1][0], o) and torch.equal(graphs[0][1][1], l)
 
 
-def test_a_stalled_pipeline_times_out_and_the_next_call_is_clean():
-    c = SparseCase([(2, 300)], 16, 64, 64, 3, seed=10)
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_a_stalled_pipeline_times_out_and_the_next_call_is_clean(kv):
+    c = SparseCase([(2, 300)], 16, 64, 64, 3, kv, seed=10)
     api.test_set_hooks(20_000_000, True)
     try:
         c.run()
