@@ -27,7 +27,7 @@ struct IndexWriteArgs {
 cudaError_t launch_index_write(IndexWriteArgs a, cudaStream_t s);
 
 struct IndexScoreArgs {
-  CUtensorMap tm_q;                // [T * H rows][128] E4M3, boxes of 16 rows
+  CUtensorMap tm_q;                // [T][H][128] E4M3, boxes of 16 heads (zeros behind the last)
   CUtensorMap tm_k;                // [num_pages * P rows][128] E4M3, boxes of box_rows rows
   const float* w;                  // [T, H]
   const float* scale;              // [num_pages * P]
@@ -38,8 +38,7 @@ struct IndexScoreArgs {
   uint32_t* err;
   int32_t B, T, H, P, MB, num_pages, max_len, block, C, causal;
   int32_t box_rows, total_rows;
-  int32_t Hp, TG, sub_tokens;      // columns of a token, tokens of a group (a power of two) and of a sub-group
-  int32_t tg_log2;
+  int32_t TG, tg_log2;             // tokens of a group, a power of two
   int32_t q_rows, units, key_slots;   // rows of a query buffer, query buffers, tiles of keys in shared memory
   int32_t unit_blocks;             // blocks of a unit
   uint32_t block_inv;              // 2^32 / block, rounded up

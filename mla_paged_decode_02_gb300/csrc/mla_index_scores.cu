@@ -7,8 +7,8 @@
 // Keys on M. A tile is 128 keys (A, 128 bytes each) against the heads of a few tokens of one sequence
 // (B, up to 128 rows of 128 bytes): four E4M3 MMAs of K = 32, exact products, float32 sums in tensor
 // memory, a key in each lane and a head in each column. So the sum over heads stays in a thread, w_h is the
-// same for all lanes, and only the maximum over a block's keys crosses lanes. A token's heads start
-// at a multiple of 16 columns; the columns between hold whatever follows in memory and are never read.
+// same for all lanes, and only the maximum over a block's keys crosses lanes. A token takes 16, 32, 64 or
+// 128 columns; those without a head have queries and weights of zero.
 //
 // Work is cut into units of one group of up to TG neighbouring tokens x `unit_blocks` blocks, as far as the
 // context goes; persistent CTAs, one per SM, take them in turn. Units are numbered by sequence and, within
@@ -63,13 +63,7 @@ __device__ __forceinline__ int ordered(float x) {
 __device__ __forceinline__ float from_ordered(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7FFFFFFF); }
 constexpr int kLowest = (int)0x807FFFFFu;         // ordered(-inf)
 
-// max(0, x) that keeps a NaN
-__device__ __forceinline__ float positive(float x) {
-  float y;
-  asm volatile("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
-  return y;
-}
-// Two values to an instruction: acc = w max(0, (x, y)) + (first ? 0 : acc). Volatile, so that it stays
+// Two values to an instruction: acc = w max(0, (x, y)) + (first ? 0 : acc), NaN kept. Volatile, so that it stays
 // behind the wait for the tensor-memory load that brings x and y.
 template <bool kFirst>
 __device__ __forceinline__ void add_positive2(uint64_t& acc, float x, float y, uint64_t w) {
@@ -183,11 +177,10 @@ __device__ uint32_t g_unreported;                 // error bits of calls without
 
 }  // namespace
 
-// CPT: 32-column chunks of a token, whose 32 CPT heads fill them; 0: any number of heads, 16 columns at a
-// time.
-template <int CPT>
+// A token's heads take PT chunks of CS columns, 16, 32, 64 or 128 (at least as many as heads).
+template <int CS, int PT>
 __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __grid_constant__ IndexScoreArgs a) {
-  constexpr int CS = CPT == 0 ? 16 : 32;
+  constexpr int Hp = CS * PT, kFull = kISColumns / Hp;   // columns of a token, tokens of an accumulator
   extern __shared__ uint8_t dsmem_raw[];
   __shared__ __align__(8) uint64_t bar_kfull[kISMaxSlots], bar_kempty[kISMaxSlots], bar_info[kISMaxUnits],
       bar_qfull[kISMaxUnits], bar_qempty[kISMaxUnits], bar_tfull[kISIssuers], bar_tempty[kISIssuers], bar_drain[kISIssuers], bar_never;
@@ -232,6 +225,7 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
   }
   if (warp == 1) tmem_alloc(smem_u32(&tmem_base_s), kISTmem);
   for (int i = threadIdx.x; i < units * maxima; i += kISThreads) best[i] = kLowest;
+  for (int i = threadIdx.x; i < units * q_rows; i += kISThreads) gW[i] = 0.f;   // columns without a head keep it
   griddep_wait();
   griddep_launch_dependents();
   tc_fence_before();
@@ -242,7 +236,8 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
     return __all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, kISFirstWaitNs) ||
                                        wait_longer(bar, parity, smem_u32(&abort_s), err, a.wait_limit_ns));
   };
-  const int TG = a.TG, Hp = a.Hp, sub_tokens = a.sub_tokens;
+  constexpr int sub_tokens = kFull;
+  const int TG = a.TG;
 
   if (warp == 0) {
     // ---------------------------------------------------------------------- units and their queries
@@ -360,8 +355,8 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
           }
           __syncwarp();
           for (int i = lane; i < qboxes; i += 32)
-            tma_load_2d(sQ + ub * q_rows * kDIndex + i * 16 * kDIndex, &a.tm_q, b_qfull + 8 * ub, 0,
-                        (ut0 + i / (Hp / 16)) * a.H + (i % (Hp / 16)) * 16);
+            tma_load_3d(sQ + ub * q_rows * kDIndex + i * 16 * kDIndex, &a.tm_q, b_qfull + 8 * ub, 0,
+                        (i % (Hp / 16)) * 16, ut0 + i / (Hp / 16));
           ++nu;
           if (++ub == (uint32_t)units) { ub = 0; uph ^= 1; }
         }
@@ -527,7 +522,6 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
     uint32_t nt = 0, n = 0, taken = 0;                  // tiles and products so far, products of this pair
     bool ok = !(a.test_stall && !wait(b_never, 0));
     const bool whole = a.block % 32 == 0;               // a warp's keys lie in one block
-    const int H = a.H;
     for (uint32_t qb = 0, qph = 0; ok; qb + 1 == (uint32_t)units ? (qb = 0, qph ^= 1) : ++qb) {
       ok = wait(b_qfull + 8 * qb, qph);
       if (!ok) break;
@@ -577,46 +571,25 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
           }
         };
         uint64_t s[4];
-        if (CPT == 0) {
+        // (the warps of a scheduler cover each other's loads: a second buffer changes nothing)
+        auto token = [&](int i) {
           float v[CS];
-          for (int i = 0; i < toks; ++i) {
-            s[0] = s[1] = s[2] = s[3] = 0ull;
-            float rest = 0.f;
-            for (int c = 0; c < H; c += CS) {
-              load_heads<CS>(acc + i * Hp + c, v);
-              tmem_wait_ld();
-              if (c + CS <= H) {
-                add_heads<CS, false>(v, w + i * Hp + c, s);
-              } else {
 #pragma unroll
-                for (int k = 0; k < CS; ++k)
-                  if (c + k < H) rest = fmaf(positive(v[k]), w[i * Hp + c + k], rest);
-              }
-            }
-            finish(i, sum8(s) + rest);
+          for (int c = 0; c < PT; ++c) {
+            const int at = (i * PT + c) * CS;
+            load_heads<CS>(acc + at, v);
+            tmem_wait_ld();
+            if (c + 1 == PT && i + 1 == toks) release();
+            if (c == 0) add_heads<CS, true>(v, w + at, s);
+            else add_heads<CS, false>(v, w + at, s);
           }
-          release();
+          finish(i, sum8(s));
+        };
+        if (toks == kFull) {
+#pragma unroll
+          for (int i = 0; i < kFull; ++i) token(i);
         } else {
-          // (the warps of a scheduler cover each other's loads: a second buffer changes nothing)
-          auto token = [&](int i) {
-            float v[CS];
-#pragma unroll
-            for (int c = 0; c < CPT; ++c) {
-              const int at = (i * CPT + c) * CS;
-              load_heads<CS>(acc + at, v);
-              tmem_wait_ld();
-              if (c + 1 == CPT && i + 1 == toks) release();
-              if (c == 0) add_heads<CS, true>(v, w + at, s);
-              else add_heads<CS, false>(v, w + at, s);
-            }
-            finish(i, sum8(s));
-          };
-          if (toks * CPT == 4) {
-#pragma unroll
-            for (int i = 0; i < 4 / (CPT > 0 ? CPT : 1); ++i) token(i);
-          } else {
-            for (int i = 0; i < toks; ++i) token(i);
-          }
+          for (int i = 0; i < toks; ++i) token(i);
         }
         if (whole && lane < toks && keep > -INFINITY) atomicMax(to + lane * a.unit_blocks, ordered(keep));
       }
@@ -634,7 +607,8 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
 }
 
 cudaError_t index_scores_prepare() {
-  for (auto* kernel : {index_scores_kernel<0>, index_scores_kernel<1>, index_scores_kernel<2>, index_scores_kernel<4>}) {
+  for (auto* kernel : {index_scores_kernel<16, 1>, index_scores_kernel<32, 1>, index_scores_kernel<32, 2>,
+                       index_scores_kernel<32, 4>}) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kISSmem);
     if (e != cudaSuccess) return e;
   }
@@ -642,15 +616,16 @@ cudaError_t index_scores_prepare() {
 }
 
 cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s) {
-  a.Hp = (a.H + 15) / 16 * 16;
-  a.sub_tokens = kISColumns / a.Hp;
+  int Hp = 16;
+  while (Hp < a.H) Hp *= 2;
+  const int sub_tokens = kISColumns / Hp;
   // tokens to a group: as many as sequences have on average (a power of two), up to four sub-groups
-  const int most_tokens = 2 * kISIssuers * a.sub_tokens;
+  const int most_tokens = 2 * kISIssuers * sub_tokens;
   a.tg_log2 = 0;
   while ((1 << a.tg_log2) < a.T / a.B && (1 << a.tg_log2) < most_tokens) ++a.tg_log2;
   a.TG = 1 << a.tg_log2;
-  const bool many = a.TG > a.sub_tokens;
-  a.q_rows = a.TG * a.Hp;
+  const bool many = a.TG > sub_tokens;
+  a.q_rows = a.TG * Hp;
   // a unit: whole blocks and whole tiles, 512 to 8192 keys, about 24 units to a CTA (6 of a decode step)
   int lcm = a.block;
   while (lcm % kISKeys != 0) lcm += a.block;
@@ -680,10 +655,10 @@ cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return a.H == 32    ? cudaLaunchKernelEx(&cfg, index_scores_kernel<1>, a)
-         : a.H == 64  ? cudaLaunchKernelEx(&cfg, index_scores_kernel<2>, a)
-         : a.H == 128 ? cudaLaunchKernelEx(&cfg, index_scores_kernel<4>, a)
-                      : cudaLaunchKernelEx(&cfg, index_scores_kernel<0>, a);
+  return Hp == 16   ? cudaLaunchKernelEx(&cfg, index_scores_kernel<16, 1>, a)
+         : Hp == 32 ? cudaLaunchKernelEx(&cfg, index_scores_kernel<32, 1>, a)
+         : Hp == 64 ? cudaLaunchKernelEx(&cfg, index_scores_kernel<32, 2>, a)
+                    : cudaLaunchKernelEx(&cfg, index_scores_kernel<32, 4>, a);
 }
 
 }  // namespace mla
