@@ -340,8 +340,9 @@ typedef struct mla_index_params {
  *   scores        [T, C] float32
  *   device_error  optional device uint32 into which MLA_DEVERR_CU_Q (offsets that do not ascend:
  *                 what is written is undefined, but within the T rows), MLA_DEVERR_SEQ_LEN (the
- *                 length is clamped) and MLA_DEVERR_BLOCK_TABLE (page 0 is read) are OR-ed
- * No synchronisation. */
+ *                 length is clamped), MLA_DEVERR_BLOCK_TABLE (page 0 is read) and
+ *                 MLA_DEVERR_TIMEOUT (a stalled pipeline: scores are missing) are OR-ed
+ * One launch on `stream`; no synchronisation. */
 mla_status mla_index_scores(const mla_index_params* p, const void* q_index, const float* q_weights,
                             const void* index_cache, const float* index_scale,
                             const int32_t* block_table, const int32_t* seq_lens,

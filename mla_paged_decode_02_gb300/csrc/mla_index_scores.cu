@@ -22,6 +22,16 @@
 // pair of accumulators of 128 columns: two sub-groups of a tile, or two tiles of one; four warpgroups take
 // an accumulator each. The maxima of a unit's blocks gather in shared memory. Every wait is bounded; a stall
 // sets the error word, and the CTA drains and leaves.
+//
+// What bounds it. Many tokens: the sums. 32 columns of 128 keys take a scheduler's four warps 58 instructions
+// and 90 clocks each at best (a loop apart: 73 without max, 58 without the tensor-memory loads), the MMAs 64;
+// with maxima, waits and bookkeeping it is 103 instructions and about 145 clocks. 2048 tokens x 64 heads
+// over 24 K keys 413 us (2.1 PFLOP/s of E4M3; 34% of tensor cycles). On the way there: one issuing warp held
+// back everything (546 us for four warpgroups, its products of 128 columns take it 570 clocks), two of them
+// 490, products of 256 columns 457; a chunk more of double buffering or a quarter of max on the FMA pipe, 3%.
+// Few tokens: latency and the loading warp. 121 sequences x 4 K keys 21.5 us for 65 MB, of which 7 us pass
+// before the first product and after the last; with one warp for units and keys 32, with keys' scales as bulk
+// copies 24 (each takes the warp about 95 clocks to issue, like a key box).
 #include "mla_index.h"
 #include "mla_ptx.cuh"
 #include "mla_ragged.cuh"

@@ -9,6 +9,7 @@
 // that is not finite gets a NaN scale. (A division for each value instead of one for the row: 41 us against
 // 23 for 4096 tokens x 64 heads.)
 //
+// Memory bound at many tokens (4096 x 64 heads 23.4 us for 103 MB, 4.4 TB/s; 128 x 64 heads 2.3 us, latency).
 // Bytes: 256 in and 132 out per row. Eight lanes share a row (16 values each: the first four lanes the
 // fixed half, the others eight pairs); a warp takes four tokens' keys, or 4 or 8 heads of a token.
 #include <cuda_fp8.h>

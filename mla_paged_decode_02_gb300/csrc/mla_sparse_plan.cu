@@ -20,7 +20,8 @@
 //
 // One cluster of eight CTAs: a warp takes a token at a time and sends its length to the first CTA's shared
 // memory, where the partition is made. Bound by latency: the list, lengths and offsets are read at once,
-// then the page numbers; after a cluster barrier two scans.
+// then the page numbers; after a cluster barrier two scans (6.5 us for 2 to 64 tokens, 10 for 512; a single CTA
+// for few tokens is no faster).
 #include "mla_index.h"
 #include "mla_ptx.cuh"
 #include "mla_ragged.cuh"

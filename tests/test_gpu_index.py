@@ -187,6 +187,16 @@ def test_scores_of_short_contexts_under_a_long_limit():
     c.check()
 
 
+def test_scores_with_weights_between_16_byte_boundaries():
+    c = ScoreCase([(3, 400)], 64, 64, 64, seed=8)
+    c.run()
+    shifted = torch.empty(c.w.numel() + 1, device="cuda")[1:].view(c.w.shape)
+    shifted.copy_(c.w)
+    assert shifted.data_ptr() % 16 == 4
+    got = api.index_scores(c.dev[0], shifted, *c.dev[2:], max_seq_len=c.max_seq_len, block_size=64)
+    assert torch.equal(got, c.out)
+
+
 def test_scores_of_calls_at_once():
     cases = [ScoreCase([(60, 900), (1, 2000)], 64, 64, 64, seed=20 + i) for i in range(3)]
     for c in cases:
