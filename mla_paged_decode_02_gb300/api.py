@@ -730,7 +730,9 @@ def sparse_attention(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch
     if workspace is not None and not workspace.is_contiguous():     # its size is taken from its elements
         raise ValueError("workspace must be contiguous")
     scale = kv_scale if kvd == KV_FP8_E4M3 else None
-    params = make_sparse_params(B, T, H, P, Np, block_table.shape[1], max_seq_len, block_size, shape[1], kvd, causal)
+    if max_seq_len > _I32_MAX or block_size > _I32_MAX:
+        raise ValueError("max_seq_len and block_size must fit 32 bits")
+    params = SparseParams(B, T, H, P, Np, block_table.shape[1], max_seq_len, block_size, shape[1], kvd, 1 if causal else 0)
     handle, at = _addresses(stream, q, kv_cache, block_table, seq_lens, cu_q_lens, selected, scale, out, lse, workspace)
     if out is None:
         out = _allocated(stream, (T, H, D_V), torch.bfloat16, q.device)

@@ -259,11 +259,15 @@ def test_a_stalled_pipeline_times_out_and_the_next_call_is_clean(kv):
     c.check()
 
 
-def test_no_tokens():
-    c = SparseCase([(0, 100), (0, 0)], 16, 64, 64, 3, seed=11)
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_no_tokens_and_no_blocks(kv):
+    c = SparseCase([(0, 100), (0, 0)], 16, 64, 64, 3, kv, seed=11)
     c.run()
     torch.cuda.synchronize()
     assert api.decode_check(c.workspace) == (0, 0)
+    c = SparseCase([(3, 100), (2, 0), (1, 64)], 16, 64, 64, 3, kv, seed=11, pad=1, selected=[[-1, 9, -7]] * 7)
+    c.run()
+    c.check()
 
 
 # --------------------------------------------------------------- the operators as they are used
