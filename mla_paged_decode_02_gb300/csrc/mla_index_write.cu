@@ -9,9 +9,9 @@
 // that is not finite gets a NaN scale. (A division for each value instead of one for the row: 41 us against
 // 23 for 4096 tokens x 64 heads.)
 //
-// Memory bound at many tokens (4096 x 64 heads 23.4 us for 103 MB, 4.4 TB/s; 128 x 64 heads 2.3 us, latency).
-// Bytes: 256 in and 132 out per row. Eight lanes share a row (16 values each: the first four lanes the
-// fixed half, the others eight pairs); a warp takes four tokens' keys, or 4 or 8 heads of a token.
+// Memory bound at many tokens (4096 x 64 heads 21.7 us for 103 MB, 4.7 TB/s; 128 x 64 heads 2.1 us, latency).
+// Bytes: 256 in and 132 out per row. Eight lanes share a row (eight values of the fixed half and eight of
+// the turned one each); a warp takes four tokens' keys, or 4 or 16 heads of a token.
 #include <cuda_fp8.h>
 #include "mla_index.h"
 #include "mla_ptx.cuh"
@@ -57,19 +57,22 @@ __device__ __forceinline__ float max_nan(float x, float y) {
   return r;
 }
 
-// The row of lane group lane / 8, of which this lane holds two 16-byte units (u0, u1) as v: turned,
-// and its largest magnitude m as above (NaN if a value is not finite). x receives the 16 values.
-__device__ __forceinline__ float row_max(const uint4* v, int p, bool turned, bool interleaved, const float* c,
-                                           const float* s, float* x) {
+// The row of lane group lane / 8, of which this lane holds eight fixed values (v[0]) and eight to be turned
+// (v[1]): x receives them all, turned, and the largest magnitude m as above is returned (NaN if a value of
+// the row is not finite). Pairs are neighbours, or their members four lanes apart.
+__device__ __forceinline__ float row_max(const uint4* v, bool interleaved, bool second, const float* c, const float* s,
+                                         float* x) {
   unpack8(v[0], x);
   unpack8(v[1], x + 8);
-  if (turned) {
-    if (interleaved) {
+  if (interleaved) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) turn(x[2 * k], x[2 * k + 1], c[k], s[k]);
-    } else {
+    for (int k = 0; k < 4; ++k) turn(x[8 + 2 * k], x[9 + 2 * k], c[k], s[k]);
+  } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) turn(x[k], x[8 + k], c[k], s[k]);
+    for (int k = 0; k < 8; ++k) {
+      const float other = __shfl_xor_sync(0xffffffffu, x[8 + k], 4);
+      const float u = __fmul_rn(x[8 + k], c[k]), w = __fmul_rn(other, s[k]);
+      x[8 + k] = second ? __fadd_rn(u, w) : __fsub_rn(u, w);
     }
   }
   float m = 0.f;
@@ -84,7 +87,7 @@ __device__ __forceinline__ float row_max(const uint4* v, int p, bool turned, boo
 
 // kIter: heads of a query task / 4.
 template <int kIter>
-__global__ void __launch_bounds__(256, 4) index_write_kernel(IndexWriteArgs a) {
+__global__ void __launch_bounds__(256, 3) index_write_kernel(IndexWriteArgs a) {
   const int lane = threadIdx.x & 31, group = lane >> 3;
   const int64_t task = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int64_t key_tasks = (a.n + 3) / 4;
@@ -102,42 +105,40 @@ __global__ void __launch_bounds__(256, 4) index_write_kernel(IndexWriteArgs a) {
   griddep_wait();                          // the inputs may be the work before's
   griddep_launch_dependents();
   const int64_t pos = a.positions[t];
-  const int p = lane & 3;
-  const bool turned = (lane & 4) != 0;
-  // the lane's 8-value units of the row's 16, so that four lanes read 64 and write 32 bytes in a row
-  const int u0 = (turned ? 8 : 0) + p, u1 = u0 + 4;
+  const int u = lane & 7;                              // the lane's 8-value unit of each half
+  const bool second = (u & 4) != 0;                    // its values are second members of pairs
   // the rows are on their way while the position, and then the cosines and sines, are read
   uint4 v[kIter][2];
   int64_t slot = -1;
   if (is_key) {
     slot = a.slots[t];
     const uint4* r = reinterpret_cast<const uint4*>(a.keys + t * a.key_stride);
-    v[0][0] = r[u0];
-    v[0][1] = r[u1];
+    v[0][0] = r[u];
+    v[0][1] = r[8 + u];
   } else {
     const __nv_bfloat16* src = a.queries + t * a.q_token_stride;
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
       const int h = min(h0 + 4 * i, a.H - 1);
       const uint4* r = reinterpret_cast<const uint4*>(src + h * a.q_head_stride);
-      v[i][0] = r[u0];
-      v[i][1] = r[u1];
+      v[i][0] = r[u];
+      v[i][1] = r[8 + u];
     }
   }
   const bool live = pos >= 0 && pos < a.max_pos;       // else a padding token, or one that is reported
   float c[8], s[8];
-  // their pairs: 4 p .. and 16 + 4 p .. (neighbours), or 8 p .. (32 columns apart: one of each unit)
-  const float* cs = a.cos_sin + (live ? pos : 0) * kDRope;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int pair = a.interleaved ? 16 * i + 4 * p : 8 * p + 4 * i;
-    *reinterpret_cast<float4*>(c + 4 * i) = *reinterpret_cast<const float4*>(cs + pair);
-    *reinterpret_cast<float4*>(s + 4 * i) = *reinterpret_cast<const float4*>(cs + 32 + pair);
+  // its pairs: 4 u .. (neighbours), or 8 (u mod 4) ..
+  const float* cs = a.cos_sin + (live ? pos : 0) * kDRope + (a.interleaved ? 4 * u : 8 * (u & 3));
+  *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(cs);
+  *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(cs + 32);
+  if (!a.interleaved) {
+    *reinterpret_cast<float4*>(c + 4) = *reinterpret_cast<const float4*>(cs + 4);
+    *reinterpret_cast<float4*>(s + 4) = *reinterpret_cast<const float4*>(cs + 36);
   }
   float x[16];
   uint2 q0, q1;
   if (is_key) {
-    const float m = row_max(v[0], p, turned, a.interleaved, c, s, x);
+    const float m = row_max(v[0], a.interleaved, second, c, s, x);
     if (task * 4 + group >= a.n || pos < 0) return;
     if (!live || slot >= a.total_slots) {
       if ((lane & 7) == 0 && a.err != nullptr) atomicOr(a.err, !live ? MLA_DEVERR_POSITION : MLA_DEVERR_SLOT);
@@ -146,8 +147,8 @@ __global__ void __launch_bounds__(256, 4) index_write_kernel(IndexWriteArgs a) {
     if (slot < 0) return;
     quantise16(x, __fdiv_rn(448.f, m), q0, q1);
     uint2* dst = reinterpret_cast<uint2*>(a.cache + slot * kDIndex);
-    dst[u0] = q0;
-    dst[u1] = q1;
+    dst[u] = q0;
+    dst[8 + u] = q1;
     if ((lane & 7) == 0) a.scale[slot] = __fdiv_rn(m, 448.f);
     return;
   }
@@ -155,21 +156,21 @@ __global__ void __launch_bounds__(256, 4) index_write_kernel(IndexWriteArgs a) {
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
     const int h = h0 + 4 * i;
-    const float m = row_max(v[i], p, turned, a.interleaved, c, s, x);
+    const float m = row_max(v[i], a.interleaved, second, c, s, x);
     if (h >= a.H) continue;
     quantise16(x, __fdiv_rn(448.f, m), q0, q1);
     const int64_t row = t * a.H + h;
     uint2* dst = reinterpret_cast<uint2*>(a.q_index + row * kDIndex);
-    dst[u0] = q0;
-    dst[u1] = q1;
+    dst[u] = q0;
+    dst[8 + u] = q1;
     if ((lane & 7) == 0) a.q_weights[row] = a.weights[row] * __fdiv_rn(m, 448.f);
   }
 }
 
 cudaError_t launch_index_write(IndexWriteArgs a, cudaStream_t s) {
-  // 8 heads to a warp, 4 where that would leave warps without work
+  // 16 heads to a warp (8: 22.5 us against 21.7 for 4096 tokens x 64 heads; 4: 30), 4 where that would leave warps without work
   const bool few = (int64_t)a.n * a.H <= 1 << 15;
-  const int per = few ? 4 : 8;
+  const int per = few ? 4 : 16;
   a.qtasks = a.queries != nullptr ? (a.H + per - 1) / per : 0;
   const int64_t tasks = ((int64_t)a.n + 3) / 4 + (int64_t)a.n * a.qtasks;
   cudaLaunchConfig_t cfg = {};
@@ -181,7 +182,7 @@ cudaError_t launch_index_write(IndexWriteArgs a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, index_write_kernel<1>, a) : cudaLaunchKernelEx(&cfg, index_write_kernel<2>, a);
+  return few ? cudaLaunchKernelEx(&cfg, index_write_kernel<1>, a) : cudaLaunchKernelEx(&cfg, index_write_kernel<4>, a);
 }
 
 }  // namespace mla
