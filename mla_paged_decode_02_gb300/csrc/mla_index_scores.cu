@@ -25,13 +25,14 @@
 //
 // What bounds it. Many tokens: the sums. 32 columns of 128 keys take a scheduler's four warps 58 instructions
 // and 90 clocks each at best (a loop apart: 73 without max, 58 without the tensor-memory loads), the MMAs 64;
-// with maxima, waits and bookkeeping it is 103 instructions and about 145 clocks. 2048 tokens x 64 heads
-// over 24 K keys 413 us (2.1 PFLOP/s of E4M3; 34% of tensor cycles). On the way there: one issuing warp held
+// with maxima, waits and bookkeeping it is about 97 instructions and 142 clocks. 2048 tokens x 64 heads
+// over 24 K keys 406 us (2.1 PFLOP/s of E4M3; 34% of tensor cycles). On the way there: one issuing warp held
 // back everything (546 us for four warpgroups, its products of 128 columns take it 570 clocks), two of them
 // 490, products of 256 columns 457; a chunk more of double buffering or a quarter of max on the FMA pipe, 3%.
 // Few tokens: latency and the loading warp. 121 sequences x 4 K keys 21.5 us for 65 MB, of which 7 us pass
 // before the first product and after the last; with one warp for units and keys 32, with keys' scales as bulk
 // copies 24 (each takes the warp about 95 clocks to issue, like a key box).
+#include <type_traits>
 #include "mla_index.h"
 #include "mla_ptx.cuh"
 #include "mla_ragged.cuh"
@@ -187,8 +188,9 @@ __device__ uint32_t g_unreported;                 // error bits of calls without
 
 }  // namespace
 
-// A token's heads take PT chunks of CS columns, 16, 32, 64 or 128 (at least as many as heads).
-template <int CS, int PT>
+// A token's heads take PT chunks of CS columns, 16, 32, 64 or 128 (at least as many as heads). kWhole: blocks
+// are a multiple of 32 keys, so that a warp's keys lie in one.
+template <int CS, int PT, bool kWhole>
 __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __grid_constant__ IndexScoreArgs a) {
   constexpr int Hp = CS * PT, kFull = kISColumns / Hp;   // columns of a token, tokens of an accumulator
   extern __shared__ uint8_t dsmem_raw[];
@@ -531,7 +533,6 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
     }
     uint32_t nt = 0, n = 0, taken = 0;                  // tiles and products so far, products of this pair
     bool ok = !(a.test_stall && !wait(b_never, 0));
-    const bool whole = a.block % 32 == 0;               // a warp's keys lie in one block
     for (uint32_t qb = 0, qph = 0; ok; qb + 1 == (uint32_t)units ? (qb = 0, qph ^= 1) : ++qb) {
       ok = wait(b_qfull + 8 * qb, qph);
       if (!ok) break;
@@ -564,25 +565,12 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
         const int in = tile * kISKeys + quad * 32 + lane;     // key within the unit
         const int key = I.k0 + in;
         const int toks = min(sub_tokens, ntok - t0);
-        const bool all_see = I.k0 + (tile + 1) * kISKeys <= I.seen[t0];
         const float* w = gW + qb * q_rows + t0 * Hp;
-        int* to = mine + t0 * a.unit_blocks + (int)__umulhi((uint32_t)(whole ? in - lane : in), a.block_inv);
+        int* to = mine + t0 * a.unit_blocks + (int)__umulhi((uint32_t)(kWhole ? in - lane : in), a.block_inv);
         float keep = -INFINITY;
-        auto finish = [&](int i, float x) {             // the sum of token t0 + i
-          x *= ks;
-          if (!all_see && key >= I.seen[t0 + i]) x = -INFINITY;
-          if (whole) {
-            x = warp_max(x);
-            if (lane == i) keep = x;
-          } else {
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-            if ((lane & 7) == 0 && x > -INFINITY) atomicMax(to + i * a.unit_blocks, ordered(x));
-          }
-        };
         uint64_t s[4];
         // (the warps of a scheduler cover each other's loads: a second buffer changes nothing)
-        auto token = [&](int i) {
+        auto token = [&](int i, auto masked) {
           float v[CS];
 #pragma unroll
           for (int c = 0; c < PT; ++c) {
@@ -593,15 +581,25 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
             if (c == 0) add_heads<CS, true>(v, w + at, s);
             else add_heads<CS, false>(v, w + at, s);
           }
-          finish(i, sum8(s));
-        };
-        if (toks == kFull) {
+          float x = sum8(s) * ks;
+          if (decltype(masked)::value && key >= I.seen[t0 + i]) x = -INFINITY;
+          if (kWhole) {
+            x = warp_max(x);
+            if (lane == i) keep = x;
+          } else {
 #pragma unroll
-          for (int i = 0; i < kFull; ++i) token(i);
+            for (int o = 4; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+            if ((lane & 7) == 0 && x > -INFINITY) atomicMax(to + i * a.unit_blocks, ordered(x));
+          }
+        };
+        // a full accumulator whose tokens see all keys of the tile, the usual case, has code of its own
+        if (toks == kFull && I.k0 + (tile + 1) * kISKeys <= I.seen[t0]) {
+#pragma unroll
+          for (int i = 0; i < kFull; ++i) token(i, std::false_type{});
         } else {
-          for (int i = 0; i < toks; ++i) token(i);
+          for (int i = 0; i < toks; ++i) token(i, std::true_type{});
         }
-        if (whole && lane < toks && keep > -INFINITY) atomicMax(to + lane * a.unit_blocks, ordered(keep));
+        if (kWhole && lane < toks && keep > -INFINITY) atomicMax(to + lane * a.unit_blocks, ordered(keep));
       }
       if (!ok) break;
       n += (uint32_t)products;
@@ -617,8 +615,9 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
 }
 
 cudaError_t index_scores_prepare() {
-  for (auto* kernel : {index_scores_kernel<16, 1>, index_scores_kernel<32, 1>, index_scores_kernel<32, 2>,
-                       index_scores_kernel<32, 4>}) {
+  for (auto* kernel : {index_scores_kernel<16, 1, false>, index_scores_kernel<32, 1, false>, index_scores_kernel<32, 2, false>,
+                       index_scores_kernel<32, 4, false>, index_scores_kernel<16, 1, true>, index_scores_kernel<32, 1, true>,
+                       index_scores_kernel<32, 2, true>, index_scores_kernel<32, 4, true>}) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kISSmem);
     if (e != cudaSuccess) return e;
   }
@@ -665,10 +664,14 @@ cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return Hp == 16   ? cudaLaunchKernelEx(&cfg, index_scores_kernel<16, 1>, a)
-         : Hp == 32 ? cudaLaunchKernelEx(&cfg, index_scores_kernel<32, 1>, a)
-         : Hp == 64 ? cudaLaunchKernelEx(&cfg, index_scores_kernel<32, 2>, a)
-                    : cudaLaunchKernelEx(&cfg, index_scores_kernel<32, 4>, a);
+  auto go = [&](auto whole) {
+    constexpr bool kWhole = decltype(whole)::value;
+    return Hp == 16   ? cudaLaunchKernelEx(&cfg, index_scores_kernel<16, 1, kWhole>, a)
+           : Hp == 32 ? cudaLaunchKernelEx(&cfg, index_scores_kernel<32, 1, kWhole>, a)
+           : Hp == 64 ? cudaLaunchKernelEx(&cfg, index_scores_kernel<32, 2, kWhole>, a)
+                      : cudaLaunchKernelEx(&cfg, index_scores_kernel<32, 4, kWhole>, a);
+  };
+  return a.block % 32 == 0 ? go(std::true_type{}) : go(std::false_type{});
 }
 
 }  // namespace mla

@@ -7,7 +7,7 @@
 // both quotients IEEE float32. A key's codes and scale go to its slot; a query head's scale is
 // multiplied into the head's weight, so that w relu(q.k) needs no further factor. A row with a value
 // that is not finite gets a NaN scale. (A division for each value instead of one for the row: 41 us against
-// 23 for 4096 tokens x 64 heads.)
+// 23 then, for 4096 tokens x 64 heads.)
 //
 // Memory bound at many tokens (4096 x 64 heads 21.7 us for 103 MB, 4.7 TB/s; 128 x 64 heads 2.1 us, latency).
 // Bytes: 256 in and 132 out per row. Eight lanes share a row (eight values of the fixed half and eight of
