@@ -15,21 +15,24 @@
 // becomes one unit per worker. (The partition of the chunk scheduler, without its search for the
 // sequence of a block: here a block's number says which token it belongs to.) Where a share holds six
 // blocks or more, blocks stay whole and go to the worker in whose share their middle lies: a worker then
-// has up to half a block more, and nothing is merged (512 tokens x 128 heads x 2048 keys, bf16: 192 us so,
-// 194 with cut blocks, whose merge takes 12).
+// has up to half a block more, and nothing is merged (512 tokens x 128 heads x 2048 keys, bf16: 2 us less
+// than with cut blocks, whose merge takes 12 by itself).
 //
 // One cluster of eight CTAs: a warp takes a token at a time and sends its length to the first CTA's shared
 // memory, where the partition is made. Bound by latency: the list, lengths and offsets are read at once,
-// then the page numbers; after a cluster barrier two scans (6.5 us for 2 to 64 tokens, 10 for 512; a single CTA
-// for few tokens is no faster).
+// then the page numbers; after a cluster barrier two scans by as many warps as there are 32 tokens. What ran
+// all 32 warps through 64-bit arithmetic took 6.5 us for 2 to 64 tokens and 10 for 512, more than half of it
+// in the partition; calls are 1 us (tiny ones) to 11 us (512 tokens) faster now. A single CTA for few tokens
+// is no faster.
+#include <type_traits>
 #include "mla_index.h"
 #include "mla_ptx.cuh"
 #include "mla_ragged.cuh"
-#include "mla_scan.cuh"
 
 namespace mla {
 namespace {
 
+constexpr int kSchedThreads = 1024;
 constexpr int kRoom = 220 * 1024;          // shared memory for lengths and sets
 constexpr int kPlanLens = 8192;            // tokens whose lengths fit the first CTA's shared memory
 
@@ -41,25 +44,55 @@ __device__ __forceinline__ int tiles_of(int len) {
   return len > 0 ? (len + kChunkTile - 1) / kChunkTile : 1;
 }
 
+// Exclusive prefix sum over the first `warps` warps, which alone take part.
+__device__ __forceinline__ int64_t warps_exclusive_scan(int64_t v, int64_t* tmp, int64_t* total, int warps) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t x = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
+  }
+  int64_t before = 0, all = __shfl_sync(0xffffffffu, x, 31);
+  if (warps > 1) {
+    if (lane == 31) tmp[warp] = x;
+    named_bar_sync(1, 32 * warps);
+    int64_t w = lane < warps ? tmp[lane] : 0;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, w, off);
+      if (lane >= off) w += y;
+    }
+    all = __shfl_sync(0xffffffffu, w, 31);
+    before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+    before = warp > 0 ? before : 0;
+    named_bar_sync(1, 32 * warps);           // tmp may be written again
+  }
+  *total = all;
+  return before + x - v;
+}
+
 }  // namespace
 
-// kFew: for the decode kernel (up to 16 rows), else for the chunk attention's.
-template <bool kFew>
+// kFew: for the decode kernel (up to 16 rows), else for the chunk attention's. kSmall: positions fit 32 bits,
+// which makes the code that runs once per launch, from instruction cache misses, a good deal shorter.
+template <bool kFew, bool kSmall>
 __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePlanArgs a, int warps) {
   extern __shared__ int32_t plan_smem[];   // [T <= kPlanLens] lengths, then [warps][words] sets
   __shared__ int64_t scan_tmp[32];
-  __shared__ uint32_t flags_s[kPlanCtas];
+  __shared__ uint32_t flags_s[kPlanCtas], bad_s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
   const uint32_t rank = cluster_ctarank();
   const bool near = a.T <= kPlanLens;
   // (the first CTA has to run before its shared memory is written)
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  if (tid == 0) bad_s = 0u;
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   griddep_wait();                          // the inputs and the workspace may be the work before's
   griddep_launch_dependents();
   uint32_t bad = 0;
   for (int b = rank * kSchedThreads + tid; b < a.B; b += kPlanCtas * kSchedThreads)
     bad |= ragged_errors(a.cu_q, a.seq_lens, b, a.T, a.max_len);
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   bool none = false;                       // a token of this warp's has no key
   const uint32_t lens_of_first = map_to_rank(smem_u32(plan_smem), 0);
   if (warp < warps) {
@@ -142,9 +175,9 @@ __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePla
       none |= total == 0;
     }
   }
-  bad = (__syncthreads_or((bad & MLA_DEVERR_CU_Q) != 0) ? MLA_DEVERR_CU_Q : 0u) |
-        (__syncthreads_or((bad & MLA_DEVERR_SEQ_LEN) != 0) ? MLA_DEVERR_SEQ_LEN : 0u) |
-        (__syncthreads_or((bad & MLA_DEVERR_BLOCK_TABLE) != 0) ? MLA_DEVERR_BLOCK_TABLE : 0u);
+  if (bad != 0) atomicOr(&bad_s, bad);
+  __syncthreads();
+  bad = bad_s;
   if (tid < kPlanCtas) st_cluster_u32(map_to_rank(smem_u32(flags_s + rank), tid), bad);
   const int first = a.cu_q[0], last = a.cu_q[a.B];
   cluster_sync();                          // tables, lengths and flags of all CTAs
@@ -169,10 +202,13 @@ __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePla
     if (tid == 0) s.hdr[1] = s.hdr[2] = s.hdr[3] = s.hdr[4] = 0;
     return;
   }
+  // a token to a thread, as long as there are threads; the other warps are done
+  const int tokens = last - first, scanning = min(kSchedThreads / 32, (tokens + 31) / 32), threads = 32 * scanning;
+  if (warp >= scanning) return;
   const int G = kFew ? 1 : (s.H + kChunkRows - 1) / kChunkRows;   // blocks of a token
   auto len_of = [&](int t) { return near ? plan_smem[t] : a.lens[t]; };
   // a thread takes neighbouring tokens
-  const int tokens = last - first, chunk = (tokens + kSchedThreads - 1) / kSchedThreads;
+  const int chunk = (tokens + threads - 1) / threads;
   const int t0 = first + min(tokens, tid * chunk), t1 = min(last, t0 + chunk);
   int64_t mine = 0;                        // tokens with tiles << 40 | tiles
   for (int t = t0; t < t1; ++t) {
@@ -180,53 +216,54 @@ __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePla
     mine += n > 0 ? ((int64_t)1 << 40) + n : 0;
   }
   int64_t all;
-  const int64_t before = block_exclusive_scan(mine, scan_tmp, &all), kTiles = ((int64_t)1 << 40) - 1;
-  const int64_t W = (all & kTiles) * G, S = (all >> 40) * G;
+  const int64_t before = warps_exclusive_scan(mine, scan_tmp, &all, scanning), kTiles = ((int64_t)1 << 40) - 1;
+  using Pos = std::conditional_t<kSmall, uint32_t, int64_t>;
+  const Pos W = (Pos)(all & kTiles) * G, S = (Pos)(all >> 40) * G, workers = (Pos)s.workers;
   // X is dropped when a worker's share would be too small for it (q <= 2 X): then every worker's range
   // holds at least one tile
-  int X = s.setup;
-  int64_t q = (W + S * X + s.workers - 1) / s.workers;
-  if (X > 0 && q <= 2 * (int64_t)X) {
+  Pos X = (Pos)s.setup, q = (W + S * X + workers - 1) / workers;
+  if (X > 0 && q <= 2 * X) {
     X = 0;
-    q = (W + s.workers - 1) / s.workers;
+    q = (W + workers - 1) / workers;
   }
   if (q == 0) q = 1;                       // (no keys at all)
-  const bool small = W + S * X + q < (int64_t)1 << 31;   // (64-bit divisions are several times as long)
-  auto worker_of = [&](int64_t p) -> int64_t { return small ? (int64_t)((uint32_t)p / (uint32_t)q) : p / q; };
-  const int64_t pos0 = (before & kTiles) * G + (before >> 40) * G * X;
+  const Pos first_block = (Pos)(before >> 40) * G, pos0 = (Pos)(before & kTiles) * G + first_block * X;
   // a unit: tiles [tb, te) of block g of token t, for the attention kernels
-  auto put_unit = [&](int64_t unit, int t, int g, int len, int tb, int te, int slot) {
+  auto put_unit = [&](Pos unit, int t, int g, int len, int tb, int te, int slot) {
     if (kFew) {
       reinterpret_cast<int4*>(s.units)[unit] = make_int4(t, 0, tb | (te << 16), slot);
     } else {
       const int r0 = g * kChunkRows;
       int4* u = reinterpret_cast<int4*>(s.units + unit);
-      u[0] = make_int4(t, (int32_t)((int64_t)t * s.H + r0), r0, len > 0 ? tb | (te << 16) : 0);
+      u[0] = make_int4(t, t * s.H + r0, r0, len > 0 ? tb | (te << 16) : 0);
       u[1] = make_int4(slot, len, len, min(kChunkRows, s.H - r0));
     }
   };
-  if (q >= 6 * (int64_t)(tiles_of<kFew>(a.width * a.block) + X)) {
-    for (int c = tid; c <= s.workers; c += kSchedThreads) s.cta_first[c] = (int32_t)S;
-    if (tid == 0) {
-      s.hdr[1] = (uint32_t)S;
-      s.hdr[2] = 0;
-      s.hdr[3] = (uint32_t)(q < 0xFFFFFFFFll ? q : 0xFFFFFFFFll);
-      s.hdr[4] = (uint32_t)X;
-    }
-    __syncthreads();
-    int64_t pos = pos0, unit = (before >> 40) * G, last_worker = -1;
+  auto put_header = [&](Pos units, uint32_t cut) {
+    if (tid != 0) return;
+    s.hdr[1] = (uint32_t)units;
+    s.hdr[2] = cut;
+    s.hdr[3] = (uint32_t)q;
+    s.hdr[4] = (uint32_t)X;
+  };
+  if (q >= 6 * ((Pos)tiles_of<kFew>(a.width * a.block) + X)) {
+    for (int c = tid; c <= s.workers; c += threads) s.cta_first[c] = (int32_t)S;
+    put_header(S, 0u);
+    named_bar_sync(1, threads);
+    Pos pos = pos0, unit = first_block, last_worker = ~(Pos)0;
     // the worker of the block before (of the last token before that has tiles)
     for (int t = t0 - 1; t >= first && t0 < t1; --t) {
-      const int n = tiles_of<kFew>(len_of(t));
+      const Pos n = tiles_of<kFew>(len_of(t));
       if (n == 0) continue;
-      last_worker = worker_of(pos0 - (X + n) + (X + n) / 2);
+      last_worker = (pos0 - (X + n) + (X + n) / 2) / q;
       break;
     }
     for (int t = t0; t < t1; ++t) {
-      const int len = len_of(t), n = tiles_of<kFew>(len);
+      const int len = len_of(t);
+      const Pos n = tiles_of<kFew>(len);
       for (int g = 0; g < G && n > 0; ++g, ++unit) {
-        const int64_t c = worker_of(pos + (X + n) / 2);
-        put_unit(unit, t, g, len, 0, n, -1);
+        const Pos c = (pos + (X + n) / 2) / q;
+        put_unit(unit, t, g, len, 0, (int)n, -1);
         if (c != last_worker) s.cta_first[c] = (int32_t)unit;
         last_worker = c;
         pos += X + n;
@@ -234,56 +271,55 @@ __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePla
     }
     return;
   }
-  int64_t pos = pos0, mine3 = 0;           // units << 32 | cut blocks << 16 | partial slots (as the chunk scheduler)
+  Pos pos = pos0;
+  int64_t mine3 = 0;                       // units << 32 | cut blocks << 16 | partial slots (as the chunk scheduler)
   for (int t = t0; t < t1; ++t) {
-    const int n = tiles_of<kFew>(len_of(t));
+    const Pos n = tiles_of<kFew>(len_of(t));
     for (int g = 0; g < G && n > 0; ++g) {
-      const int64_t ts = pos + X, ns = worker_of(ts + n - 1) - worker_of(ts) + 1;
-      mine3 += (ns << 32) + (ns >= 2 ? (1 << 16) + ns : 0);
+      const Pos ts = pos + X, ns = (ts + n - 1) / q - ts / q + 1;
+      mine3 += ((int64_t)ns << 32) + (ns >= 2 ? (1 << 16) + (int64_t)ns : 0);
       pos = ts + n;
     }
   }
   int64_t all3;
-  const int64_t before3 = block_exclusive_scan(mine3, scan_tmp, &all3);
-  const int64_t n_units = all3 >> 32, n_split = (all3 >> 16) & 0xFFFF;
-  int64_t unit = before3 >> 32, split = (before3 >> 16) & 0xFFFF, slot = before3 & 0xFFFF;
-  for (int c = tid; c <= s.workers; c += kSchedThreads) s.cta_first[c] = (int32_t)n_units;
-  __syncthreads();
+  const int64_t before3 = warps_exclusive_scan(mine3, scan_tmp, &all3, scanning);
+  const Pos n_units = (Pos)(all3 >> 32);
+  Pos unit = (Pos)(before3 >> 32);
+  int split = (int)(before3 >> 16) & 0xFFFF, slot = (int)before3 & 0xFFFF;
+  for (int c = tid; c <= s.workers; c += threads) s.cta_first[c] = (int32_t)n_units;
+  put_header(n_units, (uint32_t)(all3 >> 16) & 0xFFFFu);
+  named_bar_sync(1, threads);
   pos = pos0;
   for (int t = t0; t < t1; ++t) {
-    const int len = len_of(t), n = tiles_of<kFew>(len);
+    const int len = len_of(t);
+    const Pos n = tiles_of<kFew>(len);
     for (int g = 0; g < G && n > 0; ++g) {
-      const int64_t pre = pos, ts = pos + X, c0 = worker_of(ts);
-      const int ns = (int)(worker_of(ts + n - 1) - c0 + 1);
+      const Pos pre = pos, ts = pos + X, c0 = ts / q;
+      const int ns = (int)((ts + n - 1) / q - c0 + 1);
       if (ns >= 2) {
         const int r0 = g * kChunkRows;
-        s.split_list[split++] = kFew ? make_int4(t, 0, ns, (int)slot)
-                                     : make_int4((int32_t)((int64_t)t * s.H + r0), min(kChunkRows, s.H - r0), ns, (int)slot);
+        s.split_list[split++] = kFew ? make_int4(t, 0, ns, slot) : make_int4(t * s.H + r0, min(kChunkRows, s.H - r0), ns, slot);
       }
-      for (int k = 0; k < ns; ++k) {
-        const int64_t c = c0 + k;
-        const int64_t p0 = ts > c * q ? ts : c * q;
-        const int64_t p1 = ts + n < (c + 1) * q ? ts + n : (c + 1) * q;
-        put_unit(unit, t, g, len, (int)(p0 - ts), (int)(p1 - ts), ns >= 2 ? (int)slot + k : -1);
+      Pos edge = c0 * q;                   // where the worker's range starts
+      for (int k = 0; k < ns; ++k, ++unit, edge += q) {
+        const Pos p0 = ts > edge ? ts : edge, p1 = ts + n < edge + q ? ts + n : edge + q;
+        put_unit(unit, t, g, len, (int)(p0 - ts), (int)(p1 - ts), ns >= 2 ? slot + k : -1);
         // the worker's first unit: its range starts at this piece, or inside this block's set-up
-        if (p0 == c * q || (k == 0 && pre <= c * q)) s.cta_first[c] = (int32_t)unit;
-        ++unit;
+        if (p0 == edge || (k == 0 && pre <= edge)) s.cta_first[c0 + k] = (int32_t)unit;
       }
       if (ns >= 2) slot += ns;
       pos = ts + n;
     }
   }
-  if (tid == 0) {
-    s.hdr[1] = (uint32_t)n_units;
-    s.hdr[2] = (uint32_t)n_split;
-    s.hdr[3] = (uint32_t)(q < 0xFFFFFFFFll ? q : 0xFFFFFFFFll);
-    s.hdr[4] = (uint32_t)X;
-  }
 }
 
 cudaError_t sparse_plan_prepare() {
-  const cudaError_t e = cudaFuncSetAttribute(sparse_plan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
-  return e != cudaSuccess ? e : cudaFuncSetAttribute(sparse_plan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
+  for (auto* kernel : {sparse_plan_kernel<false, false>, sparse_plan_kernel<false, true>, sparse_plan_kernel<true, false>,
+                       sparse_plan_kernel<true, true>}) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRoom);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_sparse_plan(const SparsePlanArgs& a, cudaStream_t s) {
@@ -306,8 +342,14 @@ cudaError_t launch_sparse_plan(const SparsePlanArgs& a, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return a.few ? cudaLaunchKernelEx(&cfg, sparse_plan_kernel<true>, a, warps)
-               : cudaLaunchKernelEx(&cfg, sparse_plan_kernel<false>, a, warps);
+  // the most positions there can be, and a share more
+  const int64_t tile = a.few ? kTileTokens : kChunkTile, G = a.few ? 1 : (a.sched.H + kChunkRows - 1) / kChunkRows;
+  const int64_t most = (int64_t)a.T * G * (((int64_t)a.width * a.block + tile - 1) / tile + 1 + a.sched.setup);
+  const bool small = 2 * most + a.sched.workers < (int64_t)1 << 31;
+  return a.few ? (small ? cudaLaunchKernelEx(&cfg, sparse_plan_kernel<true, true>, a, warps)
+                        : cudaLaunchKernelEx(&cfg, sparse_plan_kernel<true, false>, a, warps))
+               : (small ? cudaLaunchKernelEx(&cfg, sparse_plan_kernel<false, true>, a, warps)
+                        : cudaLaunchKernelEx(&cfg, sparse_plan_kernel<false, false>, a, warps));
 }
 
 }  // namespace mla

@@ -41,6 +41,22 @@ def random_lists(rng, lens, block, K, causal=True, lead=0, pad=0):
     return np.array([[12345] * K] * lead + rows + [[54321] * K] * pad, dtype=np.int32).reshape(-1, K)
 
 
+def attended(q, k, kv):
+    """(out, lse, bound) in float64 of one token's queries [H, 576] over its keys [n, 576]; bounds as the chunk
+    harness derives them."""
+    s = (q @ k.T) * SCALE
+    m = s.amax(dim=1, keepdim=True)
+    w = torch.exp(s - m)
+    z = w.sum(dim=1, keepdim=True)
+    v = k[:, :512]
+    out, A = (w / z) @ v, (w / z) @ v.abs()
+    t = 2.0 ** -8 * (A + out.abs())
+    if kv == F8:
+        d = 2.0 ** -17 * q.abs().amax(dim=1, keepdim=True) * SCALE * k.abs().sum(dim=1).max()
+        t = t + 2.0 ** -11 * A + 2.0 ** -13 * v.abs().sum(dim=0)[None, :] / z + 2 * d * A
+    return out, (m + torch.log(z))[:, 0], 1.05 * t + 1e-6
+
+
 class SparseCase(ChunkCase):
     def __init__(self, lens, H, P, block, K, kv=BF, causal=True, pad=0, seed=0, lead=0, selected=None):
         super().__init__(lens, H, P, kv, causal, pad, seed, lead)
@@ -86,20 +102,7 @@ class SparseCase(ChunkCase):
             keys = self.keys_of(b, i)
             if not keys:
                 continue
-            k = self.keys[b][keys]
-            s = (q[i] @ k.T) * SCALE
-            m = s.amax(dim=1, keepdim=True)
-            w = torch.exp(s - m)
-            z = w.sum(dim=1, keepdim=True)
-            v = k[:, :512]
-            out[i] = (w / z) @ v
-            lse[i] = (m + torch.log(z))[:, 0]
-            A = (w / z) @ v.abs()
-            t = 2.0 ** -8 * (A + out[i].abs())
-            if self.kv == F8:
-                d = 2.0 ** -17 * q[i].abs().amax(dim=1, keepdim=True) * SCALE * k.abs().sum(dim=1).max()
-                t = t + 2.0 ** -11 * A + 2.0 ** -13 * v.abs().sum(dim=0)[None, :] / z + 2 * d * A
-            bound[i] = 1.05 * t + 1e-6
+            out[i], lse[i], bound[i] = attended(q[i], self.keys[b][keys], self.kv)
         return out, lse, bound
 
 

@@ -7,7 +7,7 @@ import torch
 
 from chunk_harness import BF, F8, LSE_ABS, SCALE, ChunkCase, bf16_normal
 from mla_paged_decode_02_gb300 import api
-from sparse_harness import INF, SparseCase, selection
+from sparse_harness import INF, SparseCase, attended, selection
 
 pytestmark = pytest.mark.gpu
 
@@ -123,16 +123,8 @@ def test_whole_blocks_of_many_tokens(kv, H):
             if not keys:
                 assert (out == 0).all() and (lse == -INF).all()
                 continue
-            k = c.keys[b][keys]
-            s = c.q[t].double() @ k.T * SCALE
-            w = torch.softmax(s, dim=1)
-            A, r = w @ k[:, :512].abs(), w @ k[:, :512]
-            bound = 2.0 ** -8 * (A + r.abs())
-            if kv == F8:
-                bound = bound + 2.0 ** -11 * A + 2.0 ** -13 * k[:, :512].abs().sum(dim=0) * w.amax(dim=1, keepdim=True) + \
-                    2.0 ** -16 * c.q[t].double().abs().amax() * SCALE * k.abs().sum(dim=1).max() * A
-            assert ((out - r).abs() <= 1.05 * bound + 1e-6).all()
-            assert (lse - torch.logsumexp(s, dim=1)).abs().max() <= LSE_ABS[kv]
+            r, rl, bound = attended(c.q[t].double(), c.keys[b][keys], kv)
+            assert ((out - r).abs() <= bound).all() and (lse - rl).abs().max() <= LSE_ABS[kv]
     assert (c.out[:3] == 7.0).all() and (c.out[-5:] == 7.0).all() and (c.lse[-5:] == -3.5).all()
 
 
@@ -144,12 +136,34 @@ def test_more_tokens_than_lengths_fit_shared_memory():
     assert api.decode_check(c.workspace) == (0, 0)
     for b, i in ((0, 0), (0, 1), (0, 3999), (1, 0), (1, 2500), (1, 4999), (2, 0)):
         t = c.starts[b] + i
-        k = c.keys[b][c.keys_of(b, i)]
-        s = c.q[t].double() @ k.T * SCALE
-        w = torch.softmax(s, dim=1)
-        A, r = w @ k[:, :512].abs(), w @ k[:, :512]
-        assert ((c.out[t].double().cpu() - r).abs() <= 1.05 * 2.0 ** -8 * (A + r.abs()) + 1e-6).all()
-        assert (c.lse[t].double().cpu() - torch.logsumexp(s, dim=1)).abs().max() <= LSE_ABS[BF]
+        r, rl, bound = attended(c.q[t].double(), c.keys[b][c.keys_of(b, i)], BF)
+        assert ((c.out[t].double().cpu() - r).abs() <= bound).all()
+        assert (c.lse[t].double().cpu() - rl).abs().max() <= LSE_ABS[BF]
+
+
+@pytest.mark.parametrize("kv", [BF, F8])
+def test_more_positions_than_32_bits_might_hold(kv):
+    """Lists long enough that the tokens' tiles could pass 2^30, though few entries are used."""
+    T, K, P = 1 << 18, 1024, 1024
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    cache = torch.randn((3, P, 576), generator=gen, device="cuda").to(torch.bfloat16)
+    scale = None
+    if kv == F8:
+        cache, scale = cache.to(torch.float8_e4m3fn), torch.ones(1, device="cuda")
+    q = torch.randn((T, 1, 576), generator=gen, device="cuda").to(torch.bfloat16)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.full((1, 1024), -1, **i32)
+    table[0, :3] = torch.tensor([2, 0, 1], **i32)
+    sel = torch.full((T, K), -1, **i32)
+    sel[:, 5] = torch.arange(T, device="cuda").int() % 3
+    sel[::3, 9] = 1
+    out, lse = api.sparse_attention(q, cache, table, torch.tensor([3 * P], **i32), torch.tensor([0, T], **i32), sel, SCALE, scale,
+                                    max_seq_len=1 << 20, block_size=P, causal=False)
+    rows = cache[[2, 0, 1]].double()
+    for t in (0, 1, 2, 3, 77777, T - 2, T - 1):
+        k = torch.cat([rows[c] for c in sorted({t % 3} | ({1} if t % 3 == 0 else set()))])
+        r, rl, bound = attended(q[t].double(), k, kv)
+        assert ((out[t].double() - r).abs() <= bound).all() and (lse[t].double() - rl).abs().max() <= LSE_ABS[kv]
 
 
 def test_a_long_context():
@@ -169,12 +183,8 @@ def test_a_long_context():
         rows = [j for c in sorted(set(sel[i].tolist())) if 0 <= c < nb for j in range(32 * c, min(n, 32 * c + 32))]
         j = torch.tensor(rows, device="cuda")
         k = cache.view(-1, 576)[table[0].long()[j // 64] * 64 + j % 64].double()
-        s = q[i].double() @ k.T * SCALE
-        w = torch.softmax(s, dim=1)
-        A = w @ k[:, :512].abs()
-        r = w @ k[:, :512]
-        assert ((out[i].double() - r).abs() <= 1.05 * 2.0 ** -8 * (A + r.abs()) + 1e-6).all()
-        assert (lse[i].double() - torch.logsumexp(s, dim=1)).abs().max() <= 1e-4
+        r, rl, bound = attended(q[i].double(), k, BF)
+        assert ((out[i].double() - r).abs() <= bound).all() and (lse[i].double() - rl).abs().max() <= LSE_ABS[BF]
 
 
 @pytest.mark.parametrize("kv,P", [(BF, 16), (F8, 64)])
@@ -323,12 +333,6 @@ def test_a_serving_run(kv):
             assert chosen[t].tolist() == want
             keys = torch.tensor([j for c in want if c >= 0 for j in range(c * block, min(vis, c * block + block))])
             k = rows[table[b, keys // P].long() * P + keys % P]
-            x = q[t].cpu().double() @ k.T * SCALE
-            w = torch.softmax(x, dim=1)
-            A, r = w @ k[:, :512].abs(), w @ k[:, :512]
-            bound = 2.0 ** -8 * (A + r.abs())
-            if kv == F8:
-                bound = bound + 2.0 ** -11 * A + 2.0 ** -13 * k[:, :512].abs().sum(dim=0) * w.amax(dim=1, keepdim=True) + \
-                    2.0 ** -16 * q[t].cpu().double().abs().amax() * SCALE * k.abs().sum(dim=1).max() * A
-            assert ((out[t].cpu().double() - r).abs() <= 1.05 * bound + 1e-6).all()
-            assert (lse[t].cpu().double() - torch.logsumexp(x, dim=1)).abs().max() <= LSE_ABS[kv]
+            r, rl, bound = attended(q[t].cpu().double(), k, kv)
+            assert ((out[t].cpu().double() - r).abs() <= bound).all()
+            assert (lse[t].cpu().double() - rl).abs().max() <= LSE_ABS[kv]
