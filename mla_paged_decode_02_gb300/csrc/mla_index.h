@@ -41,7 +41,7 @@ struct IndexScoreArgs {
   int32_t TG, tg_log2;             // tokens of a group, a power of two
   int32_t q_rows, units, key_slots;   // rows of a query buffer, query buffers, tiles of keys in shared memory
   int32_t unit_blocks;             // blocks of a unit
-  uint32_t block_inv;              // 2^32 / block, rounded up
+  uint32_t block_inv, page_inv;    // 2^32 / block, 2^32 / P, rounded up
   int32_t test_stall;
   uint64_t wait_limit_ns;
 };

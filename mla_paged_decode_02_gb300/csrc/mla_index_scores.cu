@@ -29,9 +29,10 @@
 // over 24 K keys 406 us (2.1 PFLOP/s of E4M3; 34% of tensor cycles). On the way there: one issuing warp held
 // back everything (546 us for four warpgroups, its products of 128 columns take it 570 clocks), two of them
 // 490, products of 256 columns 457; a chunk more of double buffering or a quarter of max on the FMA pipe, 3%.
-// Few tokens: latency and the loading warp. 121 sequences x 4 K keys 21.5 us for 65 MB, of which 7 us pass
+// Few tokens: latency and the loading warp. 121 sequences x 4 K keys 17.7 us for 65 MB, of which 6 us pass
 // before the first product and after the last; with one warp for units and keys 32, with keys' scales as bulk
-// copies 24 (each takes the warp about 95 clocks to issue, like a key box).
+// copies 24 (each takes the warp about 95 clocks to issue, like a key box), tile by tile 21.5, with integer
+// divisions where a unit's pages are looked up 18.4.
 #include <type_traits>
 #include "mla_index.h"
 #include "mla_ptx.cuh"
@@ -50,6 +51,7 @@ constexpr int kISTmem = 2 * kISIssuers * kISColumns;
 constexpr int kISKeys = 128;                      // keys of a tile
 constexpr int kISSlotBytes = kISKeys * kDIndex;   // 16 KB
 constexpr int kISMaxSlots = 12;
+constexpr int kISTogether = 8;                    // tiles whose loads are issued at once, where there are slots for them
 // Key scales have a ring of their own, read later than the keys. A slot of it is filled for tile t + 16
 // once the keys of tile t + 4 or a later one have been given back by both issuing warps. A product covers
 // two tiles at most and the two pairs of accumulators alternate, so by then the warp that issued tile t's
@@ -380,18 +382,17 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
       counted = end_units;
     }
     // the end of the units: the others leave, and the last units' scores are written
-    ok = ok && finish_unit(ub, uph, nu >= (uint32_t)units);
-    if (ok) {
-      if (lane == 0) info_s[ub].ntok = 0;
-      __syncwarp();
-      if (el) {
-        mbar_arrive(b_info + 8 * ub);
-        mbar_arrive(b_qfull + 8 * ub);
+    for (int i = 0; i < units && ok; ++i) {
+      ok = finish_unit(ub, uph, nu + i >= (uint32_t)units);
+      if (i == 0 && ok) {
+        if (lane == 0) info_s[ub].ntok = 0;
+        __syncwarp();
+        if (el) {
+          mbar_arrive(b_info + 8 * ub);
+          mbar_arrive(b_qfull + 8 * ub);
+        }
       }
-      for (int i = 1; i < units && ok; ++i) {
-        if (++ub == (uint32_t)units) { ub = 0; uph ^= 1; }
-        ok = finish_unit(ub, uph, nu + i >= (uint32_t)units);
-      }
+      if (++ub == (uint32_t)units) { ub = 0; uph ^= 1; }
     }
     if (!ok && lane == 0) {
       // copies in flight land before the CTA leaves: the last fill of each buffer
@@ -403,7 +404,10 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
   } else if (warp == 3) {
     // ---------------------------------------------------------------------------- keys and scales
     const bool el = elect_one();
-    const int per = kISKeys / a.box_rows;               // boxes of a tile: lane i issues box i
+    const int per = kISKeys / a.box_rows;               // boxes of a tile
+    const int per_log2 = __ffs(per) - 1;
+    // a lane brings four scales of each tile
+    const int my_box = lane * per >> 5, my_row = lane * 4 - my_box * a.box_rows;
     uint32_t ub = 0, uph = 0, slot = 0, ph = 1, filled = 0;
     bool ok = true;
     while (ok) {
@@ -417,7 +421,7 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
       auto row_of = [&](int box) -> int {
         const int tok = k0 + box * a.box_rows;
         if (tok >= last) return -1;
-        const int page = tok / a.P, in = tok - page * a.P;
+        const int page = (int)__umulhi((uint32_t)tok, a.page_inv), in = tok - page * a.P;
         int pg = __ldg(pages + page);
         if (pg < 0 || pg >= a.num_pages) {
           atomicOr(err, MLA_DEVERR_BLOCK_TABLE);
@@ -426,28 +430,63 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
         return pg * a.P + in;
       };
       int rows = row_of(lane), ahead = tiles * per > 32 ? row_of(lane + 32) : -1;
-      // a lane brings four scales of each tile
-      const int my_box = lane * 4 / a.box_rows, my_row = lane * 4 - my_box * a.box_rows;
-      for (int tile = 0; tile < tiles; ++tile) {
-        const int at = tile * per & 31;                 // per divides 32
-        if (tile > 0 && at == 0) {
-          rows = ahead;
-          ahead = row_of((tile * per & ~31) + 32 + lane);
+      if (S >= kISTogether) {
+        // several tiles at once: a wait, an expected count or a box costs the warp about 100 clocks whether one lane
+        // or several make it (a decode step 18.4 us, tile by tile 21.5)
+        for (int tile = 0; tile < tiles;) {
+          const int at = tile * per & 31;                 // per divides 32
+          if (tile > 0 && at == 0) {
+            rows = ahead;
+            ahead = row_of((tile * per & ~31) + 32 + lane);
+          }
+          const int some = min(min(kISTogether, tiles - tile), (32 - at) >> per_log2);
+          uint32_t my_slot = slot + (uint32_t)lane;       // lanes 0 .. some - 1: a tile each
+          const bool wraps = my_slot >= (uint32_t)S;
+          if (wraps) my_slot -= S;
+          const uint32_t empty = b_kempty + 8 * my_slot, parity = ph ^ (wraps ? 1u : 0u);
+          ok = __all_sync(0xffffffffu, lane >= some || mbar_try_wait_sleep(empty, parity, kISFirstWaitNs) ||
+                                           wait_longer(empty, parity, smem_u32(&abort_s), err, a.wait_limit_ns));
+          if (!ok) break;
+          if (lane < some) mbar_arrive_expect_tx(b_kfull + 8 * my_slot, kISSlotBytes);
+          const int row = __shfl_sync(0xffffffffu, rows, at + lane);
+          uint32_t box_slot = slot + ((uint32_t)lane >> per_log2);
+          if (box_slot >= (uint32_t)S) box_slot -= S;
+          // a box past the keys starts at the end of the pool and reads zeros
+          if (lane < some << per_log2)
+            tma_load_2d(sK + box_slot * kISSlotBytes + (lane & (per - 1)) * a.box_rows * kDIndex, &a.tm_k, b_kfull + 8 * box_slot, 0,
+                        row >= 0 ? row : a.total_rows);
+          for (int k = 0; k < some; ++k) {
+            const int srow = __shfl_sync(0xffffffffu, rows, at + (k << per_log2) + my_box);
+            if (srow >= 0) copy16(sS + ((filled % kISScales) * kISKeys + lane * 4) * 4, a.scale + srow + my_row);
+            arrive_after_copies(b_kfull + 8 * slot);
+            ++filled;
+            if (++slot == (uint32_t)S) { slot = 0; ph ^= 1; }
+          }
+          tile += some;
         }
-        const int row = __shfl_sync(0xffffffffu, rows, at + (lane & (per - 1)));
-        const int srow = __shfl_sync(0xffffffffu, rows, at + my_box);
-        ok = wait(b_kempty + 8 * slot, ph);
-        if (!ok) break;
-        const uint32_t bar = b_kfull + 8 * slot;
-        if (el) mbar_arrive_expect_tx(bar, kISSlotBytes);
-        __syncwarp();
-        // a box past the keys starts at the end of the pool and reads zeros
-        if (lane < per)
-          tma_load_2d(sK + slot * kISSlotBytes + lane * a.box_rows * kDIndex, &a.tm_k, bar, 0, row >= 0 ? row : a.total_rows);
-        if (srow >= 0) copy16(sS + ((filled % kISScales) * kISKeys + lane * 4) * 4, a.scale + srow + my_row);
-        arrive_after_copies(bar);
-        ++filled;
-        if (++slot == (uint32_t)S) { slot = 0; ph ^= 1; }
+      } else {
+        // few slots, as beside large queries: tile by tile (4 tokens x 64 heads 22.4 us; in the form above 23 to 24.7)
+        for (int tile = 0; tile < tiles; ++tile) {
+          const int at = tile * per & 31;                 // per divides 32
+          if (tile > 0 && at == 0) {
+            rows = ahead;
+            ahead = row_of((tile * per & ~31) + 32 + lane);
+          }
+          const int row = __shfl_sync(0xffffffffu, rows, at + (lane & (per - 1)));
+          const int srow = __shfl_sync(0xffffffffu, rows, at + my_box);
+          ok = wait(b_kempty + 8 * slot, ph);
+          if (!ok) break;
+          const uint32_t bar = b_kfull + 8 * slot;
+          if (el) mbar_arrive_expect_tx(bar, kISSlotBytes);
+          __syncwarp();
+          // a box past the keys starts at the end of the pool and reads zeros
+          if (lane < per)
+            tma_load_2d(sK + slot * kISSlotBytes + lane * a.box_rows * kDIndex, &a.tm_k, bar, 0, row >= 0 ? row : a.total_rows);
+          if (srow >= 0) copy16(sS + ((filled % kISScales) * kISKeys + lane * 4) * 4, a.scale + srow + my_row);
+          arrive_after_copies(bar);
+          ++filled;
+          if (++slot == (uint32_t)S) { slot = 0; ph ^= 1; }
+        }
       }
       if (++ub == (uint32_t)units) { ub = 0; uph ^= 1; }
     }
@@ -648,6 +687,7 @@ cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s) {
   if (m < 1) m = 1;
   a.unit_blocks = (int)(m * (lcm / a.block));
   a.block_inv = (uint32_t)((((uint64_t)1 << 32) + a.block - 1) / a.block);   // keys of a unit x block < 2^32
+  a.page_inv = (uint32_t)((((uint64_t)1 << 32) + a.P - 1) / a.P);            // a key of a sequence x P < 2^32
   a.units = a.q_rows <= 256 ? kISMaxUnits : 2;
   const int fixed = is_fixed_bytes(a.units, a.q_rows, a.TG * a.unit_blocks);
   a.key_slots = (kISSmem - fixed) / kISSlotBytes;
