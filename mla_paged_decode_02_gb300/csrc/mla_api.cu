@@ -524,8 +524,8 @@ bool encode_chunk_maps(ChunkArgs* ca, const void* q, int tokens, int H, const vo
 
 // the attention kernel over the units that `sa` names, and the merge of the blocks it cut
 mla_status launch_chunk_pair(ChunkArgs& ca, ChunkCombineArgs& cc, const ChunkSchedArgs& sa, uint8_t* ws, const ChunkWs& w,
-                             float softmax_scale, const float* kv_scale, void* out, float* lse, bool fp8, int pairs, int nsm,
-                             cudaStream_t s) {
+                             float softmax_scale, const float* kv_scale, void* out, float* lse, bool fp8, int pairs,
+                             int merge_blocks, cudaStream_t s) {
   ca.units = sa.units;
   ca.cta_first = sa.cta_first;
   ca.err = sa.hdr;
@@ -546,7 +546,7 @@ mla_status launch_chunk_pair(ChunkArgs& ca, ChunkCombineArgs& cc, const ChunkSch
   cc.part_lse = ca.part_lse;
   cc.out = ca.out;
   cc.lse = ca.lse;
-  if (launch_chunk_combine(cc, 8 * nsm, s) != cudaSuccess) return MLA_ERR_CUDA;
+  if (launch_chunk_combine(cc, kChunkRows, merge_blocks, s) != cudaSuccess) return MLA_ERR_CUDA;
   return MLA_OK;
 }
 
@@ -629,7 +629,7 @@ MLA_EXPORT mla_status mla_chunk_attention(const mla_chunk_params* p, const void*
   cc.P = p->page_size;
   cc.num_pages = p->num_pages;
   cc.max_len = sa.max_len;
-  return launch_chunk_pair(ca, cc, sa, ws, w, softmax_scale, kv_scale, out, lse, fp8, pairs, nsm, s);
+  return launch_chunk_pair(ca, cc, sa, ws, w, softmax_scale, kv_scale, out, lse, fp8, pairs, 8 * nsm, s);
 }
 
 // ------------------------------------------------------------ rotating append, state merge
@@ -891,6 +891,11 @@ cudaError_t prepare_decode16(int dev) {
   return e;
 }
 
+// blocks of the merge: four warps to a row of the most blocks that can be cut, one per worker
+int merge_blocks(int64_t blocks, int rows, int workers, int nsm) {
+  return (int)std::min<int64_t>(8 * nsm, std::min<int64_t>(blocks, workers) * rows / 2);
+}
+
 // the plan, the decode kernel over the tokens' selected blocks, and the merge of cut ones (E4M3, up to 16 rows)
 mla_status sparse_few(const mla_sparse_params* p, const SparsePlanArgs& pa, const void* q, const void* kv_cache,
                       float softmax_scale, const float* kv_scale, void* out, float* lse, uint8_t* ws, const SparseWs& w,
@@ -930,17 +935,15 @@ mla_status sparse_few(const mla_sparse_params* p, const SparsePlanArgs& pa, cons
   da.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   da.test_stall = g_test_stall.load(std::memory_order_relaxed);
   if (launch_decode(da, rc, true, nsm, s) != cudaSuccess) return MLA_ERR_CUDA;
-  CombineArgs ca{};                        // B = 0: the plan has checked the pages
-  ca.hdr = pa.sched.hdr;
-  ca.err = pa.sched.hdr;
-  ca.split_list = pa.sched.split_list;
-  ca.part_o = da.part_o;
-  ca.part_lse = da.part_lse;
-  ca.out = da.out;
-  ca.lse = lse;
-  ca.R = H;
-  ca.RC = rc;
-  if (launch_combine(ca, 8 * nsm, s) != cudaSuccess) return MLA_ERR_CUDA;
+  ChunkCombineArgs cc{};                   // B = 0: the plan has checked the pages
+  cc.hdr = pa.sched.hdr;
+  cc.err = pa.sched.hdr;
+  cc.split_list = pa.sched.split_list;
+  cc.part_o = da.part_o;
+  cc.part_lse = da.part_lse;
+  cc.out = da.out;
+  cc.lse = lse;
+  if (launch_chunk_combine(cc, rc, merge_blocks(p->num_tokens, rc, nsm, nsm), s) != cudaSuccess) return MLA_ERR_CUDA;
   return MLA_OK;
 }
 
@@ -1043,5 +1046,7 @@ MLA_EXPORT mla_status mla_sparse_attention(const mla_sparse_params* p, const voi
   ca.MB = width;
   ca.causal = 0;
   ChunkCombineArgs cc{};                   // B = 0: the plan has checked the pages
-  return launch_chunk_pair(ca, cc, pa.sched, ws, w.chunk, softmax_scale, kv_scale, out, lse, fp8, pairs, nsm, s);
+  const int64_t blocks = (int64_t)p->num_tokens * ((p->num_heads + kChunkRows - 1) / kChunkRows);
+  return launch_chunk_pair(ca, cc, pa.sched, ws, w.chunk, softmax_scale, kv_scale, out, lse, fp8, pairs,
+                           merge_blocks(blocks, kChunkRows, pairs, nsm), s);
 }

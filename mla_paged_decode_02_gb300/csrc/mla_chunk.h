@@ -100,6 +100,7 @@ struct ChunkCombineArgs {
 cudaError_t launch_chunk_schedule(const ChunkSchedArgs& a, cudaStream_t s);
 cudaError_t launch_chunk(const ChunkArgs& a, bool fp8, int pairs, cudaStream_t s);
 cudaError_t chunk_prepare(bool fp8);
-cudaError_t launch_chunk_combine(const ChunkCombineArgs& a, int grid, cudaStream_t s);
+// rows: of a partial slot, kChunkRows or 16
+cudaError_t launch_chunk_combine(const ChunkCombineArgs& a, int rows, int grid, cudaStream_t s);
 
 }  // namespace mla

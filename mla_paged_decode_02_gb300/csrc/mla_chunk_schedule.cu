@@ -166,24 +166,25 @@ __global__ void __launch_bounds__(kSchedThreads) chunk_schedule_kernel(ChunkSche
 // Few cut rows (four warps exist for each): a warp per 128 columns of a row, lane s holding the
 // weight of piece s, four pieces read at a time. The call on 16 blocks cut into 6 pieces each takes
 // 64.5 us so and 66.5 us with a warp per row; with 76 cut blocks a warp per row is 1 us faster.
+template <int kRows>
 __device__ __forceinline__ void merge_few_rows(const ChunkCombineArgs& a, int64_t tasks, int64_t warp) {
   const int lane = threadIdx.x & 31;
   if (warp >= tasks * 4) return;
-  const int4 st = a.split_list[warp / (kChunkRows * 4)];
-  const int r = (int)(warp >> 2) % kChunkRows, col = ((int)warp & 3) * 128 + lane * 4;
+  const int4 st = a.split_list[warp / (kRows * 4)];
+  const int r = (int)(warp >> 2) % kRows, col = ((int)warp & 3) * 128 + lane * 4;
   if (r >= st.y) return;
   const int ns = st.z;
-  const float* plse = a.part_lse + (int64_t)st.w * kChunkRows + r;
-  const float* po = a.part_o + ((int64_t)st.w * kChunkRows + r) * kDV + col;
+  const float* plse = a.part_lse + (int64_t)st.w * kRows + r;
+  const float* po = a.part_o + ((int64_t)st.w * kRows + r) * kDV + col;
   float m = -INFINITY;
-  for (int s = lane; s < ns; s += 32) m = fmaxf(m, plse[(int64_t)s * kChunkRows]);
+  for (int s = lane; s < ns; s += 32) m = fmaxf(m, plse[(int64_t)s * kRows]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float wsum = 0.f;
   for (int s0 = 0; s0 < ns; s0 += 32) {
     const int mine = s0 + lane;
-    const float ls = mine < ns ? plse[(int64_t)mine * kChunkRows] : -INFINITY;
+    const float ls = mine < ns ? plse[(int64_t)mine * kRows] : -INFINITY;
     const float w = ls == -INFINITY ? 0.f : __expf(ls - m);
     const int n = min(32, ns - s0);
     for (int s = 0; s < n; s += 4) {
@@ -194,7 +195,7 @@ __device__ __forceinline__ void merge_few_rows(const ChunkCombineArgs& a, int64_
         ww[k] = s + k < n ? __shfl_sync(0xffffffffu, w, s + k) : 0.f;
         v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         // a NaN weight is read: it makes the row NaN
-        if (ww[k] != 0.f) v[k] = *reinterpret_cast<const float4*>(po + (int64_t)(s0 + s + k) * kChunkRows * kDV);
+        if (ww[k] != 0.f) v[k] = *reinterpret_cast<const float4*>(po + (int64_t)(s0 + s + k) * kRows * kDV);
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -218,7 +219,8 @@ __device__ __forceinline__ void merge_few_rows(const ChunkCombineArgs& a, int64_
 // Merges the pieces of cut blocks, a warp per (block, row): lse = log sum_s exp(lse_s),
 // out = sum_s exp(lse_s - lse) O_s; a piece in which the row sees no key has lse_s = -inf and
 // weight 0. Lane l owns output columns 16 l ..; also reports block-table entries outside the
-// pool among those the call read (they read page 0).
+// pool among those the call read (they read page 0). A partial slot has kRows rows.
+template <int kRows>
 __global__ void __launch_bounds__(256) chunk_combine_kernel(ChunkCombineArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t gtid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, gstride = (int64_t)gridDim.x * blockDim.x;
@@ -232,28 +234,28 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(ChunkCombineArgs a) 
       }
     }
   }
-  const int64_t tasks = (int64_t)a.hdr[2] * kChunkRows;
+  const int64_t tasks = (int64_t)a.hdr[2] * kRows;
   if (tasks * 4 <= gstride >> 5) {
-    merge_few_rows(a, tasks, gtid >> 5);
+    merge_few_rows<kRows>(a, tasks, gtid >> 5);
     return;
   }
   for (int64_t task = gtid >> 5; task < tasks; task += gstride >> 5) {
-    const int4 st = a.split_list[task / kChunkRows];
-    const int r = (int)(task % kChunkRows);
+    const int4 st = a.split_list[task / kRows];
+    const int r = (int)(task % kRows);
     if (r >= st.y) continue;
     const int ns = st.z, base = st.w;
     float m = -INFINITY;
-    for (int s = 0; s < ns; ++s) m = fmaxf(m, a.part_lse[(int64_t)(base + s) * kChunkRows + r]);
+    for (int s = 0; s < ns; ++s) m = fmaxf(m, a.part_lse[(int64_t)(base + s) * kRows + r]);
     float acc[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) acc[k] = 0.f;
     float wsum = 0.f;
     for (int s = 0; s < ns; ++s) {
-      const float ls = a.part_lse[(int64_t)(base + s) * kChunkRows + r];
+      const float ls = a.part_lse[(int64_t)(base + s) * kRows + r];
       if (ls == -INFINITY) continue;
       const float w = __expf(ls - m);
       wsum += w;
-      const float4* src = reinterpret_cast<const float4*>(a.part_o + ((int64_t)(base + s) * kChunkRows + r) * kDV) + lane * 4;
+      const float4* src = reinterpret_cast<const float4*>(a.part_o + ((int64_t)(base + s) * kRows + r) * kDV) + lane * 4;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float4 v = src[k];
@@ -291,7 +293,7 @@ cudaError_t launch_chunk_schedule(const ChunkSchedArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, chunk_schedule_kernel, a);
 }
 
-cudaError_t launch_chunk_combine(const ChunkCombineArgs& a, int grid, cudaStream_t s) {
+cudaError_t launch_chunk_combine(const ChunkCombineArgs& a, int rows, int grid, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(256);
@@ -301,7 +303,8 @@ cudaError_t launch_chunk_combine(const ChunkCombineArgs& a, int grid, cudaStream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_combine_kernel, a);
+  return rows == kChunkRows ? cudaLaunchKernelEx(&cfg, chunk_combine_kernel<kChunkRows>, a)
+                            : cudaLaunchKernelEx(&cfg, chunk_combine_kernel<16>, a);
 }
 
 }  // namespace mla

@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePla
       const int ns = (int)((ts + n - 1) / q - c0 + 1);
       if (ns >= 2) {
         const int r0 = g * kChunkRows;
-        s.split_list[split++] = kFew ? make_int4(t, 0, ns, slot) : make_int4(t * s.H + r0, min(kChunkRows, s.H - r0), ns, slot);
+        s.split_list[split++] = make_int4(t * s.H + r0, min(kChunkRows, s.H - r0), ns, slot);
       }
       Pos edge = c0 * q;                   // where the worker's range starts
       for (int k = 0; k < ns; ++k, ++unit, edge += q) {
