@@ -8,15 +8,17 @@
 // them) are left out, and a list that does not ascend goes through a bit set, so that an index
 // given twice counts once.
 //
-// Then the tokens' keys are shared out. A token's H rows are ceil(H / 128) blocks of up to 128 rows with
-// equally many tiles of 256 keys (for the decode kernel one block, and tiles of 128); laid end to end, X
-// set-up positions and the tiles for each, worker c (a CTA pair; an SM) takes positions [c q, (c + 1) q),
-// q = ceil(all / workers). A block that a boundary cuts
-// becomes one unit per worker. (The partition of the chunk scheduler, without its search for the
-// sequence of a block: here a block's number says which token it belongs to.) Where a share holds six
-// blocks or more, blocks stay whole and go to the worker in whose share their middle lies: a worker then
-// has up to half a block more, and nothing is merged (512 tokens x 128 heads x 2048 keys, bf16: 2 us less
-// than with cut blocks, whose merge takes 12 by itself).
+// Then the tokens' keys are shared out. A token's H rows are ceil(H / 128) blocks of up to 128 rows with equally
+// many tiles of 256 keys (for the decode kernel one block, and tiles of 128); laid end to end, X set-up positions
+// and the tiles for each, worker c (a CTA pair; an SM) takes positions [c q, (c + 1) q), q = ceil(all / workers).
+// A block that a boundary cuts becomes one unit per worker. (The partition of the chunk scheduler, without its
+// search for the sequence of a block: here a block's number says which token it belongs to.) Where a share holds
+// six blocks or more, blocks stay whole and go to the worker in whose share their middle lies: a worker then has
+// up to half a block more, and nothing is merged (512 tokens x 128 heads x 2048 keys, bf16: 2 us less than with
+// cut blocks, whose merge takes 12 by itself). With no more blocks than workers, each worker has a piece of one
+// block where such pieces need not be much longer than q: starting on a second block costs a worker about two
+// tiles (16 heads, E4M3, 2041 keys: 48 tokens 28.8 us against 33.8, 64 33.1 against 35.4, 152 55 against 61; 128
+// heads, bf16, 64 tokens 54 against 65; those with uneven lengths from 4 less to 1 more).
 //
 // One cluster of eight CTAs: a warp takes a token at a time and sends its length to the first CTA's shared
 // memory, where the partition is made. Bound by latency: the list, lengths and offsets are read at once,
@@ -34,6 +36,7 @@ namespace {
 
 constexpr int kSchedThreads = 1024;
 constexpr int kRoom = 220 * 1024;          // shared memory for lengths and sets
+constexpr int kPieces = 8;                 // sizes of pieces that are tried (a power of two)
 constexpr int kPlanLens = 8192;            // tokens whose lengths fit the first CTA's shared memory
 
 // tiles of 256 keys (a block that sees no key has one, in which its zeros are written), or of 128 for the
@@ -81,11 +84,13 @@ __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePla
   extern __shared__ int32_t plan_smem[];   // [T <= kPlanLens] lengths, then [warps][words] sets
   __shared__ int64_t scan_tmp[32];
   __shared__ uint32_t flags_s[kPlanCtas], bad_s;
+  __shared__ int pieces_s[kPieces];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = threadIdx.x;
   const uint32_t rank = cluster_ctarank();
   const bool near = a.T <= kPlanLens;
   // (the first CTA has to run before its shared memory is written)
   if (tid == 0) bad_s = 0u;
+  if (tid < kPieces) pieces_s[tid] = 0;
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   griddep_wait();                          // the inputs and the workspace may be the work before's
   griddep_launch_dependents();
@@ -270,6 +275,41 @@ __global__ void __launch_bounds__(kSchedThreads, 1) sparse_plan_kernel(SparsePla
       }
     }
     return;
+  }
+  if (S <= workers && q > 1 && chunk == 1) {
+    // Pieces of one block each, of up to p tiles: the smallest p of a few for which there are no more pieces
+    // than workers, if it is not much above q. (lo > 1, as X was dropped or q > 2 X. Quotients by an inverse
+    // that one lane computes for each p, exact for tiles x p < 2^32.)
+    const int lo = (int)((W + workers - 1) / workers), step = 1 + lo / 16;
+    const uint32_t inverse = 0xFFFFFFFFu / (uint32_t)(lo + (lane & (kPieces - 1)) * step) + 1u;
+    const int len = t0 < t1 ? len_of(t0) : 0, n = t0 < t1 ? tiles_of<kFew>(len) : 0;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const uint32_t ns = __umulhi((uint32_t)(n + lo + i * step - 1), __shfl_sync(0xffffffffu, inverse, i));
+      const int sum = __reduce_add_sync(0xffffffffu, (int)ns);
+      if (lane == 0) atomicAdd(pieces_s + i, sum);
+    }
+    named_bar_sync(1, threads);
+    const int count = pieces_s[lane & (kPieces - 1)] * G;
+    const int best = __ffs(__ballot_sync(0xffffffffu, count <= s.workers)) - 1, p = lo + best * step;
+    if (best >= 0 && p <= (int)q + s.setup / 2) {
+      const int ns = (int)__umulhi((uint32_t)(n + p - 1), __shfl_sync(0xffffffffu, inverse, best));
+      // units << 32 | cut blocks << 16 | partial slots
+      int64_t all3;
+      const int64_t mine3 = G * (((int64_t)ns << 32) + (ns >= 2 ? (1 << 16) + (int64_t)ns : 0));
+      const int64_t before3 = warps_exclusive_scan(mine3, scan_tmp, &all3, scanning);
+      const int n_units = (int)(all3 >> 32);
+      int unit = (int)(before3 >> 32), split = (int)(before3 >> 16) & 0xFFFF, slot = (int)before3 & 0xFFFF;
+      for (int c = tid; c <= s.workers; c += threads) s.cta_first[c] = min(c, n_units);
+      put_header((Pos)n_units, (uint32_t)(all3 >> 16) & 0xFFFFu);
+      for (int g = 0; g < G && n > 0; ++g) {
+        const int r0 = g * kChunkRows;
+        if (ns >= 2) s.split_list[split++] = make_int4(t0 * s.H + r0, min(kChunkRows, s.H - r0), ns, slot);
+#pragma unroll 1
+        for (int tb = 0; tb < n; tb += p, ++unit) put_unit((Pos)unit, t0, g, len, tb, min(n, tb + p), ns >= 2 ? slot++ : -1);
+      }
+      return;
+    }
   }
   Pos pos = pos0;
   int64_t mine3 = 0;                       // units << 32 | cut blocks << 16 | partial slots (as the chunk scheduler)

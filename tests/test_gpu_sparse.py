@@ -104,6 +104,19 @@ def test_many_tokens_and_sequences():
     c.check(list(range(0, 700, 23)))
 
 
+@pytest.mark.parametrize("kv,H", [(F8, 16), (BF, 16), (F8, 130)])
+@pytest.mark.parametrize("n", [20, 38, 64, 76, 101, 152, 153])
+def test_decode_batches_of_uneven_lengths(n, kv, H):
+    """One token each: as many pieces as workers or fewer, around the sizes at which the shares change, with
+    sequences without keys, short ones and one far longer than the rest."""
+    rng = np.random.default_rng(n)
+    lens = [(1, int(x)) for x in rng.integers(1, 2600, n)]
+    lens[3], lens[n // 2], lens[n - 1], lens[7] = (1, 9000), (1, 1), (1, 64), (0, 40)
+    c = SparseCase(lens, H, 64, 64, 150, kv, seed=n)
+    c.run()
+    c.check()
+
+
 @pytest.mark.parametrize("kv,H", [(BF, 130), (F8, 130), (F8, 16)])
 def test_whole_blocks_of_many_tokens(kv, H):
     """Shares of six row blocks or more are not cut; lists of all lengths, rows that see nothing among them."""
