@@ -774,10 +774,10 @@ bool prepare_once(int dev, uint32_t bit, Prepare&& prepare) {
 }
 int blocks_of(int len, int block) { return (len + block - 1) / block; }
 // rows of 128 bytes; planes > 0: as many planes of them
-bool encode_index_map(CUtensorMap* m, const void* base, int64_t rows, uint32_t box_rows, int64_t planes) {
+bool encode_index_map(CUtensorMap* m, const void* base, int64_t rows, uint32_t box_rows, int64_t planes, uint32_t box_planes) {
   const cuuint64_t dims[3] = {(cuuint64_t)kDIndex, (cuuint64_t)rows, (cuuint64_t)planes};
   const cuuint64_t strides[2] = {(cuuint64_t)kDIndex, (cuuint64_t)kDIndex * (cuuint64_t)rows};
-  const cuuint32_t box[3] = {(cuuint32_t)kDIndex, box_rows, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)kDIndex, box_rows, box_planes};
   return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, planes > 0 ? 3 : 2, base, dims, strides, box);
 }
 
@@ -807,8 +807,10 @@ MLA_EXPORT mla_status mla_index_scores(const mla_index_params* p, const void* q_
   const int64_t rows = (int64_t)p->num_pages * p->page_size;
   a.box_rows = box_rows_of(p->page_size, 128);
   a.total_rows = (int32_t)rows;
-  if (!encode_index_map(&a.tm_q, q_index, p->num_heads, 16, p->num_tokens) ||
-      !encode_index_map(&a.tm_k, index_cache, rows, (uint32_t)a.box_rows, 0))
+  int columns, tokens;
+  index_scores_group(p->num_tokens, p->batch, p->num_heads, &columns, &tokens);
+  if (!encode_index_map(&a.tm_q, q_index, p->num_heads, (uint32_t)columns, p->num_tokens, (uint32_t)tokens) ||
+      !encode_index_map(&a.tm_k, index_cache, rows, (uint32_t)a.box_rows, 0, 1))
     return MLA_ERR_INVALID_ARG;
   a.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   a.test_stall = g_test_stall.load(std::memory_order_relaxed);

@@ -27,7 +27,7 @@ struct IndexWriteArgs {
 cudaError_t launch_index_write(IndexWriteArgs a, cudaStream_t s);
 
 struct IndexScoreArgs {
-  CUtensorMap tm_q;                // [T][H][128] E4M3, boxes of 16 heads (zeros behind the last)
+  CUtensorMap tm_q;                // [T][H][128] E4M3, boxes of a group's tokens (zeros behind the last head)
   CUtensorMap tm_k;                // [num_pages * P rows][128] E4M3, boxes of box_rows rows
   const float* w;                  // [T, H]
   const float* scale;              // [num_pages * P]
@@ -42,10 +42,12 @@ struct IndexScoreArgs {
   int32_t q_rows, units, key_slots;   // rows of a query buffer, query buffers, tiles of keys in shared memory
   int32_t unit_blocks;             // blocks of a unit
   uint32_t block_inv, page_inv;    // 2^32 / block, 2^32 / P, rounded up
+  uint32_t by_blocks, by_heads;    // (2^32 - 1) / unit_blocks, / H, rounded down
   int32_t test_stall;
   uint64_t wait_limit_ns;
 };
 cudaError_t index_scores_prepare();   // per-device kernel attributes
+void index_scores_group(int T, int B, int H, int* columns, int* tokens);
 cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s);
 
 struct SelectArgs {

@@ -23,13 +23,14 @@
 // an accumulator each. The maxima of a unit's blocks gather in shared memory. Every wait is bounded; a stall
 // sets the error word, and the CTA drains and leaves.
 //
-// What bounds it. Many tokens: the sums. 32 columns of 128 keys take a scheduler's four warps 58 instructions
-// and 90 clocks each at best (a loop apart: 73 without max, 58 without the tensor-memory loads), the MMAs 64;
-// with maxima, waits and bookkeeping it is about 97 instructions and 142 clocks. 2048 tokens x 64 heads
-// over 24 K keys 406 us (2.1 PFLOP/s of E4M3; 34% of tensor cycles). On the way there: one issuing warp held
-// back everything (546 us for four warpgroups, its products of 128 columns take it 570 clocks), two of them
-// 490, products of 256 columns 457; a chunk more of double buffering or a quarter of max on the FMA pipe, 3%.
-// Few tokens: latency and the loading warp. 121 sequences x 4 K keys 17.7 us for 65 MB, of which 6 us pass
+// What bounds it. Many tokens: the sums. 32 columns of 128 keys take a scheduler's four warps 58 instructions and
+// 90 clocks each at best (a loop apart: 73 without max, 58 without the tensor-memory loads), the MMAs 64; with
+// maxima, waits and bookkeeping it is about 97 instructions and 142 clocks. 2048 tokens x 64 heads over 24 K keys
+// 400 us (2.1 PFLOP/s of E4M3; 34% of tensor cycles), with 16 heads 129 (219 while the warp that loads queries and
+// writes scores went through a unit's tokens one by one, a box for each). On the way there: one issuing warp held
+// back everything (546 us for four warpgroups, its products of 128 columns take it 570 clocks), two of them 490,
+// products of 256 columns 457; a chunk more of double buffering or a quarter of max on the FMA pipe, 3%.
+// Few tokens: latency and the loading warp. 121 sequences x 4 K keys 17.4 us for 65 MB, of which 6 us pass
 // before the first product and after the last; with one warp for units and keys 32, with keys' scales as bulk
 // copies 24 (each takes the warp about 95 clocks to issue, like a key box), tile by tile 21.5, with integer
 // divisions where a unit's pages are looked up 18.4.
@@ -166,11 +167,8 @@ __device__ __forceinline__ void add_heads(const float* v, const float* w, uint64
     }
   }
 }
-template <int CS>
-__device__ __forceinline__ void load_heads(uint32_t taddr, float* v) {
-  if (CS == 32) tmem_ld32(taddr, v);
-  else tmem_ld16(taddr, v);
-}
+// e / d of a small e, with by = (2^32 - 1) / d rounded down: (e + 1) by falls short of (e + 1) 2^32 / d by less than 2^32 / d
+__device__ __forceinline__ int quotient(int e, uint32_t by) { return (int)__umulhi((uint32_t)e + 1u, by); }
 
 // The rest of a wait that was not over at the first look, out of line.
 __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, uint32_t abort_s, uint32_t* err, uint64_t limit_ns) {
@@ -195,6 +193,7 @@ __device__ uint32_t g_unreported;                 // error bits of calls without
 template <int CS, int PT, bool kWhole>
 __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __grid_constant__ IndexScoreArgs a) {
   constexpr int Hp = CS * PT, kFull = kISColumns / Hp;   // columns of a token, tokens of an accumulator
+  constexpr int kAtOnce = 32 / CS;                  // tokens of a load from tensor memory
   extern __shared__ uint8_t dsmem_raw[];
   __shared__ __align__(8) uint64_t bar_kfull[kISMaxSlots], bar_kempty[kISMaxSlots], bar_info[kISMaxUnits],
       bar_qfull[kISMaxUnits], bar_qempty[kISMaxUnits], bar_tfull[kISIssuers], bar_tempty[kISIssuers], bar_drain[kISIssuers], bar_never;
@@ -266,14 +265,16 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
       if (!used) return true;
       const UnitInfo& I = info_s[buffer];
       int* from = best + buffer * maxima;
-      for (int i = 0; i < I.ntok; ++i) {
-        float* to = a.out + (int64_t)(I.t0 + i) * a.C + I.c0;
-        for (int c = lane; c < a.unit_blocks; c += 32) {
-          if (c < I.blocks) to[c] = from_ordered(from[i * a.unit_blocks + c]);
-          from[i * a.unit_blocks + c] = kLowest;
-        }
-        for (int c = lane; c < I.rest; c += 32) to[I.blocks + c] = -INFINITY;
+      float* to = a.out + (int64_t)I.t0 * a.C + I.c0;
+      const int n = I.ntok * a.unit_blocks, blocks = I.blocks, rest = I.rest;
+#pragma unroll 1                                        // (shorter code beats more loads at once, 403 us against 400)
+      for (int e = lane; e < n; e += 32) {              // of all tokens at once
+        const int i = quotient(e, a.by_blocks), c = e - i * a.unit_blocks;
+        if (c < blocks) to[(int64_t)i * a.C + c] = from_ordered(from[e]);
+        from[e] = kLowest;
       }
+      for (int i = 0; rest > 0 && i < I.ntok; ++i)
+        for (int c = lane; c < rest; c += 32) to[(int64_t)i * a.C + blocks + c] = -INFINITY;
       __syncwarp();
       return true;
     };
@@ -358,19 +359,23 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
           if (lane < un) I.seen[lane] = keys_seen(ut0 + lane, ustart, uend, uL, a.causal);
           // weights: one copy where a token's fill its columns, else by loads
           const uint32_t wbytes = a.H == Hp && wide_weights ? (uint32_t)(un * Hp) * 4 : 0u;
-          if (wbytes == 0)
-            for (int i = lane; i < un * a.H; i += 32) gW[ub * q_rows + (i / a.H) * Hp + i % a.H] = a.w[(int64_t)ut0 * a.H + i];
-          __syncwarp();
-          const int qboxes = un * (Hp / 16);
-          if (el) {
-            mbar_arrive(b_info + 8 * ub);
-            mbar_arrive_expect_tx(b_qfull + 8 * ub, (uint32_t)qboxes * 16 * kDIndex + wbytes);
-            if (wbytes) bulk_load(smem_u32(gW + ub * q_rows), a.w + (int64_t)ut0 * a.H, wbytes, b_qfull + 8 * ub);
+          if (wbytes == 0) {
+            const float* from = a.w + (int64_t)ut0 * a.H;
+#pragma unroll 1
+            for (int e = lane; e < un * a.H; e += 32) {
+              const int i = quotient(e, a.by_heads);
+              gW[ub * q_rows + i * Hp + e - i * a.H] = from[e];
+            }
           }
           __syncwarp();
-          for (int i = lane; i < qboxes; i += 32)
-            tma_load_3d(sQ + ub * q_rows * kDIndex + i * 16 * kDIndex, &a.tm_q, b_qfull + 8 * ub, 0,
-                        (i % (Hp / 16)) * 16, ut0 + i / (Hp / 16));
+          if (el) {
+            mbar_arrive(b_info + 8 * ub);
+            // (a group with fewer tokens loads what lies behind them, which no product reads)
+            mbar_arrive_expect_tx(b_qfull + 8 * ub, (uint32_t)(q_rows * kDIndex) + wbytes);
+            if (wbytes) bulk_load(smem_u32(gW + ub * q_rows), a.w + (int64_t)ut0 * a.H, wbytes, b_qfull + 8 * ub);
+            tma_load_3d(sQ + ub * q_rows * kDIndex, &a.tm_q, b_qfull + 8 * ub, 0, 0, ut0);
+          }
+          __syncwarp();
           ++nu;
           if (++ub == (uint32_t)units) { ub = 0; uph ^= 1; }
         }
@@ -609,17 +614,7 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
         float keep = -INFINITY;
         uint64_t s[4];
         // (the warps of a scheduler cover each other's loads: a second buffer changes nothing)
-        auto token = [&](int i, auto masked) {
-          float v[CS];
-#pragma unroll
-          for (int c = 0; c < PT; ++c) {
-            const int at = (i * PT + c) * CS;
-            load_heads<CS>(acc + at, v);
-            tmem_wait_ld();
-            if (c + 1 == PT && i + 1 == toks) release();
-            if (c == 0) add_heads<CS, true>(v, w + at, s);
-            else add_heads<CS, false>(v, w + at, s);
-          }
+        auto finish = [&](int i, auto masked) {         // token i's score of this key, and its maximum over keys
           float x = sum8(s) * ks;
           if (decltype(masked)::value && key >= I.seen[t0 + i]) x = -INFINITY;
           if (kWhole) {
@@ -631,12 +626,29 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
             if ((lane & 7) == 0 && x > -INFINITY) atomicMax(to + i * a.unit_blocks, ordered(x));
           }
         };
+        auto tokens = [&](int i, auto masked) {         // kAtOnce of them
+          float v[32];
+#pragma unroll
+          for (int c = 0; c < PT; ++c) {
+            const int at = (i * PT + c) * CS;
+            tmem_ld32(acc + at, v);
+            tmem_wait_ld();
+            if (c + 1 == PT && i + kAtOnce >= toks) release();
+            if (c == 0) add_heads<CS, true>(v, w + at, s);
+            else add_heads<CS, false>(v, w + at, s);
+          }
+          finish(i, masked);
+          if (kAtOnce == 2 && (!decltype(masked)::value || i + 1 < toks)) {
+            add_heads<CS, true>(v + 32 - CS, w + (i + 1) * CS, s);
+            finish(i + 1, masked);
+          }
+        };
         // a full accumulator whose tokens see all keys of the tile, the usual case, has code of its own
         if (toks == kFull && I.k0 + (tile + 1) * kISKeys <= I.seen[t0]) {
 #pragma unroll
-          for (int i = 0; i < kFull; ++i) token(i, std::false_type{});
+          for (int i = 0; i < kFull; i += kAtOnce) tokens(i, std::false_type{});
         } else {
-          for (int i = 0; i < toks; ++i) token(i, std::true_type{});
+          for (int i = 0; i < toks; i += kAtOnce) tokens(i, std::true_type{});
         }
         if (kWhole && lane < toks && keep > -INFINITY) atomicMax(to + lane * a.unit_blocks, ordered(keep));
       }
@@ -663,15 +675,22 @@ cudaError_t index_scores_prepare() {
   return cudaSuccess;
 }
 
+// Columns of a token, and tokens of a group: as many as sequences have on average (a power of two), up to four
+// sub-groups.
+void index_scores_group(int T, int B, int H, int* columns, int* tokens) {
+  *columns = 16;
+  while (*columns < H) *columns *= 2;
+  const int most_tokens = 2 * kISIssuers * (kISColumns / *columns);
+  *tokens = 1;
+  while (*tokens < T / B && *tokens < most_tokens) *tokens *= 2;
+}
+
 cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s) {
-  int Hp = 16;
-  while (Hp < a.H) Hp *= 2;
+  int Hp;
+  index_scores_group(a.T, a.B, a.H, &Hp, &a.TG);
   const int sub_tokens = kISColumns / Hp;
-  // tokens to a group: as many as sequences have on average (a power of two), up to four sub-groups
-  const int most_tokens = 2 * kISIssuers * sub_tokens;
   a.tg_log2 = 0;
-  while ((1 << a.tg_log2) < a.T / a.B && (1 << a.tg_log2) < most_tokens) ++a.tg_log2;
-  a.TG = 1 << a.tg_log2;
+  while (1 << a.tg_log2 < a.TG) ++a.tg_log2;
   const bool many = a.TG > sub_tokens;
   a.q_rows = a.TG * Hp;
   // a unit: whole blocks and whole tiles, 512 to 8192 keys, about 24 units to a CTA (6 of a decode step)
@@ -687,6 +706,8 @@ cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s) {
   if (m < 1) m = 1;
   a.unit_blocks = (int)(m * (lcm / a.block));
   a.block_inv = (uint32_t)((((uint64_t)1 << 32) + a.block - 1) / a.block);   // keys of a unit x block < 2^32
+  a.by_blocks = 0xFFFFFFFFu / (uint32_t)a.unit_blocks;
+  a.by_heads = 0xFFFFFFFFu / (uint32_t)a.H;
   a.page_inv = (uint32_t)((((uint64_t)1 << 32) + a.P - 1) / a.P);            // a key of a sequence x P < 2^32
   a.units = a.q_rows <= 256 ? kISMaxUnits : 2;
   const int fixed = is_fixed_bytes(a.units, a.q_rows, a.TG * a.unit_blocks);
