@@ -40,7 +40,9 @@ struct IndexScoreArgs {
   int32_t box_rows, total_rows;
   int32_t TG, tg_log2;             // tokens of a group, a power of two
   int32_t q_rows, units, key_slots;   // rows of a query buffer, query buffers, tiles of keys in shared memory
-  int32_t unit_blocks;             // blocks of a unit
+  int32_t unit_blocks, usual_blocks;  // blocks of a unit: at most; unless the kernel chooses
+  int32_t choose, step_blocks, step_tiles;   // least whole blocks of whole tiles
+  float by_grid;                      // 1 / CTAs
   uint32_t block_inv, page_inv;    // 2^32 / block, 2^32 / P, rounded up
   uint32_t by_blocks, by_heads;    // (2^32 - 1) / unit_blocks, / H, rounded down
   int32_t test_stall;

@@ -10,7 +10,7 @@
 // same for all lanes, and only the maximum over a block's keys crosses lanes. A token takes 16, 32, 64 or
 // 128 columns; those without a head have queries and weights of zero.
 //
-// Work is cut into units of one group of up to TG neighbouring tokens x `unit_blocks` blocks, as far as the
+// Work is cut into units of one group of up to TG neighbouring tokens x some `unit_blocks` blocks, as far as the
 // context goes; persistent CTAs, one per SM, take them in turn. Units are numbered by sequence and, within
 // one, all groups of a stretch of the context before the next, so that groups of a sequence find its keys
 // in L2. Each CTA counts them itself, 512 sequences at a time, and a lane finds its unit's sequence by
@@ -30,7 +30,7 @@
 // writes scores went through a unit's tokens one by one, a box for each). On the way there: one issuing warp held
 // back everything (546 us for four warpgroups, its products of 128 columns take it 570 clocks), two of them 490,
 // products of 256 columns 457; a chunk more of double buffering or a quarter of max on the FMA pipe, 3%.
-// Few tokens: latency and the loading warp. 121 sequences x 4 K keys 17.4 us for 65 MB, of which 6 us pass
+// Few tokens: latency and the loading warp. 121 sequences x 4 K keys 17.7 us for 65 MB, of which 6 us pass
 // before the first product and after the last; with one warp for units and keys 32, with keys' scales as bulk
 // copies 24 (each takes the warp about 95 clocks to issue, like a key box), tile by tile 21.5, with integer
 // divisions where a unit's pages are looked up 18.4.
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
     const bool el = elect_one();
     uint32_t ub = 0, uph = 1, nu = 0;                   // the unit's buffer and the parity of its barriers, units so far
     bool ok = true;
-    const int unit_keys = a.unit_blocks * a.block;
+    int unit_blocks = a.usual_blocks, unit_keys = unit_blocks * a.block;
     const bool wide_weights = (reinterpret_cast<uintptr_t>(a.w) & 15) == 0;
     // waits until a buffer's last unit is done, and writes its scores
     auto finish_unit = [&](uint32_t buffer, uint32_t parity, bool used) -> bool {
@@ -286,6 +286,25 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
       for (int i = lane; i < nb; i += 32) len_s[i] = max(0, min(a.seq_lens[b0 + i], a.max_len));
       __syncwarp();
       uint32_t units_before = 0;
+      if (a.choose) {
+        // Few units: of a size that makes few rounds of short ones. A unit costs about as much as its tiles
+        // and 1.5 more; lane l looks at l + 1 steps.
+        uint32_t tiles = 0, groups = 0;
+        for (int i = lane; i < nb; i += 32) {
+          const uint32_t g = (uint32_t)(max(0, cu_s[i + 1] - cu_s[i]) + TG - 1) >> a.tg_log2;
+          tiles += g * (uint32_t)((len_s[i] + kISKeys - 1) / kISKeys);
+          groups += g;
+        }
+        tiles = __reduce_add_sync(0xffffffffu, tiles);
+        groups = __reduce_add_sync(0xffffffffu, groups);
+        const float m = (float)((lane + 1) * a.step_tiles);
+        const float units = __fdividef((float)tiles + 0.5f * (float)groups * (m - 1.f), m);
+        const float cost = fminf(ceilf(units * a.by_grid) * (m + 1.5f) * 64.f, 1e8f);
+        const bool fits = (lane + 1) * a.step_blocks <= a.unit_blocks;
+        const uint32_t best = __reduce_min_sync(0xffffffffu, fits ? (uint32_t)cost << 5 | (uint32_t)lane : 0xFFFFFFFFu);
+        unit_blocks = (int)((best & 31) + 1) * a.step_blocks;
+        unit_keys = unit_blocks * a.block;
+      }
       bool bad = false;
       for (int i0 = 0; i0 < nb; i0 += 32) {
         uint32_t mine = 0;
@@ -333,10 +352,10 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
           const int un = __shfl_sync(0xffffffffu, ntok, src), uchunk = __shfl_sync(0xffffffffu, chunk, src);
           const int ustart = __shfl_sync(0xffffffffu, start, src), uend = __shfl_sync(0xffffffffu, end, src);
           const int uL = __shfl_sync(0xffffffffu, L, src);
-          const int c0 = uchunk * a.unit_blocks, uk0 = uchunk * unit_keys;
+          const int c0 = uchunk * unit_blocks, uk0 = uchunk * unit_keys;
           const int ulast = min(keys_seen(ut0 + un - 1, ustart, uend, uL, a.causal), uk0 + unit_keys);
           // the blocks behind the sequence's last unit hold no key
-          const int blocks = min(a.unit_blocks, a.C - c0), rest = uk0 + unit_keys >= uL ? a.C - c0 - blocks : 0;
+          const int blocks = min(unit_blocks, a.C - c0), rest = uk0 + unit_keys >= uL ? a.C - c0 - blocks : 0;
           if (ulast <= uk0) {                             // no token sees these blocks
             for (int i = 0; i < un; ++i)
               for (int c = lane; c < blocks + rest; c += 32) a.out[(int64_t)(ut0 + i) * a.C + c0 + c] = -INFINITY;
@@ -704,7 +723,16 @@ cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s) {
   const int64_t most = kISBest / ((int64_t)a.TG * (lcm / a.block));
   m = m > most ? most : m;
   if (m < 1) m = 1;
-  a.unit_blocks = (int)(m * (lcm / a.block));
+  // Where the contexts may come to no more than 32 tiles a CTA, the kernel takes the size that suits their actual
+  // lengths, up to 1024 keys: 4 tokens of 4 sequences of 33-131 K 18.9 us instead of 22.5, 1 to 4 sequences of 4 K
+  // 6.2 instead of 7.2; 0.5 us on the GPU, which a step of 121 sequences would not get back
+  a.choose = a.B <= kISSeqs && groups * a.max_len <= (int64_t)32 * kISKeys * num_sms ? 1 : 0;
+  int64_t cap = a.choose ? (1024 / lcm < most ? 1024 / lcm : most) : m;
+  cap = cap < m ? m : cap;
+  a.step_blocks = lcm / a.block;
+  a.step_tiles = lcm / kISKeys;
+  a.usual_blocks = (int)m * a.step_blocks;
+  a.unit_blocks = (int)cap * a.step_blocks;
   a.block_inv = (uint32_t)((((uint64_t)1 << 32) + a.block - 1) / a.block);   // keys of a unit x block < 2^32
   a.by_blocks = 0xFFFFFFFFu / (uint32_t)a.unit_blocks;
   a.by_heads = 0xFFFFFFFFu / (uint32_t)a.H;
@@ -714,9 +742,10 @@ cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s) {
   a.key_slots = (kISSmem - fixed) / kISSlotBytes;
   if (a.key_slots > kISMaxSlots) a.key_slots = kISMaxSlots;
   const int smem = fixed + a.key_slots * kISSlotBytes;
-  const int64_t total = ((int64_t)a.T / a.TG + a.B) * ((a.C + a.unit_blocks - 1) / a.unit_blocks);   // units at most
+  const int64_t total = ((int64_t)a.T / a.TG + a.B) * ((a.C + a.step_blocks - 1) / a.step_blocks);   // units at most
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(total < num_sms ? total : num_sms));
+  a.by_grid = 1.f / (float)cfg.gridDim.x;
   cfg.blockDim = dim3(kISThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
