@@ -181,6 +181,14 @@ def test_scores_of_many_sequences_with_idle_ones_and_long_contexts():
     c.check(list(range(0, 1100, 41)) + [1100])
 
 
+@pytest.mark.parametrize("P,block", [(64, 8), (24, 24), (40, 40), (1000, 1000), (1024, 512)])
+def test_scores_of_long_and_short_contexts_together(P, block):
+    """Few sequences, whose units are sized by their lengths."""
+    c = ScoreCase([(4, 33001), (0, 700), (2, 70001), (1, 5), (3, 1)], 3, P, block, seed=P, pad=1)
+    c.run()
+    c.check()
+
+
 def test_scores_of_short_contexts_under_a_long_limit():
     c = ScoreCase([(1, 40), (0, 9), (2, 300), (1, 1)], 64, 16, 8, seed=7, max_seq_len=1 << 20)
     c.run()
