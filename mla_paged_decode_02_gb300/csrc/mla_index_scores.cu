@@ -170,6 +170,10 @@ __device__ __forceinline__ void add_heads(const float* v, const float* w, uint64
 // e / d of a small e, with by = (2^32 - 1) / d rounded down: (e + 1) by falls short of (e + 1) 2^32 / d by less than 2^32 / d
 __device__ __forceinline__ int quotient(int e, uint32_t by) { return (int)__umulhi((uint32_t)e + 1u, by); }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" :: "l"(reinterpret_cast<uint64_t>(p)));
+}
+
 // The rest of a wait that was not over at the first look, out of line.
 __device__ __noinline__ bool wait_longer(uint32_t bar, uint32_t parity, uint32_t abort_s, uint32_t* err, uint64_t limit_ns) {
   volatile uint32_t* flag = reinterpret_cast<volatile uint32_t*>(__cvta_shared_to_generic(abort_s));
@@ -345,6 +349,8 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
           chunk = (int)(in / groups);
           t0 = start + ((int)(in - (uint32_t)chunk * groups) << a.tg_log2);
           ntok = min(TG, end - t0);
+          // the pages that the loading warp will ask for are on their way to L2
+          prefetch_l2(a.block_table + (int64_t)(b0 + b) * a.MB + __umulhi((uint32_t)(chunk * unit_keys), a.page_inv));
         }
         const int taken = __popc(__ballot_sync(0xffffffffu, u < end_units));
         for (int src = 0; src < taken && ok; ++src) {
