@@ -242,7 +242,12 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
   }
   if (warp == 1) tmem_alloc(smem_u32(&tmem_base_s), kISTmem);
   for (int i = threadIdx.x; i < units * maxima; i += kISThreads) best[i] = kLowest;
-  for (int i = threadIdx.x; i < units * q_rows; i += kISThreads) gW[i] = 0.f;   // columns without a head keep it
+  // Where heads fill a token's columns, a unit's weights come by one bulk copy. Else by loads and ordinary stores,
+  // and columns without a head keep the zeros written here (with bulk copies there are none: nothing would order these
+  // stores, of the generic proxy, before the copy's, of the async proxy).
+  const bool bulk_weights = a.H == Hp && (reinterpret_cast<uintptr_t>(a.w) & 15) == 0;
+  if (!bulk_weights)
+    for (int i = threadIdx.x; i < units * q_rows; i += kISThreads) gW[i] = 0.f;
   griddep_wait();
   griddep_launch_dependents();
   tc_fence_before();
@@ -262,7 +267,6 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
     uint32_t ub = 0, uph = 1, nu = 0;                   // the unit's buffer and the parity of its barriers, units so far
     bool ok = true;
     int unit_blocks = a.usual_blocks, unit_keys = unit_blocks * a.block;
-    const bool wide_weights = (reinterpret_cast<uintptr_t>(a.w) & 15) == 0;
     // waits until a buffer's last unit is done, and writes its scores
     auto finish_unit = [&](uint32_t buffer, uint32_t parity, bool used) -> bool {
       if (!wait(b_qempty + 8 * buffer, parity)) return false;
@@ -382,8 +386,7 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
             I.seq = us;
           }
           if (lane < un) I.seen[lane] = keys_seen(ut0 + lane, ustart, uend, uL, a.causal);
-          // weights: one copy where a token's fill its columns, else by loads
-          const uint32_t wbytes = a.H == Hp && wide_weights ? (uint32_t)(un * Hp) * 4 : 0u;
+          const uint32_t wbytes = bulk_weights ? (uint32_t)(un * Hp) * 4 : 0u;
           if (wbytes == 0) {
             const float* from = a.w + (int64_t)ut0 * a.H;
 #pragma unroll 1
