@@ -68,6 +68,16 @@ constexpr int kISSmem = 216 * 1024;               // dynamic
 constexpr int is_fixed_bytes(int units, int q_rows, int maxima) {
   return 1024 + kISScales * kISKeys * 4 + units * (q_rows * kDIndex + maxima * 4 + q_rows * 4);
 }
+constexpr int is_key_slots(int units, int q_rows, int maxima) {
+  return (kISSmem - is_fixed_bytes(units, q_rows, maxima)) / kISSlotBytes;
+}
+constexpr int kISMaxRows = 2 * kISIssuers * kISColumns;   // of a query buffer: four sub-groups
+constexpr int kISManyRows = kISMaxRows / 2;               // up to which there are kISMaxUnits buffers, else 2
+static_assert(is_key_slots(2, kISMaxRows, kISBest) >= 2 && is_key_slots(kISMaxUnits, kISManyRows, kISBest) >= 2,
+              "a product of one sub-group takes two tiles of keys at once");
+static_assert(kISMaxTokens * (kISKeys / 8) <= kISBest, "the smallest unit of a full group");
+static_assert(kISScales >= kISMaxSlots + 4, "scales are read until four tiles later");
+static_assert(kISTogether <= 32, "a lane for each tile");
 
 // an order-preserving code of a float, so that maxima can be taken as integers
 __device__ __forceinline__ int ordered(float x) {
@@ -746,9 +756,9 @@ cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s) {
   a.by_blocks = 0xFFFFFFFFu / (uint32_t)a.unit_blocks;
   a.by_heads = 0xFFFFFFFFu / (uint32_t)a.H;
   a.page_inv = (uint32_t)((((uint64_t)1 << 32) + a.P - 1) / a.P);            // a key of a sequence x P < 2^32
-  a.units = a.q_rows <= 256 ? kISMaxUnits : 2;
+  a.units = a.q_rows <= kISManyRows ? kISMaxUnits : 2;
   const int fixed = is_fixed_bytes(a.units, a.q_rows, a.TG * a.unit_blocks);
-  a.key_slots = (kISSmem - fixed) / kISSlotBytes;
+  a.key_slots = is_key_slots(a.units, a.q_rows, a.TG * a.unit_blocks);
   if (a.key_slots > kISMaxSlots) a.key_slots = kISMaxSlots;
   const int smem = fixed + a.key_slots * kISSlotBytes;
   const int64_t total = ((int64_t)a.T / a.TG + a.B) * ((a.C + a.step_blocks - 1) / a.step_blocks);   // units at most
