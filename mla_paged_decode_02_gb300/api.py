@@ -527,6 +527,10 @@ def _ragged(seq_lens, cu_q_lens, block_table=None) -> int:
         table = block_table.shape
         if len(table) != 2 or table[0] != shape[0] or block_table.dtype is not i32 or not block_table.is_contiguous():
             raise ValueError("block_table must be a contiguous int32 [B, MB] tensor")
+        if table[1] > _I32_MAX:
+            raise ValueError("the columns of block_table must fit 32 bits")
+    if shape[0] > _I32_MAX:
+        raise ValueError("the number of sequences must fit 32 bits")
     return shape[0]
 
 
@@ -651,6 +655,8 @@ def select_blocks(scores: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens: torch
     if len(shape) != 2 or scores.dtype is not torch.float32:
         raise ValueError("scores must be a float32 [T, blocks] tensor with contiguous rows")
     T, C = shape
+    if T > _I32_MAX or C > _I32_MAX:
+        raise ValueError("the rows and columns of scores must fit 32 bits")
     stride, inner = scores.stride()
     if inner != 1 and T > 0 and C > 1:
         raise ValueError("scores must be a float32 [T, blocks] tensor with contiguous rows")
@@ -680,12 +686,12 @@ def select_blocks(scores: torch.Tensor, seq_lens: torch.Tensor, cu_q_lens: torch
 
 def make_sparse_params(batch, num_tokens, num_heads, page_size, num_pages, max_blocks_per_seq, max_seq_len, block_size,
                        top_k, kv_dtype, causal=True) -> SparseParams:
-    for name, value in (("max_seq_len", max_seq_len), ("block_size", block_size), ("top_k", top_k)):
-        if value > _I32_MAX:
+    fields = [int(v) for v in (batch, num_tokens, num_heads, page_size, num_pages, max_blocks_per_seq, max_seq_len,
+                               block_size, top_k, kv_dtype, bool(causal))]
+    for (name, _), value in zip(SparseParams._fields_, fields):
+        if not -_I32_MAX <= value <= _I32_MAX:
             raise ValueError(f"{name} must fit 32 bits")
-    return SparseParams(int(batch), int(num_tokens), int(num_heads), int(page_size), int(num_pages),
-                        int(max_blocks_per_seq), int(max_seq_len), int(block_size), int(top_k), int(kv_dtype),
-                        int(bool(causal)))
+    return SparseParams(*fields)
 
 
 def sparse_workspace_size(params: SparseParams, num_sms: int = 0) -> int:
@@ -720,6 +726,8 @@ def sparse_attention(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch
     shape = selected.shape
     if len(shape) != 2 or shape[0] != T or selected.dtype is not torch.int32 or not selected.is_contiguous():
         raise ValueError("selected must be a contiguous int32 [T, K] tensor")
+    if shape[1] > _I32_MAX:
+        raise ValueError("the columns of selected must fit 32 bits")
     kvd = _kv_dtype_of(kv_cache)
     if kvd == KV_FP8_E4M3 and (kv_scale is None or kv_scale.dtype != torch.float32 or kv_scale.numel() < 1):
         raise ValueError("the FP8 cache needs kv_scale as a float32 device tensor")
@@ -730,8 +738,8 @@ def sparse_attention(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch
     if workspace is not None and not workspace.is_contiguous():     # its size is taken from its elements
         raise ValueError("workspace must be contiguous")
     scale = kv_scale if kvd == KV_FP8_E4M3 else None
-    if max_seq_len > _I32_MAX or block_size > _I32_MAX:
-        raise ValueError("max_seq_len and block_size must fit 32 bits")
+    if not 0 < max_seq_len <= _I32_MAX or not 0 < block_size <= _I32_MAX:
+        raise ValueError("max_seq_len and block_size must be positive and fit 32 bits")
     params = SparseParams(B, T, H, P, Np, block_table.shape[1], max_seq_len, block_size, shape[1], kvd, 1 if causal else 0)
     handle, at = _addresses(stream, q, kv_cache, block_table, seq_lens, cu_q_lens, selected, scale, out, lse, workspace)
     if out is None:

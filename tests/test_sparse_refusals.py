@@ -179,3 +179,36 @@ def test_index_tensors():
             write(**bad)
     with pytest.raises(ValueError, match="on the GPU"):
         write()
+
+
+@pytest.mark.parametrize("far", [(1 << 31) + 1, (1 << 32) + 1])
+def test_sizes_whose_32_bit_fields_would_keep_their_low_bits(far):
+    """Tensors of these shapes fit a GPU; the calls must not take them for ones of a few rows or columns."""
+    def empty(*shape, dtype=torch.int32):
+        return torch.empty(shape, dtype=dtype, device="meta")
+    t = tensors()
+    q, w = torch.zeros(4, 2, 128, dtype=torch.uint8), torch.zeros(4, 2)
+    cache, scale = torch.zeros(3, 64, 128, dtype=torch.uint8), torch.zeros(3, 64)
+
+    def scores(table=t["table"], lens=t["lens"], cu=t["cu"]):
+        api.index_scores(q, w, cache, scale, table, lens, cu, max_seq_len=64, block_size=64)
+
+    def select(s, lens=t["lens"], cu=t["cu"]):
+        api.select_blocks(s, lens, cu, 3, block_size=64)
+
+    def sparse(table=t["table"], lens=t["lens"], cu=t["cu"], sel=t["sel"], max_seq_len=64, block_size=64):
+        api.sparse_attention(t["q"], t["cache"], table, lens, cu, sel, 0.1, max_seq_len=max_seq_len, block_size=block_size)
+    ragged = dict(lens=empty(far), cu=empty(far + 1))
+    for call in (lambda: scores(table=empty(2, far)), lambda: scores(table=empty(far, 1), **ragged),
+                 lambda: select(empty(4, far, dtype=torch.float32)), lambda: select(empty(far, 4, dtype=torch.float32)),
+                 lambda: select(torch.zeros(4, 9), **ragged), lambda: sparse(table=empty(2, far)),
+                 lambda: sparse(table=empty(far, 1), **ragged), lambda: sparse(sel=empty(4, far)),
+                 lambda: sparse(max_seq_len=far), lambda: sparse(block_size=far), lambda: sparse(max_seq_len=64 - (1 << 32)),
+                 lambda: sparse(block_size=64 - (1 << 32))):
+        with pytest.raises(ValueError, match="fit 32 bits"):
+            call()
+    good = [3, 40, 16, 64, 30, 8, 500, 64, 4, api.KV_BF16]
+    for i in range(9):
+        for value in (far, -far):
+            with pytest.raises(ValueError, match="fit 32 bits"):
+                api.make_sparse_params(*good[:i], value, *good[i + 1:])
