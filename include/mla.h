@@ -333,7 +333,8 @@ typedef struct mla_index_params {
  * a token sees are as in mla_chunk_attention. With k_j the codes and s_j the scale of key j,
  *   score_j = s_j sum_h q_weights[t][h] max(0, q_index[t][h] . k_j)
  *   scores[t][c] = max of score_j over the keys j of block c that token t sees, c < C,
- * C = ceil(max_seq_len / block_size); -infinity for a block without such a key. A score that is NaN
+ * C = ceil(max_seq_len / block_size); -infinity for a block without such a key. Sums are float32, and
+ * finite where sum_h |q_weights[t][h]| max(0, ..) is below 2^127. A score that is NaN
  * counts as -infinity. Keys a token does not see may hold anything. Rows that belong to no sequence
  * are left as they are.
  *   q_index, index_cache, index_scale   as written by mla_index_cache_write, 16-byte aligned

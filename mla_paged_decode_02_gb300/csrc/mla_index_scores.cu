@@ -100,7 +100,8 @@ __device__ __forceinline__ void add_positive2(uint64_t& acc, float x, float y, u
                  "max.NaN.f32 b, %2, 0f00000000;\n\tmov.b64 p, {a, b};\n\tfma.rn.f32x2 %0, p, %3, %0;\n\t}"
                  : "+l"(acc) : "f"(x), "f"(y), "l"(w));
 }
-// The same with x + |x| = 2 max(0, x) in its place, on the FMA pipe instead of the ALU.
+// The same with x + |x| = 2 max(0, x) in its place, on the FMA pipe instead of the ALU: these sums are halved at the
+// end, so they overflow from 2^127 on. (Half of it as a further operand costs an instruction for each pair.)
 template <bool kFirst>
 __device__ __forceinline__ void add_positive2_twice(uint64_t& acc, float x, float y, uint64_t w) {
   if (kFirst)
