@@ -88,7 +88,9 @@ cudaError_t launch_sparse_plan(const SparsePlanArgs& a, cudaStream_t s);
 // Up to 16 rows with the FP8 cache and blocks of whole 64-row boxes go to the decode kernel (16 rows, keys
 // on M), everything else to the chunk attention's (128 rows on M). The kernels alone, 16 heads x 2041 keys,
 // E4M3: 15.6 us against 17.6 for 16 tokens, 28.6 against 35.8 for 64, 79 against 101 for 256. Calls: blocks of
-// 32 rows, 512 tokens, 192 against 183 us; 32 heads, 64 tokens, 49 against 46; bf16, 60 against 55.
+// 32 rows, 512 tokens, 192 against 183 us; 32 heads, 64 tokens, 49 against 46; bf16, 16 heads, 1 to 4 tokens
+// about equal, 16 tokens 25.4 against 28.3, 64 54 against 51, 152 77 against 87, 512 223 against 259: there the decode
+// kernel would gain a tenth from some 100 tokens on, which is not made use of.
 inline bool sparse_few_rows(int H, bool fp8, int block) { return fp8 && H <= 16 && block % 64 == 0; }
 
 struct SparseWs {

@@ -26,14 +26,14 @@
 // What bounds it. Many tokens: the sums. 32 columns of 128 keys take a scheduler's four warps 58 instructions and
 // 90 clocks each at best (a loop apart: 73 without max, 58 without the tensor-memory loads), the MMAs 64; with
 // maxima, waits and bookkeeping it is about 97 instructions and 142 clocks. 2048 tokens x 64 heads over 24 K keys
-// 400 us (2.1 PFLOP/s of E4M3; 34% of tensor cycles), with 16 heads 129 (219 while the warp that loads queries and
+// 400 us (2.1 PFLOP/s of E4M3; 44% of tensor cycles), with 16 heads 129 (219 while the warp that loads queries and
 // writes scores went through a unit's tokens one by one, a box for each). On the way there: one issuing warp held
 // back everything (546 us for four warpgroups, its products of 128 columns take it 570 clocks), two of them 490,
 // products of 256 columns 457; a chunk more of double buffering or a quarter of max on the FMA pipe, 3%.
-// Few tokens: latency and the loading warp. 121 sequences x 4 K keys 17.7 us for 65 MB, of which 6 us pass
-// before the first product and after the last; with one warp for units and keys 32, with keys' scales as bulk
-// copies 24 (each takes the warp about 95 clocks to issue, like a key box), tile by tile 21.5, with integer
-// divisions where a unit's pages are looked up 18.4.
+// Few tokens: latency and the loading warp. 121 sequences x 4 K keys 17.2 us for 65 MB (21.2 where they come from
+// DRAM), of which 6 us pass before the first product and after the last; with one warp for units and keys 32, with
+// keys' scales as bulk copies 24 (each takes the warp about 95 clocks to issue, like a key box), tile by tile 21.5,
+// with integer divisions where a unit's pages are looked up 18.4.
 #include <type_traits>
 #include "mla_index.h"
 #include "mla_ptx.cuh"
@@ -509,7 +509,8 @@ __global__ void __launch_bounds__(kISThreads, 1) index_scores_kernel(const __gri
           tile += some;
         }
       } else {
-        // few slots, as beside large queries: tile by tile (4 tokens x 64 heads 22.4 us; in the form above 23 to 24.7)
+        // few slots, as beside large queries: tile by tile (4 tokens of 4 long sequences x 64 heads, four slots, 19.9 us;
+        // in the form above, four at once, 23.3; 4 tokens of 64 sequences 18.6 and 22.8)
         for (int tile = 0; tile < tiles; ++tile) {
           const int at = tile * per & 31;                 // per divides 32
           if (tile > 0 && at == 0) {
@@ -715,7 +716,10 @@ cudaError_t index_scores_prepare() {
 }
 
 // Columns of a token, and tokens of a group: as many as sequences have on average (a power of two), up to four
-// sub-groups.
+// sub-groups. One size for all units keeps their queries in one box. Where sequences are alike that is the right one;
+// in a batch of both kinds, 64 heads, us, together / a call for each: 127 single tokens and a prompt of 2048 tokens
+// over 24 K keys 413 / 21 + 404, over none 48 / 21 + 29; 255 and a prompt of 512 over 8 K (groups of two, which fetch
+// the prompt's keys four times as often) 99 / 40 + 44, over 24 K 208 / 40 + 105.
 void index_scores_group(int T, int B, int H, int* columns, int* tokens) {
   *columns = 16;
   while (*columns < H) *columns *= 2;
@@ -732,7 +736,8 @@ cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s) {
   while (1 << a.tg_log2 < a.TG) ++a.tg_log2;
   const bool many = a.TG > sub_tokens;
   a.q_rows = a.TG * Hp;
-  // a unit: whole blocks and whole tiles, 512 to 8192 keys, about 24 units to a CTA (6 of a decode step)
+  // A unit: about 24 to a CTA (6 of a decode step), of 512 to 8192 keys (1024), as far as they are whole blocks and
+  // whole tiles (blocks of 1016 keys: 16256) and their maxima fit (256 keys for 32 tokens and blocks of 8).
   int lcm = a.block;
   while (lcm % kISKeys != 0) lcm += a.block;
   const int64_t groups = (a.T + a.TG - 1) / a.TG;
@@ -744,8 +749,9 @@ cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s) {
   m = m > most ? most : m;
   if (m < 1) m = 1;
   // Where the contexts may come to no more than 32 tiles a CTA, the kernel takes the size that suits their actual
-  // lengths, up to 1024 keys: 4 tokens of 4 sequences of 33-131 K 18.9 us instead of 22.5, 1 to 4 sequences of 4 K
-  // 6.2 instead of 7.2; 0.5 us on the GPU, which a step of 121 sequences would not get back
+  // lengths, from one step (128 keys where blocks divide a tile) up to 1024 keys: 4 tokens of 4 sequences of 33-131 K
+  // 18.9 us instead of 22.5, 1 to 4 sequences of 4 K 6.2 instead of 7.2; 0.5 us on the GPU, which a step of 121
+  // sequences would not get back
   a.choose = a.B <= kISSeqs && groups * a.max_len <= (int64_t)32 * kISKeys * num_sms ? 1 : 0;
   int64_t cap = a.choose ? (1024 / lcm < most ? 1024 / lcm : most) : m;
   cap = cap < m ? m : cap;
@@ -757,6 +763,8 @@ cudaError_t launch_index_scores(IndexScoreArgs a, int num_sms, cudaStream_t s) {
   a.by_blocks = 0xFFFFFFFFu / (uint32_t)a.unit_blocks;
   a.by_heads = 0xFFFFFFFFu / (uint32_t)a.H;
   a.page_inv = (uint32_t)((((uint64_t)1 << 32) + a.P - 1) / a.P);            // a key of a sequence x P < 2^32
+  // (queries of 256 rows: two buffers leave eight slots for keys instead of four, and 4 tokens of 4 long sequences x 64
+  // heads take 22.2 us instead of 19.9, of 64 sequences 21.4 instead of 18.6: short units want their queries early)
   a.units = a.q_rows <= kISManyRows ? kISMaxUnits : 2;
   const int fixed = is_fixed_bytes(a.units, a.q_rows, a.TG * a.unit_blocks);
   a.key_slots = is_key_slots(a.units, a.q_rows, a.TG * a.unit_blocks);
