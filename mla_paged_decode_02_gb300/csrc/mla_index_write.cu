@@ -9,7 +9,8 @@
 // that is not finite gets a NaN scale. (A division for each value instead of one for the row: 41 us against
 // 23 then, for 4096 tokens x 64 heads.)
 //
-// Memory bound at many tokens (4096 x 64 heads 21.7 us for 103 MB, 4.7 TB/s; 128 x 64 heads 2.1 us, latency).
+// Memory bound at many tokens (4096 x 64 heads 23.7 us for 103 MB, 4.3 TB/s, and 21.9 where inputs stay in L2; 128 x 64
+// heads 3.0 and 1.9 us, latency).
 // Bytes: 256 in and 132 out per row. Eight lanes share a row (eight values of the fixed half and eight of
 // the turned one each); a warp takes four tokens' keys, or 4 or 16 heads of a token.
 #include <cuda_fp8.h>

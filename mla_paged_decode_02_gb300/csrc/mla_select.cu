@@ -12,8 +12,8 @@
 //
 // Bound by latency: reading the row, then some 20 rounds of counting. Up to 1024 blocks a warp takes a
 // token, its codes in registers; beyond that a block of 1024 threads does, where a round takes a barrier.
-// 128 tokens x 96 blocks 3.6 us, 16 x 4096 6.4, 2048 x 512 8.2 (histograms of eight bits in shared memory, the
-// first form: 6.7, 16.0, 20.2).
+// 128 tokens x 96 blocks 3.1 us, 16 x 4096 6.8, 2048 x 512 8.7, each call on other inputs (histograms of eight bits in
+// shared memory, the first form, on the same inputs: 6.7, 16.0, 20.2, where this one took 3.6, 6.4, 8.2).
 #include "mla_index.h"
 #include "mla_ptx.cuh"
 #include "mla_ragged.cuh"
